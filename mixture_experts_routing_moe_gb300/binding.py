@@ -16,6 +16,7 @@ import torch
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmoe.so")
 HEADER = os.path.join(os.path.dirname(_HERE), "include", "moe.h")
+MX4_HEADER = os.path.join(os.path.dirname(_HERE), "include", "moe_mx4.h")
 
 MOE_F32, MOE_F16, MOE_BF16 = 0, 1, 2
 DTYPE_CODE = {torch.float32: MOE_F32, torch.float16: MOE_F16, torch.bfloat16: MOE_BF16}
@@ -61,6 +62,16 @@ _SIGS = {
                                     _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "moe_dispatch_backward": (_int, [_vp, _int, _vp, _i64, _i64, _int, _vp, _vp]),
     "moe_device_status": (_int, [_vp, _sz, _vp]),
+    "moe_mx4_code_bytes": (_sz, [_i64]),
+    "moe_mx4_scale_bytes": (_sz, [_i64]),
+    "moe_mx4_quantize": (_int, [_vp, _int, _i64, _i64, _i64, _vp, _vp, _vp]),
+    "moe_mx4_dequantize": (_int, [_vp, _vp, _i64, _i64, _vp, _int, _i64, _vp]),
+    "moe_mx4_product_workspace_bytes": (_sz, []),
+    "moe_mx4_product": (_int, [_vp, _vp, _i64, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _int, _vp,
+                               _sz, _vp]),
+    "moe_mx4_experts_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "moe_mx4_experts_forward_dispatched": (_int, [_vp, _int, _vp, _i64, _vp, _vp, _vp, _vp, _vp,
+                                                  _vp, _i64, _i64, _i64, _vp, _vp, _sz, _vp]),
 }
 
 _lib = None
@@ -88,9 +99,9 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
-def header_functions() -> list[str]:
-    """Names of the functions include/moe.h declares."""
-    src = open(HEADER).read()
+def header_functions(header: str = HEADER) -> list[str]:
+    """Names of the functions a header (include/moe.h) declares."""
+    src = open(header).read()
     src = re.sub(r"/\*.*?\*/", "", src, flags=re.S)
     return sorted(set(re.findall(r"\b(moe_[a-z_0-9]+)\s*\(", src)))
 
@@ -382,3 +393,140 @@ def moe_wait_selftest(ws, stream=None) -> None:
 def moe_device_status(ws, stream=None) -> int:
     """Synchronise, read and clear the workspace status word (0 = MOE_OK)."""
     return lib().moe_device_status(_ptr(ws), ws.numel(), _stream(stream))
+
+
+# ------------------------------------------------------------- microscaled 4-bit (moe_mx4.h)
+def _mx4_pitch(K: int):
+    """(bytes of codes, bytes of scales) of a row of K values."""
+    blocks = -(-K // 32)
+    return 16 * blocks, -(-blocks // 4) * 4
+
+
+def _mx4_rows(codes, scales, K: int, where: str):
+    """Checks one operand in blocks: [..., rows] rows of K values."""
+    _cuda(codes, scales)
+    if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
+        raise MoeError(3, f"{where}: codes and scales are uint8")
+    pc, ps = _mx4_pitch(K)
+    if codes.shape[-1] != pc or scales.shape != codes.shape[:-1] + (ps,):
+        raise MoeError(2, f"{where}: rows of {K} values have {pc} code bytes and {ps} scale bytes")
+
+
+def _mx4_ws(ws, need: int, device):
+    if ws is None:
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    _cuda(ws)
+    return ws
+
+
+def moe_mx4_quantize(x, codes=None, scales=None, stream=None):
+    """Rows of x [..., K] to blocks -> (codes uint8 [..., 16 ceil(K/32)], scales uint8
+    [..., 4 ceil(K/128)]).  x is contiguous, or two-dimensional with rows a stride apart."""
+    K = x.shape[-1]
+    if not x.is_cuda or not (x.is_contiguous() or (x.dim() == 2 and x.stride(1) == 1
+                                                   and x.stride(0) >= K)):
+        raise ValueError("moe_mx4_quantize takes CUDA rows of consecutive values")
+    dt = _code(x)
+    rows = x.numel() // K if K else 0
+    pc, ps = _mx4_pitch(K)
+    lead = x.shape[:-1]
+    if codes is None:
+        codes = torch.empty(lead + (pc,), dtype=torch.uint8, device=x.device)
+    if scales is None:
+        scales = torch.empty(lead + (ps,), dtype=torch.uint8, device=x.device)
+    _mx4_rows(codes, scales, K, "moe_mx4_quantize")
+    if codes.shape[:-1] != lead:
+        raise MoeError(2, "moe_mx4_quantize: codes have other rows than x")
+    ld = K if x.is_contiguous() else x.stride(0)
+    _check(lib().moe_mx4_quantize(x.data_ptr(), dt, rows, K, ld, codes.data_ptr(),
+                                  scales.data_ptr(), _stream(stream)), "moe_mx4_quantize")
+    return codes, scales
+
+
+def moe_mx4_dequantize(codes, scales, K: int, dtype=torch.bfloat16, out=None, stream=None):
+    """The values of rows of K values in blocks -> out [..., K] of dtype."""
+    _mx4_rows(codes, scales, K, "moe_mx4_dequantize")
+    if out is None:
+        out = torch.empty(codes.shape[:-1] + (K,), dtype=dtype, device=codes.device)
+    elif out.shape != codes.shape[:-1] + (K,):
+        raise MoeError(2, "moe_mx4_dequantize: out has another shape")
+    elif not out.is_cuda or not (out.is_contiguous() or (out.dim() == 2 and out.stride(1) == 1
+                                                         and out.stride(0) >= K)):
+        raise ValueError("moe_mx4_dequantize writes CUDA rows of consecutive values")
+    rows = out.numel() // K if K else 0
+    ld = K if out.is_contiguous() else out.stride(0)
+    _check(lib().moe_mx4_dequantize(codes.data_ptr(), scales.data_ptr(), rows, K, out.data_ptr(),
+                                    _code(out), ld, _stream(stream)), "moe_mx4_dequantize")
+    return out
+
+
+def moe_mx4_product(a_codes, a_scales, b_codes, b_scales, offsets=None, dtype=torch.bfloat16,
+                    out=None, ws=None, stream=None):
+    """A [rows] times B [E, N] (or [N]) by groups of rows -> out [rows, N] of dtype.  The rows of A
+    and B hold the same number of blocks; offsets int32 [E + 1] on the device, or None for one
+    group."""
+    K = 2 * a_codes.shape[-1]
+    _mx4_rows(a_codes, a_scales, K, "moe_mx4_product")
+    _mx4_rows(b_codes, b_scales, K, "moe_mx4_product")
+    if a_codes.dim() != 2 or b_codes.dim() not in (2, 3):
+        raise MoeError(2, "moe_mx4_product: A is [rows, bytes], B [N, bytes] or [E, N, bytes]")
+    rows, N = a_codes.shape[0], b_codes.shape[-2]
+    E = b_codes.shape[0] if b_codes.dim() == 3 else 1
+    if offsets is not None:
+        _offsets(offsets, E, "moe_mx4_product")
+    if out is None:
+        out = torch.empty(rows, N, dtype=dtype, device=a_codes.device)
+    elif out.shape != (rows, N):
+        raise MoeError(2, "moe_mx4_product: out has another shape")
+    _cuda(out)
+    ws = _mx4_ws(ws, 256, a_codes.device)
+    _check(lib().moe_mx4_product(a_codes.data_ptr(), a_scales.data_ptr(), rows,
+                                 b_codes.data_ptr(), b_scales.data_ptr(), _ptr(offsets), E, N, K,
+                                 out.data_ptr(), _code(out), ws.data_ptr(), ws.numel(),
+                                 _stream(stream)), "moe_mx4_product")
+    return out
+
+
+def _offsets(offsets, E: int, where: str):
+    _cuda(offsets)
+    if offsets.dtype != torch.int32 or offsets.numel() != E + 1:
+        raise MoeError(2, f"{where}: offsets are int32 [E + 1]")
+
+
+def _mx4_expert_weights(gate, up, down, H: int, where: str):
+    """Checks (codes, scales) of gate, up [E, I] rows of H and down [E, H] rows of I -> (E, I)."""
+    for m in (gate, up, down):
+        if m[0].dim() != 3:
+            raise MoeError(2, f"{where}: expert weights are [E, rows, bytes]")
+    E, I = gate[0].shape[:2]
+    _mx4_rows(*gate, H, where)
+    _mx4_rows(*up, H, where)
+    _mx4_rows(*down, I, where)
+    if up[0].shape[:2] != (E, I) or down[0].shape[:2] != (E, H):
+        raise MoeError(2, f"{where}: gate, up and down do not belong together")
+    return E, I
+
+
+def mx4_experts_workspace_bytes(rows: int, H: int, I: int) -> int:
+    return lib().moe_mx4_experts_workspace_bytes(rows, H, I)
+
+
+def moe_mx4_experts_forward_dispatched(x_d, offsets, gate, up, down, y=None, ws=None,
+                                       stream=None):
+    """SwiGLU experts with weights and activations in blocks -> y [rows, H] in x_d's dtype.
+    gate, up, down: (codes, scales) of [E, I, H], [E, I, H] and [E, H, I]."""
+    _cuda(x_d)
+    rows, H = x_d.shape
+    E, I = _mx4_expert_weights(gate, up, down, H, "moe_mx4_experts_forward_dispatched")
+    _offsets(offsets, E, "moe_mx4_experts_forward_dispatched")
+    y = torch.empty_like(x_d) if y is None else y
+    if y.shape != x_d.shape or y.dtype != x_d.dtype:
+        raise MoeError(2, "moe_mx4_experts_forward_dispatched: y is not like x_d")
+    _cuda(y)
+    ws = _mx4_ws(ws, mx4_experts_workspace_bytes(rows, H, I), x_d.device)
+    _check(lib().moe_mx4_experts_forward_dispatched(
+        x_d.data_ptr(), _code(x_d), offsets.data_ptr(), rows, gate[0].data_ptr(),
+        gate[1].data_ptr(), up[0].data_ptr(), up[1].data_ptr(), down[0].data_ptr(),
+        down[1].data_ptr(), E, H, I, y.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream)),
+        "moe_mx4_experts_forward_dispatched")
+    return y

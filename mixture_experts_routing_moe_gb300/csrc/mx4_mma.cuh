@@ -1,0 +1,80 @@
+// Inline-PTX wrappers of the block-scaled tensor instructions the microscaled kernels use, beside
+// those of tcgen05.cuh.
+//
+// tcgen05.mma kind::mxf4 multiplies packed e2m1 operands (128-byte swizzled K-major tiles, 256
+// values a 128-byte row; one instruction takes K = 64, 32 bytes of a row) with one power-of-two
+// scale for each 32 values of each row, read from tensor memory.  Scales of 128 rows and four
+// blocks (128 values) are one 512-byte chunk in shared memory, the four bytes of row r at
+// (r % 32) * 16 + (r / 32) * 4; tcgen05.cp 32x128b.warpx4 spreads it over four 32-bit columns
+// (column j: rows 32 j .. 32 j + 31, repeated in each 32-lane quarter).  Each K = 64 step uses two
+// of the four bytes, named by the scale ids of the instruction descriptor (0 or 2).
+#pragma once
+
+#include "tcgen05.cuh"
+
+namespace moe {
+namespace tc {
+
+constexpr int kScaleChunk = 512;  // bytes: 128 rows x 4 blocks
+
+// Byte offset in a chunk of row r's four scales.
+static __device__ __forceinline__ uint32_t scale_chunk_offset(int r) {
+  return (uint32_t)((r & 31) * 16 + (r >> 5) * 4);
+}
+// Shared-memory descriptor of a scale chunk: no swizzle, 8-row groups of 16-byte rows 128 bytes
+// apart.
+static __device__ __forceinline__ uint64_t make_sdesc_scale(uint32_t saddr) {
+  return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
+}
+static __device__ __forceinline__ void tmem_cp_scale(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
+               : "memory");
+}
+// Instruction descriptor of kind::mxf4: e2m1 (1) x e2m1 (1), both K-major, scales ue8m0; N >> 3 at
+// bit 17, M >> 7 at bit 27, scale ids of B at bit 4 and of A at bit 29.
+static __host__ __device__ constexpr uint32_t make_idesc_mxf4(int M, int N, int sf_id) {
+  return ((uint32_t)sf_id << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) |
+         (1u << 23) | ((uint32_t)(M >> 7) << 27) | ((uint32_t)sf_id << 29);
+}
+static __device__ __forceinline__ void umma_mxf4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                                 uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                                 uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], "
+      "[%5], p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
+
+// Four-byte asynchronous copy into shared memory (through L1, whose lines hold the neighbouring
+// slices of the same rows' scales).
+static __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+static __device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+static __device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// 2-D map over a row-major byte matrix [rows, pitch], box 128 bytes x box_rows, 128-byte swizzle;
+// bytes past the end read as zero.  pitch is a multiple of 16.
+static inline bool make_map_bytes(CUtensorMap* m, const void* ptr, int64_t pitch, int64_t rows,
+                                  int box_rows) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)pitch, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)pitch};
+  cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace tc
+}  // namespace moe
