@@ -4,20 +4,23 @@
 //   gate/up   the blocks of silu(A gate_e^T) * (A up_e^T), quantised in the epilogue
 // over the ragged row groups offsets[e] .. offsets[e+1]-1.
 //
-// A persistent kernel, one CTA per SM, walks 128 x 256 tiles (expert, m-tile, n-tile).  Roles:
-//   warp 0      one thread loads, for each 256-deep K slice, the codes of 128 A rows and 256 B rows
-//               (128 bytes a row) by TMA into a 4-stage ring.  For gate/up the B tile holds gate
-//               rows 0-63, up rows 0-63, gate rows 64-127, up rows 64-127 of 128 columns of a.
-//   warp 1      one thread copies each slice's scales to tensor memory and issues its four
-//               K = 64 MMAs (M = 128, N = 256); tcgen05.commit frees the slot.
-//   warps 2-3   gather the scales of the slice's 384 rows with 4-byte cp.async into the chunk
-//               layout; groups start at any row, so no bulk copy of a fixed box would do.
-//   warps 4-11  epilogue: each warp takes 32 rows x 128 columns of the accumulator into registers
+// A persistent kernel walks tiles (expert, m-tile, n-tile) of 256 columns and 128 rows (a CTA) or
+// 256 rows (a cluster of two CTAs, cta_group::2: each CTA holds 128 of the rows and half of the B
+// rows, so a tile pulls a third fewer bytes through L2).  Roles in each CTA:
+//   warp 0      one thread loads, for each 256-deep K slice, the codes of its A and B rows (128
+//               bytes a row) by TMA into a ring.  For gate/up the B tile holds gate rows 0-63, up
+//               rows 0-63, gate rows 64-127, up rows 64-127 of 128 columns of a.
+//   warp 1      one thread (of CTA 0) copies each slice's scales to tensor memory and issues its
+//               four K = 64 MMAs (N = 256); tcgen05.commit frees the slot.
+//   warps 4-7   scales: each thread holds 32 bytes (four slices) of one A row and two B rows in
+//               registers, loads the next 32 ahead, and writes each slice's words to the chunk
+//               layout.  Groups start at any row, so no bulk copy of a fixed box would do; four
+//               bytes at a time per slice (the first form) kept the L1 tag stage busy for 768
+//               cycles a slice and held the product at 1.64 PFLOP/s.
+//   warps 8-15  epilogue: each warp takes 32 rows x 128 columns of the accumulator into registers
 //               at once and frees it, so the next tile's MMAs run while it converts and stores.
 //               (256 accumulator columns and the scales leave no room for a second accumulator.)
 // Waits are bounded; on expiry the status word records the timeout and every role leaves.
-#include <atomic>
-
 #include "launch.h"
 #include "mx4.cuh"
 #include "mx4_mma.cuh"
@@ -28,17 +31,26 @@ namespace {
 using namespace tc;
 using namespace mx4;
 
-constexpr int BM = 128, BN = 256, STAGES = 4;
-constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128;
-constexpr int SF_BYTES = 6 * kScaleChunk;  // A: 2 chunks; B: 2 x 2 (K chunk, row half)
-constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-constexpr int kThreads = 384;
-constexpr int kLoaders = 64, kLag = STAGES - 1;
+constexpr int BM = 128, BN = 256;  // rows of a CTA, columns of a tile
+constexpr int SF_BYTES = 6 * kScaleChunk;  // a slice: 2 chunks of A, 2 x 2 (K chunk, row half) of B
+constexpr int kThreads = 512;
+// Registers of a thread of each warpgroup (the launch gives 128 to each; 72 + 104 + 2 * 168 = 512
+// = 4 * 128 are taken): the epilogue holds 128 accumulator values at once.
+constexpr int kRegsIssue = 72, kRegsScales = 104, kRegsEpilogue = 168;
 constexpr int kMaxExperts = 1024;
-constexpr int kBarBytes = 128;
-constexpr size_t kSmemBytes = 1024 + (size_t)STAGES * (STAGE_BYTES + SF_BYTES) + kBarBytes +
-                              2 * (kMaxExperts + 4) * sizeof(int);
+constexpr int kBarBytes = 256;
 constexpr uint32_t kTmemCols = 512, kScaleCol = 256;
+
+// CG: CTAs of a tile
+template <int CG>
+struct Shape {
+  static constexpr int STAGES = CG == 2 ? 6 : 4;
+  static constexpr int A_BYTES = BM * 128, B_BYTES = BN / CG * 128;
+  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+  static constexpr size_t SMEM = 1024 + (size_t)STAGES * (STAGE_BYTES + SF_BYTES) + kBarBytes +
+                                 2 * (kMaxExperts + 4) * sizeof(int);
+};
+static_assert(Shape<1>::SMEM <= 232448 && Shape<2>::SMEM <= 232448, "shared memory of a CTA");
 
 struct Params {
   const int32_t* offsets;  // null: one group of `rows` rows
@@ -47,6 +59,7 @@ struct Params {
   const uint8_t* b_scales;   // gate for the gate/up product
   const uint8_t* b2_scales;  // up
   int64_t scale_pitch;       // of a row of K values
+  int scales_vec;            // every scale base is a multiple of 16 bytes
   int E, N, KB, NT;          // N: rows of one expert's B (gate/up: I); KB: 256-deep slices
   void* out;
   uint8_t* codes;            // gate/up: rows of N values in blocks
@@ -55,15 +68,41 @@ struct Params {
   int zero_status;
 };
 
+// 32 consecutive bytes of a row's scales from byte `at` (a multiple of 32) on; bytes past the row
+// are zero.  VEC: the pitch and the base are multiples of 16 bytes.
+template <bool VEC>
+__device__ __forceinline__ void load_scales(const uint8_t* row, int at, int pitch, uint32_t* w) {
+  if (VEC) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (at + 16 * j < pitch) v = ld_nc_v4(row + at + 16 * j);
+      w[4 * j] = v.x, w[4 * j + 1] = v.y, w[4 * j + 2] = v.z, w[4 * j + 3] = v.w;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      w[j] = at + 4 * j < pitch ? __ldg(reinterpret_cast<const uint32_t*>(row + at + 4 * j)) : 0u;
+  }
+}
+
+__device__ __forceinline__ void st_v8(void* p, const uint4& a, const uint4& b) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(a.x), "r"(a.y),
+               "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+               : "memory");
+}
+// 32 accumulator columns of a row.  vec: the row pitch and the base are multiples of 32 bytes, so
+// that a store fills a whole 32-byte sector (16-byte stores cost twice the requests).
 template <typename T>
 __device__ __forceinline__ void store_row(T* row, const float* v, int col0, int N, bool vec) {
   constexpr int W = 16 / sizeof(T);
   if (vec && col0 + 32 <= N) {
 #pragma unroll
-    for (int i = 0; i < 32 / W; ++i) {
-      Vec16<T> q;
+    for (int i = 0; i < 32 / W; i += 2) {
+      Vec16<T> q, r;
       q.from_float(v + i * W);
-      st_v4(row + col0 + i * W, q.u);
+      r.from_float(v + (i + 1) * W);
+      st_v8(row + col0 + i * W, q.u, r.u);
     }
   } else {
 #pragma unroll
@@ -72,10 +111,12 @@ __device__ __forceinline__ void store_row(T* row, const float* v, int col0, int 
   }
 }
 
-template <bool GATEUP, typename T>
+template <int CG, bool GATEUP, typename T>
 __global__ void __launch_bounds__(kThreads, 1)
     moe_mx4_gemm(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
                  const __grid_constant__ CUtensorMap mapB2, const Params p) {
+  using S = Shape<CG>;
+  constexpr int STAGES = S::STAGES, STAGE_BYTES = S::STAGE_BYTES;
   extern __shared__ uint8_t mx4_smem_raw[];
   const uint32_t raw = smem_u32(mx4_smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -83,8 +124,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t sf_base = base + STAGES * STAGE_BYTES;
   uint64_t* bars = reinterpret_cast<uint64_t*>(gbase + STAGES * (STAGE_BYTES + SF_BYTES));
   const uint32_t bar0 = smem_u32(bars);
-  auto full_bar = [&](int s) { return bar0 + 8u * s; };
-  auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };               // CTA 0's is used
+  auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };   // each CTA's own
   const uint32_t tfull = bar0 + 8u * (2 * STAGES), tempty = tfull + 8, drain_bar = tfull + 16;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 3);
   volatile int* abort_f = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -92,19 +133,26 @@ __global__ void __launch_bounds__(kThreads, 1)
   int* offs = pref + (kMaxExperts + 4);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = CG == 2 ? (int)cluster_rank() : 0;
+  const bool leader = rank == 0;
+  const int first = CG == 2 ? (int)cluster_id_x() : (int)blockIdx.x;
+  const int step = CG == 2 ? (int)ncluster_x() : (int)gridDim.x;
   if (p.zero_status && blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(full_bar(s), 1 + kLoaders);
+      mbar_init(full_bar(s), 1 + 4 * CG);  // the producer's expect_tx and the scale warps
       mbar_init(empty_bar(s), 1);
     }
     mbar_init(tfull, 1);
-    mbar_init(tempty, 8);
+    mbar_init(tempty, 8 * CG);
     mbar_init(drain_bar, 1);
     *abort_f = 0;
     fence_mbar_init();
   }
-  if (warp == 1) tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+  if (warp == 1) {
+    if (CG == 2) tmem_alloc2(smem_u32(tmem_slot), kTmemCols);
+    else tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+  }
   // a copy of the offsets, kept inside [0, rows] whatever the caller's array holds
   for (int i = threadIdx.x; i <= p.E; i += kThreads) {
     const int64_t v = p.offsets ? (int64_t)__ldg(p.offsets + i) : (i ? p.rows : 0);
@@ -112,18 +160,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncthreads();
   if (warp == 2)
-    build_expert_prefix(offs, p.E, [](int n) { return n > 0 ? (n + BM - 1) / BM : 0; }, pref, lane);
+    build_expert_prefix(
+        offs, p.E, [](int n) { return n > 0 ? (n + BM * CG - 1) / (BM * CG) : 0; }, pref, lane);
   if (threadIdx.x == 0) {
     tma_prefetch(&mapA);
     tma_prefetch(&mapB);
     if (GATEUP) tma_prefetch(&mapB2);
   }
   tc_fence_before();
-  __syncthreads();
+  if (CG == 2) cluster_sync_all();
+  else __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const int total = pref[p.E] * p.NT;
-  // tile t -> first row, end of the group's rows, first row of the expert's B, n-tile
+  // an arrival on the same barrier of CTA 0
+  auto arrive_leader = [&](uint32_t bar) {
+    if (leader) mbar_arrive(bar);
+    else mbar_arrive_cluster(map_to_rank(bar, 0));
+  };
+  // tile t -> this CTA's first row, end of the group's rows, expert, n-tile
   struct Tile {
     int r0, r1, e, n;
   };
@@ -134,36 +189,43 @@ __global__ void __launch_bounds__(kThreads, 1)
     // eight m-tiles beside one n-tile, then the next n-tile
     const int g0 = local / (8 * p.NT) * 8, gm = min(8, mt - g0), q = local - g0 * p.NT;
     x.n = q / gm;
-    x.r0 = offs[x.e] + (g0 + q % gm) * BM;
+    x.r0 = offs[x.e] + (g0 + q % gm) * (BM * CG) + rank * BM;
     x.r1 = offs[x.e + 1];
     return x;
   };
 
-  if (warp == 0) {
-    if (lane == 0) {
+  if (warp < 4) {
+    set_max_regs_dec<kRegsIssue>();
+    if (warp == 0 && lane == 0) {
       int stage = 0, armed = 0;
       uint32_t phase = 0;
       bool stop = false;
       const uint64_t pol = policy_evict_normal();
-      for (int t = blockIdx.x; t < total && !stop; t += gridDim.x) {
+      for (int t = first; t < total && !stop; t += step) {
         const Tile x = tile_of(t);
-        const int b_row = x.e * p.N + x.n * (GATEUP ? BN / 2 : BN);
+        const int b_row = x.e * p.N + x.n * (GATEUP ? BN / 2 : BN) +
+                          rank * (GATEUP ? BN / 4 : BN / 2);
         for (int kb = 0; kb < p.KB; ++kb) {
           if (!wait_bounded(empty_bar(stage), phase ^ 1u, abort_f, p.status)) {
             stop = true;
             break;
           }
-          const uint32_t sa = base + stage * STAGE_BYTES, sb = sa + A_BYTES, fb = full_bar(stage);
-          mbar_expect_tx(fb, STAGE_BYTES);
-          tma_load_2d(sa, &mapA, fb, kb * 128, x.r0, pol);
+          const uint32_t sa = base + stage * STAGE_BYTES, sb = sa + S::A_BYTES;
+          if (leader) mbar_expect_tx(full_bar(stage), CG * STAGE_BYTES);
+          const uint32_t fb = CG == 2 ? map_to_rank(full_bar(stage), 0) : full_bar(stage);
+          auto load = [&](uint32_t dst, const CUtensorMap* m, int row) {
+            if (CG == 2) tma_load_2d_pair(dst, m, fb, kb * 128, row, pol);
+            else tma_load_2d(dst, m, fb, kb * 128, row, pol);
+          };
+          load(sa, &mapA, x.r0);
           if (GATEUP) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              tma_load_2d(sb + h * 128 * 128, &mapB, fb, kb * 128, b_row + h * 64, pol);
-              tma_load_2d(sb + h * 128 * 128 + 64 * 128, &mapB2, fb, kb * 128, b_row + h * 64, pol);
+            for (int h = 0; h < 2 / CG; ++h) {
+              load(sb + h * 128 * 128, &mapB, b_row + h * 64);
+              load(sb + h * 128 * 128 + 64 * 128, &mapB2, b_row + h * 64);
             }
           } else {
-            tma_load_2d(sb, &mapB, fb, kb * 128, b_row, pol);
+            load(sb, &mapB, b_row);
           }
           ++armed;
           if (++stage == STAGES) {
@@ -172,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (*abort_f) {  // let copies still in flight land
+      if (*abort_f && leader) {  // let copies still in flight land
         for (int i = 0; i < min(armed, STAGES); ++i) {
           if (stage == 0) {
             stage = STAGES - 1;
@@ -184,112 +246,134 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-  } else if (warp == 1) {
-    if (lane == 0) {
-      constexpr uint32_t idesc0 = make_idesc_mxf4(BM, BN, 0), idesc2 = make_idesc_mxf4(BM, BN, 2);
+    if (warp == 1 && leader && lane == 0) {
+      constexpr uint32_t idesc0 = make_idesc_mxf4(BM * CG, BN, 0);
+      constexpr uint32_t idesc2 = make_idesc_mxf4(BM * CG, BN, 2);
+      auto wait = [&](uint32_t bar, uint32_t parity) {
+        return CG == 2 ? wait_bounded_cluster(bar, parity, abort_f, p.status)
+                       : wait_bounded(bar, parity, abort_f, p.status);
+      };
+      auto copy = [&](uint32_t taddr, uint32_t chunk) {
+        if (CG == 2) tmem_cp_scale2(taddr, make_sdesc_scale(chunk));
+        else tmem_cp_scale(taddr, make_sdesc_scale(chunk));
+      };
       int stage = 0;
       uint32_t phase = 0, tphase = 0;
       bool stop = false;
-      for (int t = blockIdx.x; t < total && !stop; t += gridDim.x) {
-        if (!wait_bounded(tempty, tphase ^ 1u, abort_f, p.status)) break;
+      for (int t = first; t < total && !stop; t += step) {
+        if (!wait(tempty, tphase ^ 1u)) break;
         tphase ^= 1u;
         tc_fence_after();
         for (int kb = 0; kb < p.KB; ++kb) {
-          if (!wait_bounded(full_bar(stage), phase, abort_f, p.status)) {
+          if (!wait(full_bar(stage), phase)) {
             stop = true;
             break;
           }
           tc_fence_after();
-          const uint32_t sa = base + stage * STAGE_BYTES, sb = sa + A_BYTES;
+          const uint32_t sa = base + stage * STAGE_BYTES, sb = sa + S::A_BYTES;
           const uint32_t sf = sf_base + stage * SF_BYTES;
           const uint64_t da = make_sdesc(sa), db = make_sdesc(sb);
 #pragma unroll
           for (int c = 0; c < 2; ++c) {  // 128 values: A chunk c, B chunks (c, half)
             const uint32_t ca = tmem + kScaleCol + c * 12, cb = ca + 4;
-            tmem_cp_scale(ca, make_sdesc_scale(sf + c * kScaleChunk));
-            tmem_cp_scale(cb, make_sdesc_scale(sf + (2 + 2 * c) * kScaleChunk));
-            tmem_cp_scale(cb + 4, make_sdesc_scale(sf + (3 + 2 * c) * kScaleChunk));
+            copy(ca, sf + c * kScaleChunk);
+            copy(cb, sf + (2 + 2 * c) * kScaleChunk);
+            copy(cb + 4, sf + (3 + 2 * c) * kScaleChunk);
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk)
-              umma_mxf4(tmem, da + 2u * (2 * c + kk), db + 2u * (2 * c + kk), kk ? idesc2 : idesc0,
-                        ca, cb, (kb | c | kk) != 0);
+            for (int kk = 0; kk < 2; ++kk) {
+              const uint64_t a = da + 2u * (2 * c + kk), b = db + 2u * (2 * c + kk);
+              const uint32_t idesc = kk ? idesc2 : idesc0, more = (kb | c | kk) != 0;
+              if (CG == 2) umma2_mxf4(tmem, a, b, idesc, ca, cb, more);
+              else umma_mxf4(tmem, a, b, idesc, ca, cb, more);
+            }
           }
-          umma_commit(empty_bar(stage));
+          if (CG == 2) umma_commit2(empty_bar(stage), 0x3);
+          else umma_commit(empty_bar(stage));
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;
           }
         }
-        if (!stop) umma_commit(tfull);
+        if (stop) break;
+        if (CG == 2) umma_commit2(tfull, 0x3);
+        else umma_commit(tfull);
       }
-      umma_commit(drain_bar);  // arrives once every MMA issued above has completed
+      // arrives once every MMA issued above has completed
+      if (CG == 2) umma_commit2(drain_bar, 0x1);
+      else umma_commit(drain_bar);
       wait_drain(drain_bar, 0);
     }
-  } else if (warp < 4) {
-    // scales: thread i takes A rows i, i + 64 and B rows i, i + 64, i + 128, i + 192 of the tile
-    const int i0 = threadIdx.x - 64;
-    int stage = 0, pending = 0, done = 0;
+  } else if (warp < 8) {
+    set_max_regs_dec<kRegsScales>();
+    // scales: thread i takes A row i and B rows i, i + 128 of the tile
+    const int i = threadIdx.x - 128;
+    const int pitch = (int)p.scale_pitch;
+    const bool vec = (pitch & 15) == 0 && p.scales_vec;
+    const uint32_t dst = scale_chunk_offset(i);
+    int stage = 0;
     uint32_t phase = 0;
     bool stop = false;
-    auto arrive_oldest = [&]() {
-      fence_proxy_async_smem();
-      mbar_arrive(full_bar(done));
-      if (++done == STAGES) done = 0;
-      --pending;
-    };
-    const int words = (int)(p.scale_pitch / 4);
-    for (int t = blockIdx.x; t < total && !stop; t += gridDim.x) {
+    // quads of slices over all of this CTA's tiles; the next quad's words are loaded ahead
+    const int quads = (p.KB + 3) / 4;
+    uint32_t next[3][8];
+    auto load_quad = [&](int t, int quad) {
       const Tile x = tile_of(t);
-      const uint8_t* src[6];
-      uint32_t dst[6];
+      const uint8_t* src[3];
+      src[0] = p.a_scales + min((int64_t)x.r0 + i, p.rows - 1) * pitch;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int r = i0 + 64 * j;
-        const int64_t row = min((int64_t)x.r0 + r, p.rows - 1);
-        src[j] = p.a_scales + row * p.scale_pitch;
-        dst[j] = scale_chunk_offset(r);
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int r = i0 + 64 * j;  // j selects gate 0, up 0, gate 1, up 1 of the gate/up tile
-        int n = GATEUP ? x.n * (BN / 2) + (j >> 1) * 64 + i0 : x.n * BN + r;
+      for (int h = 0; h < 2; ++h) {
+        int n = GATEUP ? x.n * (BN / 2) + h * 64 + (i & 63) : x.n * BN + h * 128 + i;
         n = min(n, p.N - 1);
-        const uint8_t* b = GATEUP && (j & 1) ? p.b2_scales : p.b_scales;
-        src[2 + j] = b + ((int64_t)x.e * p.N + n) * p.scale_pitch;
-        dst[2 + j] = (2 + (r >> 7)) * kScaleChunk + scale_chunk_offset(r & 127);
+        const uint8_t* b = GATEUP && i >= 64 ? p.b2_scales : p.b_scales;
+        src[1 + h] = b + ((int64_t)x.e * p.N + n) * pitch;
       }
-      for (int kb = 0; kb < p.KB; ++kb) {
-        if (!wait_bounded(empty_bar(stage), phase ^ 1u, abort_f, p.status)) {
-          stop = true;
-          break;
-        }
-        const uint32_t sf = sf_base + stage * SF_BYTES;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          // a row's last slice may have no second chunk: its codes are the zeros TMA fills in, and
-          // any finite scale will do
-          const int w = min(kb * 2 + c, words - 1);
+      for (int j = 0; j < 3; ++j) {
+        if (vec) load_scales<true>(src[j], quad * 32, pitch, next[j]);
+        else load_scales<false>(src[j], quad * 32, pitch, next[j]);
+      }
+    };
+    if (first < total) load_quad(first, 0);
+    for (int t = first; t < total && !stop; t += step) {
+      for (int quad = 0; quad < quads && !stop; ++quad) {
+        uint32_t now[3][8];
 #pragma unroll
-          for (int j = 0; j < 6; ++j)
-            cp_async4(sf + dst[j] + (j < 2 ? c : 2 * c) * kScaleChunk, src[j] + w * 4);
-        }
-        cp_async_commit();
-        if (++pending > kLag) {
-          cp_async_wait<kLag>();
-          arrive_oldest();
-        }
-        if (++stage == STAGES) {
-          stage = 0;
-          phase ^= 1u;
+        for (int j = 0; j < 3; ++j)
+#pragma unroll
+          for (int w = 0; w < 8; ++w) now[j][w] = next[j][w];
+        if (quad + 1 < quads) load_quad(t, quad + 1);
+        else if (t + step < total) load_quad(t + step, 0);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (quad * 4 + k >= p.KB || stop) continue;
+          // (every lane waits: the warp's threads write together)
+          if (!__all_sync(0xFFFFFFFFu,
+                          wait_bounded(empty_bar(stage), phase ^ 1u, abort_f, p.status))) {
+            stop = true;
+            continue;
+          }
+          const uint32_t sf = sf_base + stage * SF_BYTES + dst;
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            st_shared_u32(sf + c * kScaleChunk, now[0][2 * k + c]);
+            st_shared_u32(sf + (2 + 2 * c) * kScaleChunk, now[1][2 * k + c]);
+            st_shared_u32(sf + (3 + 2 * c) * kScaleChunk, now[2][2 * k + c]);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) arrive_leader(full_bar(stage));
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
         }
       }
     }
-    cp_async_wait<0>();
-    while (pending > 0) arrive_oldest();
   } else {
-    const int q = warp & 3, h = (warp >> 2) - 1;  // lane quarter, column half
+    set_max_regs_inc<kRegsEpilogue>();
+    const int q = warp & 3, h = warp >= 12;  // lane quarter, column half
     uint32_t tphase = 0;
-    for (int t = blockIdx.x; t < total; t += gridDim.x) {
+    for (int t = first; t < total; t += step) {
       const Tile x = tile_of(t);
       const bool ok = wait_bounded(tfull, tphase, abort_f, p.status);
       if (!__all_sync(0xFFFFFFFFu, ok)) break;
@@ -302,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_wait_ld();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(tempty);
+      if (lane == 0) arrive_leader(tempty);
       const int row = x.r0 + q * 32 + lane;
       if (row < x.r1) {
         if (GATEUP) {
@@ -334,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         } else {
           T* orow = (T*)p.out + (int64_t)row * p.N;
-          const bool vec = ((uintptr_t)p.out & 15u) == 0 && (p.N * sizeof(T)) % 16 == 0;
+          const bool vec = ((uintptr_t)p.out & 31u) == 0 && (p.N * sizeof(T)) % 32 == 0;
 #pragma unroll
           for (int c = 0; c < 4; ++c)
             store_row(orow, reinterpret_cast<const float*>(acc[c]), x.n * BN + h * 128 + c * 32,
@@ -345,10 +429,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   tc_fence_before();
-  __syncthreads();
+  __syncwarp();
+  if (CG == 2) cluster_sync_all();  // no CTA leaves while its pair may still signal it
+  else __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, kTmemCols);
+    if (CG == 2) tmem_dealloc2(tmem, kTmemCols);
+    else tmem_dealloc(tmem, kTmemCols);
   }
 }
 
@@ -359,20 +446,46 @@ int sm_count(cudaError_t* err) {
   return sms;
 }
 
+template <int CG, bool GATEUP, typename T>
+cudaError_t launch_cg(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& b2,
+                      const Params& p, int sms, cudaStream_t s) {
+  auto kern = moe_mx4_gemm<CG, GATEUP, T>;
+  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)Shape<CG>::SMEM);
+  if (err != cudaSuccess) return err;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = CG;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Shape<CG>::SMEM;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = CG == 2 ? 1 : 0;
+  const int64_t rows_per = BM * CG;
+  const int64_t upper = ((p.rows + rows_per - 1) / rows_per + p.E) * (int64_t)p.NT;  // >= tiles
+  const int64_t fit = sms / CG;
+  cfg.gridDim = dim3((unsigned)(CG * (upper < fit ? upper : fit)));
+  return cudaLaunchKernelEx(&cfg, kern, a, b, b2, p);
+}
+
+// Pairs when groups average at least 128 rows; below that a pair's taller tiles mostly multiply
+// padding.
+bool use_pairs(int64_t rows, int E) { return rows >= (int64_t)BM * E; }
+
 template <bool GATEUP, typename T>
 cudaError_t launch(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& b2,
                    const Params& p, cudaStream_t s) {
   cudaError_t err;
   const int sms = sm_count(&err);
   if (err != cudaSuccess) return err;
-  err = cudaFuncSetAttribute(moe_mx4_gemm<GATEUP, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)kSmemBytes);
-  if (err != cudaSuccess) return err;
-  const int64_t upper = ((p.rows + BM - 1) / BM + p.E) * (int64_t)p.NT;  // >= number of tiles
-  moe_mx4_gemm<GATEUP, T>
-      <<<(unsigned)(upper < sms ? upper : sms), kThreads, kSmemBytes, s>>>(a, b, b2, p);
-  return cudaGetLastError();
+  return use_pairs(p.rows, p.E) ? launch_cg<2, GATEUP, T>(a, b, b2, p, sms, s)
+                                : launch_cg<1, GATEUP, T>(a, b, b2, p, sms, s);
 }
+
+bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
 Params make_params(Mx4Rows a, int64_t rows, const int32_t* offsets, int E, int N, int K, int cols,
                    unsigned* status) {
@@ -397,10 +510,11 @@ cudaError_t launch_mx4_product(Mx4Rows a, int64_t rows, Mx4Rows b, const int32_t
   CUtensorMap ma, mb;
   const int64_t pitch = code_pitch(K);
   if (!make_map_bytes(&ma, a.codes, pitch, rows, BM) ||
-      !make_map_bytes(&mb, b.codes, pitch, (int64_t)E * N, BN))
+      !make_map_bytes(&mb, b.codes, pitch, (int64_t)E * N, use_pairs(rows, E) ? BN / 2 : BN))
     return cudaErrorInvalidValue;
   Params p = make_params(a, rows, offsets, E, N, K, BN, status);
   p.b_scales = b.scales;
+  p.scales_vec = aligned16(a.scales) && aligned16(b.scales);
   p.out = out;
   p.zero_status = zero_status;
   switch (odt) {
@@ -423,6 +537,7 @@ cudaError_t launch_mx4_gate_up(Mx4Rows a, int64_t rows, Mx4Rows gate, Mx4Rows up
   Params p = make_params(a, rows, offsets, E, I, H, BN / 2, status);
   p.b_scales = gate.scales;
   p.b2_scales = up.scales;
+  p.scales_vec = aligned16(a.scales) && aligned16(gate.scales) && aligned16(up.scales);
   p.codes = codes;
   p.scales = scales;
   return launch<true, float>(ma, mg, mu, p, s);
