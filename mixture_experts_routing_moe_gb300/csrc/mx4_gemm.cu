@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // an arrival on the same barrier of CTA 0
   auto arrive_leader = [&](uint32_t bar) {
     if (leader) mbar_arrive(bar);
-    else mbar_arrive_cluster(map_to_rank(bar, 0));
+    else mbar_arrive_cluster_shared(map_to_rank(bar, 0));
   };
   // tile t -> this CTA's first row, end of the group's rows, expert, n-tile
   struct Tile {

@@ -79,6 +79,15 @@ static __device__ __forceinline__ void set_max_regs_inc() {
 static __device__ __forceinline__ void st_shared_u32(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
+// Arrival on a barrier of another CTA of the cluster that releases this thread's (and, by
+// cumulativity, its warp's) shared-memory writes only: a full release at cluster scope also waits
+// for the warp's global accesses in flight.
+static __device__ __forceinline__ void mbar_arrive_cluster_shared(uint32_t cluster_addr) {
+  asm volatile(
+      "fence.release.sync_restrict::shared::cta.cluster;\n\t"
+      "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+      : "memory");
+}
 // Wait of wait_bounded() for a phase that threads of the other CTA complete too (acquire at
 // cluster scope).
 static __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
