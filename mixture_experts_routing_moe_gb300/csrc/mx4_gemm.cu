@@ -12,11 +12,11 @@
 //               rows 0-63, gate rows 64-127, up rows 64-127 of 128 columns of a.
 //   warp 1      one thread (of CTA 0) copies each slice's scales to tensor memory and issues its
 //               four K = 64 MMAs (N = 256); tcgen05.commit frees the slot.
-//   warps 4-7   scales: each thread holds 32 bytes (four slices) of one A row and two B rows in
-//               registers, loads the next 32 ahead, and writes each slice's words to the chunk
-//               layout.  Groups start at any row, so no bulk copy of a fixed box would do; four
-//               bytes at a time per slice (the first form) kept the L1 tag stage busy for 768
-//               cycles a slice and held the product at 1.64 PFLOP/s.
+//   warps 4-6   scales of A and of the two halves of B: each lane holds 32 bytes (four slices) of
+//               four rows in registers, loads the next 32 ahead, and writes each slice's words to
+//               the chunk layout, 16 bytes at a time.  Groups start at any row, so no bulk copy of
+//               a fixed box would do; four bytes at a time per slice (the first form) kept the L1
+//               tag stage busy for 768 cycles a slice and held the product at 1.64 PFLOP/s.
 //   warps 8-15  epilogue: each warp takes 32 rows x 128 columns of the accumulator into registers
 //               at once and frees it, so the next tile's MMAs run while it converts and stores.
 //               (256 accumulator columns and the scales leave no room for a second accumulator.)
@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (p.zero_status && blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(full_bar(s), 1 + 4 * CG);  // the producer's expect_tx and the scale warps
+      mbar_init(full_bar(s), 1 + 3 * CG);  // the producer's expect_tx and the scale warps
       mbar_init(empty_bar(s), 1);
     }
     mbar_init(tfull, 1);
@@ -273,19 +273,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t sa = base + stage * STAGE_BYTES, sb = sa + S::A_BYTES;
           const uint32_t sf = sf_base + stage * SF_BYTES;
           const uint64_t da = make_sdesc(sa), db = make_sdesc(sb);
+          // a slot of columns for each stage, so that the copies need not wait for the MMAs of the
+          // slice before: 128 values (c) take 4 columns for A and 8 for the two halves of B
+          const uint32_t cols = tmem + kScaleCol + stage * 24;
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {  // 128 values: A chunk c, B chunks (c, half)
-            const uint32_t ca = tmem + kScaleCol + c * 12, cb = ca + 4;
-            copy(ca, sf + c * kScaleChunk);
-            copy(cb, sf + (2 + 2 * c) * kScaleChunk);
-            copy(cb + 4, sf + (3 + 2 * c) * kScaleChunk);
+          for (int c = 0; c < 2; ++c) {
+            copy(cols + c * 12, sf + c * kScaleChunk);
+            copy(cols + c * 12 + 4, sf + (2 + 2 * c) * kScaleChunk);
+            copy(cols + c * 12 + 8, sf + (3 + 2 * c) * kScaleChunk);
+          }
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {
-              const uint64_t a = da + 2u * (2 * c + kk), b = db + 2u * (2 * c + kk);
-              const uint32_t idesc = kk ? idesc2 : idesc0, more = (kb | c | kk) != 0;
-              if (CG == 2) umma2_mxf4(tmem, a, b, idesc, ca, cb, more);
-              else umma_mxf4(tmem, a, b, idesc, ca, cb, more);
-            }
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t ca = cols + (k >> 1) * 12, cb = ca + 4;
+            const uint32_t idesc = (k & 1) ? idesc2 : idesc0, more = (kb | k) != 0;
+            if (CG == 2) umma2_mxf4(tmem, da + 2u * k, db + 2u * k, idesc, ca, cb, more);
+            else umma_mxf4(tmem, da + 2u * k, db + 2u * k, idesc, ca, cb, more);
           }
           if (CG == 2) umma_commit2(empty_bar(stage), 0x3);
           else umma_commit(empty_bar(stage));
@@ -305,40 +307,45 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp < 8) {
     set_max_regs_dec<kRegsScales>();
-    // scales: thread i takes A row i and B rows i, i + 128 of the tile
-    const int i = threadIdx.x - 128;
+    // scales: warp 4 takes the A rows, warps 5 and 6 the two halves of the B rows; lane l holds
+    // rows l, l + 32, l + 64, l + 96, whose words are 16 consecutive bytes of a chunk
+    const int part = warp - 4;
     const int pitch = (int)p.scale_pitch;
     const bool vec = (pitch & 15) == 0 && p.scales_vec;
-    const uint32_t dst = scale_chunk_offset(i);
     int stage = 0;
     uint32_t phase = 0;
-    bool stop = false;
+    bool stop = part == 3;
     // quads of slices over all of this CTA's tiles; the next quad's words are loaded ahead
     const int quads = (p.KB + 3) / 4;
-    uint32_t next[3][8];
+    uint32_t next[4][8];
     auto load_quad = [&](int t, int quad) {
       const Tile x = tile_of(t);
-      const uint8_t* src[3];
-      src[0] = p.a_scales + min((int64_t)x.r0 + i, p.rows - 1) * pitch;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        int n = GATEUP ? x.n * (BN / 2) + h * 64 + (i & 63) : x.n * BN + h * 128 + i;
-        n = min(n, p.N - 1);
-        const uint8_t* b = GATEUP && i >= 64 ? p.b2_scales : p.b_scales;
-        src[1 + h] = b + ((int64_t)x.e * p.N + n) * pitch;
-      }
-#pragma unroll
-      for (int j = 0; j < 3; ++j) {
-        if (vec) load_scales<true>(src[j], quad * 32, pitch, next[j]);
-        else load_scales<false>(src[j], quad * 32, pitch, next[j]);
+      for (int j = 0; j < 4; ++j) {
+        const int i = 32 * j + lane;
+        const uint8_t* src;
+        if (part == 0) {
+          src = p.a_scales + min((int64_t)x.r0 + i, p.rows - 1) * pitch;
+        } else {
+          const int h = part - 1;
+          int n = GATEUP ? x.n * (BN / 2) + h * 64 + (i & 63) : x.n * BN + h * 128 + i;
+          n = min(n, p.N - 1);
+          const uint8_t* b = GATEUP && j >= 2 ? p.b2_scales : p.b_scales;
+          src = b + ((int64_t)x.e * p.N + n) * pitch;
+        }
+        if (vec) load_scales<true>(src, quad * 32, pitch, next[j]);
+        else load_scales<false>(src, quad * 32, pitch, next[j]);
       }
     };
-    if (first < total) load_quad(first, 0);
+    if (first < total && !stop) load_quad(first, 0);
+    // chunk (c, half) of B is chunk 2 + 2 c + half of a slice, chunk c of A is chunk c
+    const uint32_t dst = sf_base + (part == 0 ? 0 : 1 + part) * kScaleChunk + lane * 16;
+    const uint32_t chunk_step = (part == 0 ? 1 : 2) * kScaleChunk;
     for (int t = first; t < total && !stop; t += step) {
       for (int quad = 0; quad < quads && !stop; ++quad) {
-        uint32_t now[3][8];
+        uint32_t now[4][8];
 #pragma unroll
-        for (int j = 0; j < 3; ++j)
+        for (int j = 0; j < 4; ++j)
 #pragma unroll
           for (int w = 0; w < 8; ++w) now[j][w] = next[j][w];
         if (quad + 1 < quads) load_quad(t, quad + 1);
@@ -352,13 +359,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             stop = true;
             continue;
           }
-          const uint32_t sf = sf_base + stage * SF_BYTES + dst;
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            st_shared_u32(sf + c * kScaleChunk, now[0][2 * k + c]);
-            st_shared_u32(sf + (2 + 2 * c) * kScaleChunk, now[1][2 * k + c]);
-            st_shared_u32(sf + (3 + 2 * c) * kScaleChunk, now[2][2 * k + c]);
-          }
+          for (int c = 0; c < 2; ++c)
+            st_shared_v4(dst + stage * SF_BYTES + c * chunk_step, now[0][2 * k + c],
+                         now[1][2 * k + c], now[2][2 * k + c], now[3][2 * k + c]);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) arrive_leader(full_bar(stage));
