@@ -72,6 +72,9 @@ _SIGS = {
     "moe_mx4_experts_workspace_bytes": (_sz, [_i64, _i64, _i64]),
     "moe_mx4_experts_forward_dispatched": (_int, [_vp, _int, _vp, _i64, _vp, _vp, _vp, _vp, _vp,
                                                   _vp, _i64, _i64, _i64, _vp, _vp, _sz, _vp]),
+    "moe_mx4_tokens_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64, _int, _int]),
+    "moe_mx4_forward_tokens": (_int, [_vp, _vp, _int, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64,
+                                      _i64, _i64, _int, _int, _vp, _vp, _vp, _vp, _sz, _vp]),
 }
 
 _lib = None
@@ -530,3 +533,37 @@ def moe_mx4_experts_forward_dispatched(x_d, offsets, gate, up, down, y=None, ws=
         down[1].data_ptr(), E, H, I, y.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream)),
         "moe_mx4_experts_forward_dispatched")
     return y
+
+
+def mx4_tokens_workspace_bytes(T: int, E: int, H: int, I: int, top_k: int, dtype) -> int:
+    return lib().moe_mx4_tokens_workspace_bytes(T, E, H, I, top_k, DTYPE_CODE[dtype])
+
+
+def moe_mx4_forward_tokens(x, router, gate, up, down, top_k: int, renormalize: bool = True,
+                           out=None, idx=None, w=None, ws=None, stream=None):
+    """A whole layer for a few tokens (router, top-k, experts in blocks, combine) -> out [T, H].
+    router [E, H] in x's dtype (f16 / bf16); gate, up, down: (codes, scales).  idx (uint32
+    [T, top_k]) and w (float32 [T, top_k]), when given, receive the selection."""
+    where = "moe_mx4_forward_tokens"
+    _cuda(x, router, idx, w)
+    T, H = x.shape
+    E, I = _mx4_expert_weights(gate, up, down, H, where)
+    if router.shape != (E, H) or router.dtype != x.dtype:
+        raise MoeError(2, f"{where}: router is [E, H] in x's dtype")
+    if (idx is not None and (idx.dtype != torch.uint32 or idx.shape != (T, top_k))) or (
+            w is not None and (w.dtype != torch.float32 or w.shape != (T, top_k))):
+        raise MoeError(2, f"{where}: idx is uint32 [T, top_k], w float32 [T, top_k]")
+    out = torch.empty_like(x) if out is None else out
+    if out.shape != x.shape or out.dtype != x.dtype:
+        raise MoeError(2, f"{where}: out is not like x")
+    _cuda(out)
+    if ws is None:
+        ws = torch.empty(max(lib().moe_mx4_tokens_workspace_bytes(T, E, H, I, top_k, _code(x)), 256),
+                         dtype=torch.uint8, device=x.device)
+    _cuda(ws)
+    _check(lib().moe_mx4_forward_tokens(
+        x.data_ptr(), router.data_ptr(), _code(x), gate[0].data_ptr(), gate[1].data_ptr(),
+        up[0].data_ptr(), up[1].data_ptr(), down[0].data_ptr(), down[1].data_ptr(), T, E, H, I,
+        top_k, int(bool(renormalize)), out.data_ptr(), _ptr(idx), _ptr(w), ws.data_ptr(),
+        ws.numel(), _stream(stream)), where)
+    return out

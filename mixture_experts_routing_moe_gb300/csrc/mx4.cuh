@@ -85,4 +85,25 @@ cudaError_t launch_mx4_gate_up(Mx4Rows a, int64_t rows, Mx4Rows gate, Mx4Rows up
                                const int32_t* offsets, int E, int I, int H, uint8_t* codes,
                                uint8_t* scales, unsigned* status, cudaStream_t s);
 
+
+// The whole layer for a few tokens (one cooperative launch).  ws holds tokens_layout().total bytes;
+// its first `zeroed` bytes are cleared by the launch.
+struct Mx4TokensLayout {
+  size_t ready, done, zeroed;      // counters behind the header
+  size_t logits, xq, xs, aq, as, y, total;
+};
+Mx4TokensLayout mx4_tokens_layout(int64_t T, int64_t E, int64_t H, int64_t I, int k, int dt);
+struct Mx4TokensArgs {
+  const void* x;
+  const void* router;
+  int dt, T, E, H, I, k, renorm;
+  Mx4Rows gate, up, down;
+  void* out;
+  uint32_t* idx;  // may be null
+  float* w;       // may be null
+  uint8_t* ws;
+};
+cudaError_t launch_mx4_tokens(const Mx4TokensArgs& a, cudaStream_t s);
+constexpr int kMx4TokensMaxT = 64, kMx4TokensMaxK = 32, kMx4TokensMaxSlots = 1024;
+
 }  // namespace moe

@@ -55,6 +55,15 @@ ExpertsLayout experts_layout(int64_t rows, int64_t H, int64_t I) {
   return l;
 }
 
+int check_tokens_shape(int64_t T, int64_t E, int64_t H, int64_t I, int k, int dt) {
+  if (dt != MOE_F16 && dt != MOE_BF16) return MOE_ERR_DTYPE;
+  if (T < 0 || T > kMx4TokensMaxT || E < 1 || E > kMaxE || k < 1 || k > E || k > kMx4TokensMaxK ||
+      T * k > kMx4TokensMaxSlots || !dim_ok(H) || !dim_ok(I) || E * H >= kMaxRows ||
+      E * I >= kMaxRows)
+    return MOE_ERR_SHAPE;
+  return H % 128 || I % 128 ? MOE_ERR_ALIGN : MOE_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -145,6 +154,50 @@ int moe_mx4_experts_forward_dispatched(const void* x_d, int xdt, const int32_t* 
     err = launch_mx4_product({b + l.ac, b + l.as}, rows, {down_codes, down_scales}, offsets, (int)E,
                              (int)H, (int)I, y, xdt, status, false, s);
   return cuda_status(err);
+}
+
+size_t moe_mx4_tokens_workspace_bytes(int64_t T, int64_t E, int64_t H, int64_t I, int top_k,
+                                      int dt) {
+  if (check_tokens_shape(T, E, H, I, top_k, dt) != MOE_OK) return 0;
+  return mx4_tokens_layout(T, E, H, I, top_k, dt).total;
+}
+
+int moe_mx4_forward_tokens(const void* x, const void* router, int dt, const uint8_t* gate_codes,
+                           const uint8_t* gate_scales, const uint8_t* up_codes,
+                           const uint8_t* up_scales, const uint8_t* down_codes,
+                           const uint8_t* down_scales, int64_t T, int64_t E, int64_t H, int64_t I,
+                           int top_k, int renormalize, void* out, uint32_t* idx, float* w,
+                           void* ws, size_t ws_bytes, moe_stream_t stream) {
+  if (int st = check_tokens_shape(T, E, H, I, top_k, dt)) return st;
+  if (int st = check_operand(gate_codes, gate_scales)) return st;
+  if (int st = check_operand(up_codes, up_scales)) return st;
+  if (int st = check_operand(down_codes, down_scales)) return st;
+  if (!router) return MOE_ERR_NULL;
+  if (T == 0) return MOE_OK;
+  if (!x || !out) return MOE_ERR_NULL;
+  if (!aligned(x, 16) || !aligned(router, 16) || !aligned(gate_codes, 32) ||
+      !aligned(up_codes, 32) || !aligned(down_codes, 32) || !aligned(out, 2) || !aligned(idx, 4) ||
+      !aligned(w, 4))
+    return MOE_ERR_ALIGN;
+  if (int st = check_ws(ws, ws_bytes, mx4_tokens_layout(T, E, H, I, top_k, dt).total)) return st;
+  Mx4TokensArgs a{};
+  a.x = x;
+  a.router = router;
+  a.dt = dt;
+  a.T = (int)T;
+  a.E = (int)E;
+  a.H = (int)H;
+  a.I = (int)I;
+  a.k = top_k;
+  a.renorm = renormalize != 0;
+  a.gate = {gate_codes, gate_scales};
+  a.up = {up_codes, up_scales};
+  a.down = {down_codes, down_scales};
+  a.out = out;
+  a.idx = idx;
+  a.w = w;
+  a.ws = (uint8_t*)ws;
+  return cuda_status(launch_mx4_tokens(a, (cudaStream_t)stream));
 }
 
 }  // extern "C"

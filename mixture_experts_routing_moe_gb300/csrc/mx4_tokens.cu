@@ -1,0 +1,825 @@
+// A whole MoE layer for a few tokens with microscaled 4-bit expert weights, in one cooperative
+// launch: router logits, top-k, gate/up, SwiGLU, down and combine.
+//
+//   logits[t, e] = x[t] . router[e];  idx, w as moe_route (softmax over all experts, ties to the
+//   lower id);  a = round16(silu(x gate_e^T) * (x up_e^T));  out[t] = sum_j w[t, j] (a_j down_e^T)
+//
+// The layer reads each active expert's weights once, 17/32 of a byte a weight, and that is its
+// floor, so nothing may be spent on the weights but the copy.  The tensor cores decode them:
+// tcgen05.mma kind::mxf8f6f4 takes e2m1 weights (M = 128 weight rows, widened to a byte in shared
+// memory by the tensor map) against e4m3 tokens, and applies the weights' block scales.  The
+// tokens keep their 16 bits: e4m3 has four significant bits, so a bf16 value (eight) is the exact
+// sum of two e4m3 terms and an f16 value (eleven) of three, each in blocks of 32 with a scale of
+// its own, 2^-4 of the one before.  The terms are separate columns (N) of the MMA, and the
+// epilogue adds them up.  (Exact for values down to 2^-13 of their block's largest; below that the
+// error is under 2^-22 of that largest.)  N is small, so the extra columns cost no time: a K = 128
+// slice of 128 weight rows takes the MMAs about 130 cycles and the memory about 370.
+//
+// Steps.  One CTA per SM, all resident; grid-wide hand-overs go through counters in global memory:
+//   0  every CTA splits its share of x into terms (xq, xs) and computes the logits of its experts;
+//      grid barrier.
+//   1  every CTA selects the top-k of all tokens for itself (the same arithmetic everywhere) and
+//      lists the active experts' tokens in shared memory.
+//   2  units of work: (expert, group of tokens, 64 columns of a) for gate/up, then (expert, group,
+//      128 columns of the output) for down, dealt to the CTAs in turn.  Warp roles as in the
+//      grouped products: weight codes (TMA), token terms (TMA), weight scales, token scales, MMA,
+//      epilogue.  The gate/up epilogue writes a as terms (aq, as) and counts the unit on its
+//      expert; a down unit's weights are loaded ahead, its tokens once that count is full.  The
+//      weight loads never wait for anything but a free slot, from the first unit to the last.
+//   3  the down epilogue writes y (FP32, one row a slot); whoever finishes the last unit of an
+//      output tile adds the slots up in the order j = 0 .. k - 1 and writes out.
+// Waits are bounded; on expiry the status word records the timeout and every role leaves.
+#include <atomic>
+
+#include "launch.h"
+#include "mx4.cuh"
+#include "mx4_mma.cuh"
+#include "route_core.cuh"
+#include "tiles.cuh"
+
+namespace moe {
+namespace {
+using namespace tc;
+using namespace mx4;
+
+constexpr int kThreads = 384, kWarps = kThreads / 32;
+constexpr int kA = 128 * 128;          // bytes of a stage's weights, widened
+constexpr int kMaxStages = 12;
+constexpr int kBarBytes = 512;
+constexpr uint32_t kTmemCols = 512, kScaleCol = 256;
+constexpr int kExchange = 16 * 64 * 4;  // u of up to 16 tokens x 64 columns
+
+// terms of a token value, columns between two tokens, tokens of a group (N <= 128)
+template <typename T> struct Terms;
+template <> struct Terms<__nv_bfloat16> { static constexpr int P = 2, STRIDE = 2, G = 64; };
+template <> struct Terms<__half> { static constexpr int P = 3, STRIDE = 4, G = 32; };
+
+struct TokensParams {
+  const void* x;
+  const void* router;
+  int T, E, H, I, k, renorm;
+  const uint8_t *gs, *us, *ds;
+  int scales_vec;
+  float* logits;
+  uint8_t *xq, *xs, *aq, *as;
+  float* y;
+  unsigned *status, *grid_count, *ready, *done;
+  void* out;
+  uint32_t* idx;
+  float* w;
+  int stages, stage_bytes;  // ring
+};
+
+__device__ __forceinline__ unsigned ld_acquire_u32(const unsigned* p) {
+  unsigned v;
+  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ bool wait_count(const unsigned* c, unsigned want, volatile int* abort_f,
+                                           unsigned* status) {
+  const long long t0 = clock64();
+  while (ld_acquire_u32(c) < want) {
+    if (*abort_f) return false;
+    if (clock64() - t0 > kWaitLimit) {
+      *abort_f = 1;
+      atomicOr(status, kStatusTimeout);
+      return false;
+    }
+    __nanosleep(20);
+  }
+  return true;
+}
+__device__ __forceinline__ void fence_proxy_async_all() {
+  asm volatile("fence.proxy.async;" ::: "memory");
+}
+
+// A warp writes one block of 32 values (one a lane) as P e4m3 terms: term p of the lane's value at
+// q[p * pitch], the scale bytes at sc[p * sc_pitch] (lane 0).  With the largest magnitude in
+// [2^n, 2^(n + 1)) the first scale is 2^(n - 7), so scaled values stay under 2^8 < 448; each
+// remainder is at most 8 of the first grid's sixteenths and is scaled up by 16.
+template <int P>
+__device__ __forceinline__ void write_terms(float v, uint8_t* q, int64_t pitch, uint8_t* sc,
+                                            int64_t sc_pitch, int lane) {
+  const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v) & 0x7FFFFFFFu);
+  const int f = (int)(top >> 23);
+  const bool bad = f == 255;
+  const int b0 = max(f - 7, 4 * (P - 1));
+  float r = bad ? 0.f : v * __uint_as_float((uint32_t)(254 - min(b0, 253)) << 23);
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    uint16_t h;
+    uint32_t back;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h) : "f"(0.f), "f"(r));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(h));
+    q[p * pitch] = (uint8_t)(h & 0xFFu);
+    if (lane == 0) sc[p * sc_pitch] = (uint8_t)(bad ? 255 : b0 - 4 * p);
+    r = (r - __low2float(*reinterpret_cast<const __half2*>(&back))) * 16.f;
+  }
+}
+
+// One warp selects the top-k of a row of FP32 logits: ids and weights of slots 0 .. k - 1.  Lane l
+// holds experts l, l + 32, ...; keys order as route_core.cuh's, ties to the lower id.
+template <int C>
+__device__ __forceinline__ void select_row(const float* row, int E, int k, int renorm, int lane,
+                                           uint16_t* ids, float* ws) {
+  uint32_t key[C];
+  float m = -INFINITY;
+  uint32_t flags = 0;
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int e = c * 32 + lane;
+    key[c] = 0;
+    if (e < E) {
+      const float v = __ldcg(row + e);
+      if (v != v || v == INFINITY) flags |= 1u;
+      if (v != -INFINITY) flags |= 2u;
+      m = fmaxf(m, v);
+      key[c] = monotone_bits(v == 0.f ? 0.f : v);  // both zeros take +0's key
+    }
+  }
+  flags = __reduce_or_sync(0xFFFFFFFFu, flags);
+  m = group_max<32>(m);
+  if ((flags & 1u) || !(flags & 2u)) {
+    if (lane < k) {
+      ids[lane] = (uint16_t)lane;
+      ws[lane] = __int_as_float(0x7FC00000);
+    }
+    return;
+  }
+  float s = 0.f, sel = 0.f, mine = 0.f;
+  if (!renorm) {
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+      if (c * 32 + lane < E) s += expf(from_monotone_bits(key[c]) - m);
+    s = group_sum<32>(s);
+  }
+  for (int j = 0; j < k; ++j) {
+    uint32_t best = key[0];
+    int at = 0;
+#pragma unroll
+    for (int c = 1; c < C; ++c)
+      if (key[c] > best) best = key[c], at = c;
+    const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, best);
+    const uint32_t id =
+        __reduce_min_sync(0xFFFFFFFFu, best == top ? (uint32_t)(at * 32 + lane) : 0xFFFFu);
+    const float ex = expf(from_monotone_bits(top) - m);
+    sel += ex;
+    if (lane == j) {
+      ids[j] = (uint16_t)id;
+      mine = ex;
+    }
+    if ((id & 31u) == (uint32_t)lane) {
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+        if (c == (int)(id >> 5)) key[c] = 0;
+    }
+  }
+  if (lane < k) ws[lane] = mine / (renorm ? sel : s);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 1)
+    moe_mx4_tokens(const __grid_constant__ CUtensorMap mapG, const __grid_constant__ CUtensorMap mapU,
+                   const __grid_constant__ CUtensorMap mapD,
+                   const __grid_constant__ CUtensorMap mapX,
+                   const __grid_constant__ CUtensorMap mapA, const TokensParams p) {
+  constexpr int P = Terms<T>::P, STRIDE = Terms<T>::STRIDE, G = Terms<T>::G;
+  extern __shared__ uint8_t mx4_smem_raw[];
+  const uint32_t raw = smem_u32(mx4_smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* at = mx4_smem_raw + (base - raw) + p.stages * p.stage_bytes;
+  const uint32_t sf_base = smem_u32(at);  // a stage's scales: one chunk of A, one of B
+  at += p.stages * 2 * kScaleChunk;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(at);
+  at += kBarBytes;
+  float* exchange = reinterpret_cast<float*>(at);
+  at += kExchange;
+  unsigned long long* mask = reinterpret_cast<unsigned long long*>(at);  // tokens of an expert
+  at += p.E * 8;
+  int* start = reinterpret_cast<int*>(at);  // first entry of an expert's tokens in `list`
+  at += (p.E + 1) * 4;
+  int* gpref = reinterpret_cast<int*>(at);  // groups of tokens before an expert
+  at += (p.E + 1) * 4;
+  const int R = p.T * p.k;
+  float* sel_w = reinterpret_cast<float*>(at);
+  at += R * 4;
+  uint16_t* sel_id = reinterpret_cast<uint16_t*>(at);
+  uint16_t* list = sel_id + R;  // slots t * k + j, expert by expert, by token
+  float* red = reinterpret_cast<float*>(mx4_smem_raw + (base - raw));  // step 0 only: in the ring
+
+  const uint32_t bar0 = smem_u32(bars);
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (kMaxStages + s); };
+  auto tfull_bar = [&](int a) { return bar0 + 8u * (2 * kMaxStages + a); };
+  auto tempty_bar = [&](int a) { return bar0 + 8u * (2 * kMaxStages + 2 + a); };
+  const uint32_t drain_bar = bar0 + 8u * (2 * kMaxStages + 4);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kMaxStages + 5);
+  volatile int* abort_f = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* last_s = reinterpret_cast<int*>(tmem_slot + 2);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(full_bar(s), 4);  // weights, tokens, weight scales, token scales
+      mbar_init(empty_bar(s), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(tfull_bar(a), 1);
+      mbar_init(tempty_bar(a), 4);
+    }
+    mbar_init(drain_bar, 1);
+    *abort_f = 0;
+    fence_mbar_init();
+    tma_prefetch(&mapG);
+    tma_prefetch(&mapU);
+    tma_prefetch(&mapD);
+    tma_prefetch(&mapX);
+    tma_prefetch(&mapA);
+  }
+  if (warp == 1) tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+  for (int e = threadIdx.x; e < p.E; e += kThreads) mask[e] = 0;
+
+  // ------------------------------------------------ 0. terms of x, router logits
+  const T* x = (const T*)p.x;
+  const T* router = (const T*)p.router;
+  {
+    const int hb = p.H / 32;
+    for (int b = blockIdx.x * kWarps + warp; b < p.T * hb; b += gridDim.x * kWarps) {
+      const int t = b / hb, c = b - t * hb;
+      const float v = Dt<T>::to_f(x[(int64_t)t * p.H + c * 32 + lane]);
+      write_terms<P>(v, p.xq + (int64_t)t * P * p.H + c * 32 + lane, p.H,
+                     p.xs + (int64_t)t * P * hb + c, hb, lane);
+    }
+    constexpr int TB = 4;  // tokens at a time
+    for (int e = blockIdx.x; e < p.E; e += gridDim.x) {
+      for (int t0 = 0; t0 < p.T; t0 += TB) {
+        float acc[TB] = {};
+        for (int v = threadIdx.x; v < p.H / 8; v += kThreads) {
+          Vec16<T> r;
+          r.u = ld_nc_v4(router + (int64_t)e * p.H + v * 8);
+          float rf[8];
+          r.to_float(rf);
+#pragma unroll
+          for (int i = 0; i < TB; ++i) {
+            if (t0 + i < p.T) {
+              Vec16<T> q;
+              q.u = ld_nc_v4(x + (int64_t)(t0 + i) * p.H + v * 8);
+              float xf[8];
+              q.to_float(xf);
+#pragma unroll
+              for (int z = 0; z < 8; ++z) acc[i] = fmaf(xf[z], rf[z], acc[i]);
+            }
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < TB; ++i) {
+          const float s = group_sum<32>(acc[i]);
+          if (lane == 0) red[(t0 + i) * kWarps + warp] = s;
+        }
+      }
+      __syncthreads();
+      if (threadIdx.x < p.T) {
+        float s = 0.f;
+        for (int w = 0; w < kWarps; ++w) s += red[threadIdx.x * kWarps + w];
+        p.logits[(int64_t)threadIdx.x * p.E + e] = s;
+      }
+      __syncthreads();
+    }
+  }
+  fence_proxy_async_all();  // xq is read by TMA
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    __threadfence();
+    atomicAdd(p.grid_count, 1u);
+    wait_count(p.grid_count, gridDim.x, abort_f, p.status);
+    __threadfence();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  // ------------------------------------------------ 1. top-k, lists of the experts' tokens
+  if (!*abort_f) {
+    for (int t = warp; t < p.T; t += kWarps) {
+      const float* row = p.logits + (int64_t)t * p.E;
+      uint16_t* ids = sel_id + t * p.k;
+      float* ws = sel_w + t * p.k;
+      if (p.E <= 128) select_row<4>(row, p.E, p.k, p.renorm, lane, ids, ws);
+      else if (p.E <= 256) select_row<8>(row, p.E, p.k, p.renorm, lane, ids, ws);
+      else select_row<32>(row, p.E, p.k, p.renorm, lane, ids, ws);
+      __syncwarp();
+      if (lane < p.k) {
+        atomicOr(mask + ids[lane], 1ull << t);
+        if (blockIdx.x == 0) {
+          if (p.idx) p.idx[t * p.k + lane] = ids[lane];
+          if (p.w) p.w[t * p.k + lane] = ws[lane];
+        }
+      }
+    }
+  }
+  __syncthreads();
+  if (warp == 0) {
+    int carry = 0, gcarry = 0;
+    for (int e0 = 0; e0 < p.E; e0 += 32) {
+      const int e = e0 + lane;
+      const int n = e < p.E ? __popcll(mask[e]) : 0, g = (n + G - 1) / G;
+      int s = n, sg = g;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xFFFFFFFFu, s, o), yg = __shfl_up_sync(0xFFFFFFFFu, sg, o);
+        if (lane >= o) s += y, sg += yg;
+      }
+      if (e < p.E) start[e] = carry + s - n, gpref[e] = gcarry + sg - g;
+      carry += __shfl_sync(0xFFFFFFFFu, s, 31);
+      gcarry += __shfl_sync(0xFFFFFFFFu, sg, 31);
+    }
+    if (lane == 0) start[p.E] = carry, gpref[p.E] = gcarry;
+  }
+  __syncthreads();
+  if (!*abort_f) {
+    for (int s = threadIdx.x; s < R; s += kThreads) {
+      const int e = sel_id[s], t = s / p.k;
+      list[start[e] + __popcll(mask[e] & ((1ull << t) - 1))] = (uint16_t)s;
+    }
+  }
+  __syncthreads();
+
+  // ------------------------------------------------ 2. units
+  const int NI = p.I / 64, NH = p.H / 128;
+  const int groups = *abort_f ? 0 : gpref[p.E];
+  const int n1 = groups * NI, total = n1 + groups * NH;
+  struct Unit {
+    bool down;
+    int e, eg, tile;    // expert, group (over all experts), column tile
+    int first, n;       // its tokens: list[first .. first + n)
+    int KB;             // 128-deep slices
+  };
+  auto unit_of = [&](int u) {
+    Unit r;
+    r.down = u >= n1;
+    const int v = r.down ? u - n1 : u, NT = r.down ? NH : NI;
+    r.eg = v / NT;
+    r.tile = v - r.eg * NT;
+    r.e = find_expert(gpref, p.E, r.eg);
+    r.first = start[r.e] + (r.eg - gpref[r.e]) * G;
+    r.n = min(start[r.e + 1] - r.first, G);
+    r.KB = (r.down ? p.I : p.H) / 128;
+    return r;
+  };
+  auto columns = [&](int n) { return (n * STRIDE + 15) / 16 * 16; };  // N of a unit
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // -------------------------------------------------------------- weight codes
+      int stage = 0;
+      uint32_t phase = 0;
+      bool stop = false;
+      const uint64_t pol = policy_evict_normal();
+      for (int u = blockIdx.x; u < total && !stop; u += gridDim.x) {
+        const Unit r = unit_of(u);
+        for (int kb = 0; kb < r.KB; ++kb) {
+          if (!wait_bounded(empty_bar(stage), phase ^ 1u, abort_f, p.status)) {
+            stop = true;
+            break;
+          }
+          const uint32_t sa = base + stage * p.stage_bytes, fb = full_bar(stage);
+          mbar_expect_tx(fb, kA / 2);  // counted in packed bytes, not in the widened ones
+          if (r.down) {
+            tma_load_2d(sa, &mapD, fb, kb * 128, r.e * p.H + r.tile * 128, pol);
+          } else {
+            tma_load_2d(sa, &mapG, fb, kb * 128, r.e * p.I + r.tile * 64, pol);
+            tma_load_2d(sa + kA / 2, &mapU, fb, kb * 128, r.e * p.I + r.tile * 64, pol);
+          }
+          if (++stage == p.stages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // -------------------------------------------------------------- MMA
+      int stage = 0, acc = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool stop = false;
+      for (int u = blockIdx.x; u < total && !stop; u += gridDim.x) {
+        const Unit r = unit_of(u);
+        const int N = columns(r.n);
+        if (!wait_bounded(tempty_bar(acc), acc_phase ^ 1u, abort_f, p.status)) break;
+        tc_fence_after();
+        const uint32_t d = tmem + acc * 128;
+        for (int kb = 0; kb < r.KB; ++kb) {
+          if (!wait_bounded(full_bar(stage), phase, abort_f, p.status)) {
+            stop = true;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = base + stage * p.stage_bytes;
+          const uint32_t sf = sf_base + stage * 2 * kScaleChunk;
+          const uint32_t cols = tmem + kScaleCol + stage * 8;
+          const uint64_t da = make_sdesc(sa), db = make_sdesc(sa + kA);
+          tmem_cp_scale(cols, make_sdesc_scale(sf));
+          tmem_cp_scale(cols + 4, make_sdesc_scale(sf + kScaleChunk));
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_mxf8f6f4(d, da + 2u * kk, db + 2u * kk, make_idesc_mxf4_f8(128, N, kk), cols,
+                          cols + 4, (kb | kk) != 0);
+          umma_commit(empty_bar(stage));
+          if (++stage == p.stages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (stop) break;
+        umma_commit(tfull_bar(acc));
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1u;
+      }
+      umma_commit(drain_bar);
+      wait_drain(drain_bar, 0);
+    }
+  } else if (warp == 2) {
+    // -------------------------------------------------------------- token terms
+    int stage = 0, armed = 0;
+    uint32_t phase = 0;
+    bool stop = false;
+    const uint64_t pol = policy_evict_normal();
+    fence_proxy_async_all();  // xq was written by other CTAs before the grid barrier
+    for (int u = blockIdx.x; u < total && !stop; u += gridDim.x) {
+      const Unit r = unit_of(u);
+      if (r.down) {
+        bool ok = true;
+        if (lane == 0) ok = wait_count(p.ready + r.eg, NI, abort_f, p.status);
+        if (!__all_sync(0xFFFFFFFFu, ok)) break;
+        fence_proxy_async_all();
+      }
+      for (int kb = 0; kb < r.KB; ++kb) {
+        if (!__all_sync(0xFFFFFFFFu,
+                        wait_bounded(empty_bar(stage), phase ^ 1u, abort_f, p.status))) {
+          stop = true;
+          break;
+        }
+        const uint32_t sb = base + stage * p.stage_bytes + kA, fb = full_bar(stage);
+        if (lane == 0) mbar_expect_tx(fb, r.n * P * 128);
+        __syncwarp();
+        for (int i = lane; i < r.n; i += 32) {
+          const int slot = list[r.first + i];
+          tma_load_2d(sb + i * STRIDE * 128, r.down ? &mapA : &mapX, fb, kb * 128,
+                      (r.down ? slot : slot / p.k) * P, pol);
+        }
+        ++armed;
+        if (++stage == p.stages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    if (*abort_f && lane == 0) {  // let copies still in flight land
+      for (int i = 0; i < min(armed, p.stages); ++i) {
+        if (stage == 0) {
+          stage = p.stages - 1;
+          phase ^= 1u;
+        } else {
+          --stage;
+        }
+        wait_drain(full_bar(stage), phase);
+      }
+    }
+  } else if (warp == 4) {
+    // -------------------------------------------------------------- weight scales
+    // lane l holds rows l, l + 32, l + 64, l + 96 of the unit's 128, eight slices (32 bytes) each
+    int stage = 0;
+    uint32_t phase = 0;
+    bool stop = false;
+    uint32_t next[4][8];
+    auto load = [&](int u, int part) {
+      const Unit r = unit_of(u);
+      const int pitch = r.KB * 4;
+      const bool vec = p.scales_vec && (pitch & 15) == 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint8_t* src =
+            r.down ? p.ds + ((int64_t)r.e * p.H + r.tile * 128 + 32 * j + lane) * pitch
+                   : (j < 2 ? p.gs : p.us) +
+                         ((int64_t)r.e * p.I + r.tile * 64 + 32 * (j & 1) + lane) * pitch;
+        src += part * 32;
+        const int left = pitch - part * 32;
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+          if (vec) {
+            uint4 q = make_uint4(0, 0, 0, 0);
+            if (16 * z < left) q = ld_nc_v4(src + 16 * z);
+            next[j][4 * z] = q.x, next[j][4 * z + 1] = q.y;
+            next[j][4 * z + 2] = q.z, next[j][4 * z + 3] = q.w;
+          } else {
+#pragma unroll
+            for (int i = 4 * z; i < 4 * z + 4; ++i)
+              next[j][i] =
+                  4 * i < left ? __ldg(reinterpret_cast<const uint32_t*>(src + 4 * i)) : 0u;
+          }
+        }
+      }
+    };
+    if (blockIdx.x < total) load(blockIdx.x, 0);
+    for (int u = blockIdx.x; u < total && !stop; u += gridDim.x) {
+      const int KB = unit_of(u).KB, parts = (KB + 7) / 8;
+      for (int part = 0; part < parts && !stop; ++part) {
+        uint32_t now[4][8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) now[j][i] = next[j][i];
+        if (part + 1 < parts) load(u, part + 1);
+        else if (u + (int)gridDim.x < total) load(u + gridDim.x, 0);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (part * 8 + i >= KB || stop) continue;
+          if (!__all_sync(0xFFFFFFFFu,
+                          wait_bounded(empty_bar(stage), phase ^ 1u, abort_f, p.status))) {
+            stop = true;
+            continue;
+          }
+          st_shared_v4(sf_base + stage * 2 * kScaleChunk + lane * 16, now[0][i], now[1][i],
+                       now[2][i], now[3][i]);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(full_bar(stage));
+          if (++stage == p.stages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+    }
+  } else if (warp == 5) {
+    // -------------------------------------------------------------- token scales
+    // lane l holds the terms in columns l, l + 32, l + 64, l + 96, four slices each
+    int stage = 0;
+    uint32_t phase = 0;
+    bool stop = false;
+    for (int u = blockIdx.x; u < total && !stop; u += gridDim.x) {
+      const Unit r = unit_of(u);
+      if (r.down) {
+        bool ok = true;
+        if (lane == 0) ok = wait_count(p.ready + r.eg, NI, abort_f, p.status);
+        if (!__all_sync(0xFFFFFFFFu, ok)) break;
+      }
+      const int pitch = r.KB * 4;
+      const uint8_t* src[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int c = 32 * j + lane, i = c / STRIDE, term = c % STRIDE;
+        src[j] = nullptr;
+        if (i < r.n && term < P) {
+          const int slot = list[r.first + i];
+          src[j] = r.down ? p.as + ((int64_t)slot * P + term) * pitch
+                          : p.xs + ((int64_t)(slot / p.k) * P + term) * pitch;
+        }
+      }
+      uint32_t next[4][4];
+      auto load = [&](int quad) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            next[j][i] = src[j] && quad * 4 + i < r.KB ? ld_cg_u32(src[j] + quad * 16 + i * 4) : 0u;
+      };
+      load(0);
+      const int quads = (r.KB + 3) / 4;
+      for (int quad = 0; quad < quads && !stop; ++quad) {
+        uint32_t now[4][4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) now[j][i] = next[j][i];
+        if (quad + 1 < quads) load(quad + 1);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (quad * 4 + i >= r.KB || stop) continue;
+          if (!__all_sync(0xFFFFFFFFu,
+                          wait_bounded(empty_bar(stage), phase ^ 1u, abort_f, p.status))) {
+            stop = true;
+            continue;
+          }
+          st_shared_v4(sf_base + (stage * 2 + 1) * kScaleChunk + lane * 16, now[0][i], now[1][i],
+                       now[2][i], now[3][i]);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(full_bar(stage));
+          if (++stage == p.stages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+    }
+  } else if (warp >= 8) {
+    // -------------------------------------------------------------- epilogue
+    constexpr int PER = 32 / STRIDE;  // tokens in 32 columns
+    const int q = warp & 3;
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    auto any_of_epilogue = [&](bool v) {
+      uint32_t r;
+      asm volatile(
+          "{\n\t.reg .pred a, b;\n\tsetp.ne.u32 a, %1, 0;\n\t"
+          "barrier.cta.red.or.pred b, 1, 128, a;\n\tselp.u32 %0, 1, 0, b;\n\t}"
+          : "=r"(r)
+          : "r"((uint32_t)v)
+          : "memory");
+      return r != 0;
+    };
+    auto sync_epilogue = [&]() { asm volatile("bar.sync 1, 128;" ::: "memory"); };
+    for (int u = blockIdx.x; u < total; u += gridDim.x) {
+      const Unit r = unit_of(u);
+      // the four warps give up together, as the barriers below need all of them
+      if (any_of_epilogue(!wait_bounded(tfull_bar(acc), acc_phase, abort_f, p.status))) break;
+      tc_fence_after();
+      const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + acc * 128;
+      for (int i0 = 0; i0 < r.n; i0 += PER) {
+        uint32_t v[32];
+        tmem_ld32(taddr + i0 * STRIDE, v);
+        tmem_wait_ld();
+        float s[PER];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          s[i] = 0.f;
+#pragma unroll
+          for (int term = P - 1; term >= 0; --term) s[i] += __uint_as_float(v[i * STRIDE + term]);
+        }
+        if (r.down) {
+          float* y = p.y + r.tile * 128 + q * 32 + lane;
+#pragma unroll
+          for (int i = 0; i < PER; ++i)
+            if (i0 + i < r.n) y[(int64_t)list[r.first + i0 + i] * p.H] = s[i];
+        } else {
+          // warps of quarters 0 and 1 hold 64 gate rows, 2 and 3 the same up rows
+          if (q >= 2) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i) exchange[i * 64 + (q - 2) * 32 + lane] = s[i];
+          }
+          sync_epilogue();
+          if (q < 2) {
+            const int ib = p.I / 32, col = r.tile * 64 + q * 32;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+              if (i0 + i >= r.n) continue;
+              const float g = s[i];
+              const float up = exchange[i * 64 + q * 32 + lane];
+              const float a = Dt<T>::to_f(Dt<T>::from_f(g / (1.f + expf(-g)) * up));
+              const int64_t row = (int64_t)list[r.first + i0 + i] * P;
+              write_terms<P>(a, p.aq + row * p.I + col + lane, p.I, p.as + row * ib + col / 32, ib,
+                             lane);
+            }
+          }
+          sync_epilogue();
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(tempty_bar(acc));
+      acc ^= 1;
+      if (acc == 0) acc_phase ^= 1u;
+      if (!r.down) {
+        fence_proxy_async_all();  // aq is read by TMA
+        __threadfence();
+        sync_epilogue();
+        if (threadIdx.x == 8 * 32) atomicAdd(p.ready + r.eg, 1u);
+        continue;
+      }
+      __threadfence();
+      sync_epilogue();
+      if (threadIdx.x == 8 * 32)
+        *last_s = atomicAdd(p.done + r.tile, 1u) + 1 == (unsigned)groups;
+      sync_epilogue();
+      if (*last_s) {
+        __threadfence();
+        const int h = r.tile * 128 + (int)threadIdx.x - 8 * 32;
+        T* out = (T*)p.out + h;
+        for (int t = 0; t < p.T; ++t) {
+          float s = 0.f;
+          const float* y = p.y + (int64_t)t * p.k * p.H + h;
+#pragma unroll 8
+          for (int j = 0; j < p.k; ++j) s = fmaf(sel_w[t * p.k + j], __ldcg(y + (int64_t)j * p.H), s);
+          out[(int64_t)t * p.H] = Dt<T>::from_f(s);
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// Bytes of shared memory beside the ring.
+size_t fixed_smem(int E, int R) {
+  return 1024 + kBarBytes + kExchange + (size_t)E * 8 + 2 * (size_t)(E + 1) * 4 + (size_t)R * 8;
+}
+
+template <typename T>
+cudaError_t launch_t(const Mx4TokensArgs& a, cudaStream_t s) {
+  constexpr int P = Terms<T>::P, STRIDE = Terms<T>::STRIDE, G = Terms<T>::G;
+  int dev = 0, sms = 0, most = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err == cudaSuccess)
+    err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (err == cudaSuccess)
+    err = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+  if (err != cudaSuccess) return err;
+  const Mx4TokensLayout l = mx4_tokens_layout(a.T, a.E, a.H, a.I, a.k, a.dt);
+  TokensParams p{};
+  p.x = a.x;
+  p.router = a.router;
+  p.T = a.T;
+  p.E = a.E;
+  p.H = a.H;
+  p.I = a.I;
+  p.k = a.k;
+  p.renorm = a.renorm;
+  p.gs = a.gate.scales;
+  p.us = a.up.scales;
+  p.ds = a.down.scales;
+  p.scales_vec =
+      (((uintptr_t)p.gs | (uintptr_t)p.us | (uintptr_t)p.ds) & 15u) == 0;
+  p.status = (unsigned*)a.ws;
+  p.grid_count = (unsigned*)(a.ws + 64);
+  p.ready = (unsigned*)(a.ws + l.ready);
+  p.done = (unsigned*)(a.ws + l.done);
+  p.logits = (float*)(a.ws + l.logits);
+  p.xq = a.ws + l.xq;
+  p.xs = a.ws + l.xs;
+  p.aq = a.ws + l.aq;
+  p.as = a.ws + l.as;
+  p.y = (float*)(a.ws + l.y);
+  p.out = a.out;
+  p.idx = a.idx;
+  p.w = a.w;
+  const int R = a.T * a.k;
+  // the ring: as many slices as fit, each with room for the columns of the largest group
+  const int n = a.T < G ? a.T : G;
+  p.stage_bytes = kA + (n * STRIDE + 15) / 16 * 16 * 128;
+  const size_t fixed = fixed_smem(a.E, R);
+  p.stages = (int)(((size_t)most - fixed) / (p.stage_bytes + 2 * kScaleChunk));
+  if (p.stages > kMaxStages) p.stages = kMaxStages;
+  const size_t smem = fixed + (size_t)p.stages * (p.stage_bytes + 2 * kScaleChunk);
+
+  CUtensorMap mg, mu, md, mx, ma;
+  if (!make_map_codes(&mg, a.gate.codes, a.H, (int64_t)a.E * a.I, 64) ||
+      !make_map_codes(&mu, a.up.codes, a.H, (int64_t)a.E * a.I, 64) ||
+      !make_map_codes(&md, a.down.codes, a.I, (int64_t)a.E * a.H, 128) ||
+      !make_map_bytes(&mx, p.xq, a.H, (int64_t)a.T * P, P) ||
+      !make_map_bytes(&ma, p.aq, a.I, (int64_t)R * P, P))
+    return cudaErrorInvalidValue;
+  auto kern = moe_mx4_tokens<T>;
+  err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (err != cudaSuccess) return err;
+  err = cudaMemsetAsync(a.ws, 0, l.zeroed, s);
+  if (err != cudaSuccess) return err;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(sms);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, mg, mu, md, mx, ma, p);
+}
+
+}  // namespace
+
+Mx4TokensLayout mx4_tokens_layout(int64_t T, int64_t E, int64_t H, int64_t I, int k, int dt) {
+  const int64_t R = T * k, P = dt == MOE_F16 ? Terms<__half>::P : Terms<__nv_bfloat16>::P;
+  Mx4TokensLayout l;
+  size_t off = kWsHeader;
+  auto take = [&](size_t bytes) {
+    const size_t o = off;
+    off = align_up(off + bytes, 256);
+    return o;
+  };
+  l.ready = take((size_t)R * 4);
+  l.done = take((size_t)(H / 128) * 4);
+  l.zeroed = off;
+  l.logits = take((size_t)T * E * 4);
+  l.xq = take((size_t)T * P * H);
+  l.xs = take((size_t)T * P * (H / 32));
+  l.aq = take((size_t)R * P * I);
+  l.as = take((size_t)R * P * (I / 32));
+  l.y = take((size_t)R * H * 4);
+  l.total = off;
+  return l;
+}
+
+cudaError_t launch_mx4_tokens(const Mx4TokensArgs& a, cudaStream_t s) {
+  return a.dt == MOE_BF16 ? launch_t<__nv_bfloat16>(a, s) : launch_t<__half>(a, s);
+}
+
+}  // namespace moe

@@ -298,6 +298,151 @@ def test_experts_nan_row_and_empty():
     assert y.shape == (0, 64)
 
 
+# ------------------------------------------------------------------------------------- tokens
+def layer(T, E, H, I, dtype, seed):
+    rng = np.random.default_rng(seed)
+    x = torch.from_numpy(rng.standard_normal((T, H))).to(dtype)
+    router = torch.from_numpy(rng.standard_normal((E, H)) / np.sqrt(H)).to(dtype)
+    shapes = ((E, I, H), (E, I, H), (E, H, I))
+    packed = [blocks(rng.standard_normal(s) / np.sqrt(s[2])) for s in shapes]
+    return x, router, packed
+
+
+def tokens_reference(x, router, packed, idx, w):
+    """(out, tolerance without the last rounding) for a given selection and its weights."""
+    dtype = x.dtype
+    eps = torch.finfo(dtype).eps
+    xs, wt = np64(x), [M.values(p[2], p[3]) for p in packed]
+    T, H, I = xs.shape[0], xs.shape[1], wt[0].shape[1]
+    out, tol = np.zeros((T, H)), np.zeros((T, H))
+    u = 2.0 ** -23
+    for t in range(T):
+        for j, e in enumerate(idx[t]):
+            gate, up, down = (m[e] for m in wt)
+            g, v = gate @ xs[t], up @ xs[t]
+            # sums of 3 K products (the terms of x) in FP32, and terms that are exact to 2^-22 of
+            # their block's largest value
+            top = np.repeat(np.abs(xs[t]).reshape(-1, 32).max(-1), 32)
+            mag_g = (3 * H + 64) * u * (np.abs(gate) @ np.abs(xs[t])) + 2 * u * (np.abs(gate) @ top)
+            mag_v = (3 * H + 64) * u * (np.abs(up) @ np.abs(xs[t])) + 2 * u * (np.abs(up) @ top)
+            a = M.silu_mul(g, v)
+            da = 1.1 * mag_g * np.abs(v) + np.abs(M.silu_mul(g, 1.0)) * mag_v + 1.1 * mag_g * mag_v
+            da += eps / 2 * (np.abs(a) + da) + torch.finfo(dtype).tiny   # rounded to the type
+            ar = torch.from_numpy(a).to(dtype).double().numpy()
+            y = down @ a
+            top = np.repeat(np.abs(ar).reshape(-1, 32).max(-1), 32)
+            dy = np.abs(down) @ (da + 2 * u * top) + (3 * I + 64) * u * (np.abs(down) @ np.abs(a))
+            out[t] += w[t, j] * y
+            tol[t] += w[t, j] * (dy + 64 * u * np.abs(y))
+    return out, tol
+
+
+def check_tokens(T, E, H, I, k, dtype, renorm, seed):
+    x, router, packed = layer(T, E, H, I, dtype, seed)
+    ws = torch.empty(moe.mx4_tokens_workspace_bytes(T, E, H, I, k, dtype), dtype=torch.uint8,
+                     device=DEV)
+    idx = torch.empty(T, k, dtype=torch.uint32, device=DEV)
+    w = torch.empty(T, k, dtype=torch.float32, device=DEV)
+    out = moe.moe_mx4_forward_tokens(x.to(DEV), router.to(DEV), *[p[:2] for p in packed], top_k=k,
+                                     renormalize=renorm, idx=idx, w=w, ws=ws)
+    assert moe.moe_device_status(ws) == 0 and out.dtype == dtype
+    # selection: descending logits, none left out that is larger by more than the sums' error
+    logits = np64(x) @ np64(router).T
+    err = (H + 64) * 2.0 ** -23 * (np.abs(np64(x)) @ np.abs(np64(router)).T)
+    got = idx.view(torch.int32).cpu().numpy()
+    for t in range(T):
+        l, d = logits[t][got[t]], err[t].max()
+        assert len(set(got[t])) == k and (np.diff(l) <= 2 * d).all()
+        rest = np.delete(logits[t], got[t])
+        assert not len(rest) or rest.max() <= l[-1] + 2 * d
+    p = np.exp(logits - logits.max(-1, keepdims=True))
+    p /= p.sum(-1, keepdims=True)
+    ref_w = np.take_along_axis(p, got, 1)
+    if renorm:
+        ref_w /= ref_w.sum(-1, keepdims=True)
+    gw = np64(w)
+    # a logit off by err moves a weight by that factor; the rest is a few FP32 roundings
+    assert (np.abs(gw - ref_w) <= ref_w * (4 * err.max() + 64 * 2.0 ** -23)).all()
+    ref, tol = tokens_reference(x, router, packed, got, gw)
+    check_within(np64(out), ref, tol * (1 + torch.finfo(dtype).eps) + half_step(dtype, ref), dtype)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("T,E,H,I,k,renorm", [
+    (1, 1, 128, 128, 1, True), (1, 8, 256, 384, 2, True), (3, 5, 640, 128, 5, False),
+    (8, 16, 512, 256, 4, True), (9, 33, 128, 640, 3, False), (33, 2, 256, 128, 2, True),
+    (64, 6, 384, 256, 2, True), (64, 64, 128, 128, 16, True), (17, 200, 256, 128, 8, True),
+    (5, 1024, 128, 128, 32, False), (40, 1, 1152, 1280, 1, True)])
+def test_tokens(dtype, T, E, H, I, k, renorm):
+    check_tokens(T, E, H, I, k, dtype, renorm, T * 1000 + E + H + I)
+
+
+def test_tokens_repeats_and_other_streams():
+    """The same bits every time, on any stream, after another layer has used the workspace, and
+    from a captured graph."""
+    x, router, packed = layer(12, 16, 512, 384, torch.bfloat16, 3)
+    args = [x.to(DEV), router.to(DEV)] + [p[:2] for p in packed]
+    ws = torch.empty(moe.mx4_tokens_workspace_bytes(64, 16, 512, 384, 8, torch.bfloat16),
+                     dtype=torch.uint8, device=DEV)
+    want = moe.moe_mx4_forward_tokens(*args, top_k=4, ws=ws)
+    moe.moe_mx4_forward_tokens(*args, top_k=8, ws=ws)
+    for _ in range(20):
+        assert torch.equal(moe.moe_mx4_forward_tokens(*args, top_k=4, ws=ws), want)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = moe.moe_mx4_forward_tokens(*args, top_k=4, ws=ws, stream=side)
+    side.synchronize()
+    assert torch.equal(got, want)
+    out = torch.empty_like(want)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        moe.moe_mx4_forward_tokens(*args, top_k=4, ws=ws, out=out)
+    for _ in range(3):
+        out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_tokens_wide_range_of_values(dtype):
+    """Activations whose blocks span the type's range keep their 16 bits (no overflow in terms)."""
+    x, router, packed = layer(4, 4, 256, 256, dtype, 7)
+    rng = np.random.default_rng(8)
+    scale = np.exp2(rng.integers(-8, 9, (4, 8, 1)))
+    xs = torch.from_numpy(np64(x).reshape(4, 8, 32) * scale).reshape(4, 256).to(dtype)
+    xs[0, :32] = 0
+    xs[1, 5] = torch.finfo(dtype).smallest_normal
+    idx = torch.empty(4, 2, dtype=torch.uint32, device=DEV)
+    w = torch.empty(4, 2, dtype=torch.float32, device=DEV)
+    out = moe.moe_mx4_forward_tokens(xs.to(DEV), (router / 64).to(DEV), *[p[:2] for p in packed],
+                                     top_k=2, idx=idx, w=w)
+    ref, tol = tokens_reference(xs, router, packed, idx.view(torch.int32).cpu().numpy(), np64(w))
+    check_within(np64(out), ref, tol * (1 + torch.finfo(dtype).eps) + half_step(dtype, ref), dtype)
+
+
+def test_tokens_ties_and_bad_rows():
+    x, router, packed = layer(6, 8, 128, 128, torch.bfloat16, 11)
+    router[:] = router[0]                                   # every logit equal: lowest ids
+    x[2, 7], x[4, 100] = float("nan"), float("inf")
+    idx = torch.empty(6, 3, dtype=torch.uint32, device=DEV)
+    w = torch.empty(6, 3, dtype=torch.float32, device=DEV)
+    out = moe.moe_mx4_forward_tokens(x.to(DEV), router.to(DEV), *[p[:2] for p in packed], top_k=3,
+                                     idx=idx, w=w)
+    assert (idx.view(torch.int32).cpu().numpy() == [0, 1, 2]).all()
+    bad = np.array([False, False, True, False, True, False])
+    assert (np.isnan(np64(w)).all(-1) == bad).all()
+    assert (np.isnan(np64(out)).all(-1) == bad).all() and np.isfinite(np64(out)[~bad]).all()
+    assert np.allclose(np64(w)[~bad], 1 / 3, atol=1e-6)
+
+
+def test_tokens_none():
+    _, router, packed = layer(1, 4, 128, 128, torch.bfloat16, 2)
+    out = moe.moe_mx4_forward_tokens(torch.empty(0, 128, dtype=torch.bfloat16, device=DEV),
+                                     router.to(DEV), *[p[:2] for p in packed], top_k=2)
+    assert out.shape == (0, 128)
+
+
 # ----------------------------------------------------------------------------------- refusals
 def test_refusals():
     x = torch.zeros(4, 64, device=DEV)
@@ -328,3 +473,20 @@ def test_refusals():
         moe.moe_mx4_experts_forward_dispatched(x, off, w, w, w)
     with pytest.raises(moe.MoeError):
         moe.moe_mx4_product(c, s, *w, offsets=off, ws=torch.empty(64, dtype=torch.uint8, device=DEV))
+
+
+def test_tokens_refusals():
+    x, router, packed = layer(2, 4, 128, 128, torch.bfloat16, 2)
+    x, router, ws = x.to(DEV), router.to(DEV), [p[:2] for p in packed]
+    for bad in (dict(top_k=5), dict(top_k=0), dict(top_k=2, idx=torch.zeros(2, 2, device=DEV)),
+                dict(top_k=2, ws=torch.empty(256, dtype=torch.uint8, device=DEV))):
+        with pytest.raises(moe.MoeError):
+            moe.moe_mx4_forward_tokens(x, router, *ws, **bad)
+    with pytest.raises(moe.MoeError):
+        moe.moe_mx4_forward_tokens(x, router.half(), *ws, top_k=2)
+    with pytest.raises(moe.MoeError):
+        moe.moe_mx4_forward_tokens(x.float(), router.float(), *ws, top_k=2)
+    with pytest.raises(moe.MoeError):
+        moe.moe_mx4_forward_tokens(x.repeat(33, 1), router, *ws, top_k=2)
+    with pytest.raises(moe.MoeError):
+        moe.moe_mx4_forward_tokens(x, router[:3].contiguous(), *ws, top_k=2)

@@ -80,3 +80,26 @@ def test_experts_rejects(L):
     assert f(gs=FAKE + 2) == 4 and f(y=FAKE + 1) == 4
     assert f(wsb=need - 1) == 5 and f(ws=FAKE + 16) == 5
     assert f(rows=0, x=None, y=None, ws=None) == 0
+
+
+def test_tokens_rejects(L):
+    need = L.moe_mx4_tokens_workspace_bytes(8, 16, 256, 384, 4, BF16)
+    assert need > 256
+    assert L.moe_mx4_tokens_workspace_bytes(8, 16, 256, 384, 4, F32) == 0
+    assert L.moe_mx4_tokens_workspace_bytes(65, 16, 256, 384, 4, BF16) == 0
+
+    def f(x=FAKE, r=FAKE, dt=BF16, g=FAKE, gs=FAKE, T=8, E=16, H=256, I=384, k=4, out=FAKE,
+          idx=None, w=None, ws=FAKE, wsb=need):
+        return L.moe_mx4_forward_tokens(x, r, dt, g, gs, FAKE, FAKE, FAKE, FAKE, T, E, H, I, k, 1,
+                                        out, idx, w, ws, wsb, None)
+    assert f(dt=F32) == 3 and f(dt=7) == 3
+    for bad in (dict(T=-1), dict(T=65), dict(E=0), dict(E=1025), dict(k=0), dict(k=17),
+                dict(E=64, k=33), dict(T=64, k=17, E=64), dict(H=0), dict(I=0),
+                dict(E=1024, H=1 << 22)):
+        assert f(**bad) == 2, bad
+    assert f(H=192) == 4 and f(I=448) == 4 and f(x=FAKE + 8) == 4 and f(g=FAKE + 16) == 4
+    assert f(idx=FAKE + 2) == 4 and f(w=FAKE + 1) == 4
+    for k in ("x", "r", "g", "gs", "out"):
+        assert f(**{k: None}) == 1, k
+    assert f(ws=None) == 5 and f(wsb=need - 1) == 5 and f(ws=FAKE + 64) == 5
+    assert f(T=0, x=None, out=None, ws=None) == 0
