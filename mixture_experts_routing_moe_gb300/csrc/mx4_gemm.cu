@@ -7,10 +7,10 @@
 // A persistent kernel walks tiles (expert, m-tile, n-tile) of 256 columns and 128 rows (a CTA) or
 // 256 rows (a cluster of two CTAs, cta_group::2: each CTA holds 128 of the rows and half of the B
 // rows, so a tile pulls a third fewer bytes through L2).  Roles in each CTA:
-//   warp 0      one thread loads, for each 256-deep K slice, the codes of its A and B rows (128
+//   warp 0      one lane loads, for each 256-deep K slice, the codes of its A and B rows (128
 //               bytes a row) by TMA into a ring.  For gate/up the B tile holds gate rows 0-63, up
 //               rows 0-63, gate rows 64-127, up rows 64-127 of 128 columns of a.
-//   warp 1      one thread (of CTA 0) copies each slice's scales to tensor memory and issues its
+//   warp 1      one lane (of CTA 0) copies each slice's scales to tensor memory and issues its
 //               four K = 64 MMAs (N = 256); tcgen05.commit frees the slot.
 //   warps 4-6   scales of A and of the two halves of B: each lane holds 32 bytes (four slices) of
 //               four rows in registers, loads the next 32 ahead, and writes each slice's words to
@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp < 4) {
     set_max_regs_dec<kRegsIssue>();
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
       int stage = 0, armed = 0;
       uint32_t phase = 0;
       bool stop = false;
@@ -206,26 +206,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int b_row = x.e * p.N + x.n * (GATEUP ? BN / 2 : BN) +
                           rank * (GATEUP ? BN / 4 : BN / 2);
         for (int kb = 0; kb < p.KB; ++kb) {
-          if (!wait_bounded(empty_bar(stage), phase ^ 1u, abort_f, p.status)) {
+          if (!__all_sync(0xFFFFFFFFu,
+                          wait_bounded(empty_bar(stage), phase ^ 1u, abort_f, p.status))) {
             stop = true;
             break;
           }
           const uint32_t sa = base + stage * STAGE_BYTES, sb = sa + S::A_BYTES;
-          if (leader) mbar_expect_tx(full_bar(stage), CG * STAGE_BYTES);
           const uint32_t fb = CG == 2 ? map_to_rank(full_bar(stage), 0) : full_bar(stage);
           auto load = [&](uint32_t dst, const CUtensorMap* m, int row) {
             if (CG == 2) tma_load_2d_pair(dst, m, fb, kb * 128, row, pol);
             else tma_load_2d(dst, m, fb, kb * 128, row, pol);
           };
-          load(sa, &mapA, x.r0);
-          if (GATEUP) {
+          if (elect_one()) {
+            if (leader) mbar_expect_tx(full_bar(stage), CG * STAGE_BYTES);
+            load(sa, &mapA, x.r0);
+            if (GATEUP) {
 #pragma unroll
-            for (int h = 0; h < 2 / CG; ++h) {
-              load(sb + h * 128 * 128, &mapB, b_row + h * 64);
-              load(sb + h * 128 * 128 + 64 * 128, &mapB2, b_row + h * 64);
+              for (int h = 0; h < 2 / CG; ++h) {
+                load(sb + h * 128 * 128, &mapB, b_row + h * 64);
+                load(sb + h * 128 * 128 + 64 * 128, &mapB2, b_row + h * 64);
+              }
+            } else {
+              load(sb, &mapB, b_row);
             }
-          } else {
-            load(sb, &mapB, b_row);
           }
           ++armed;
           if (++stage == STAGES) {
@@ -234,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (*abort_f && leader) {  // let copies still in flight land
+      if (stop && leader) {  // let copies still in flight land
         for (int i = 0; i < min(armed, STAGES); ++i) {
           if (stage == 0) {
             stage = STAGES - 1;
@@ -246,12 +249,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-    if (warp == 1 && leader && lane == 0) {
+    if (warp == 1 && leader) {
       constexpr uint32_t idesc0 = make_idesc_mxf4(BM * CG, BN, 0);
       constexpr uint32_t idesc2 = make_idesc_mxf4(BM * CG, BN, 2);
       auto wait = [&](uint32_t bar, uint32_t parity) {
-        return CG == 2 ? wait_bounded_cluster(bar, parity, abort_f, p.status)
-                       : wait_bounded(bar, parity, abort_f, p.status);
+        return __all_sync(0xFFFFFFFFu, CG == 2
+                                           ? wait_bounded_cluster(bar, parity, abort_f, p.status)
+                                           : wait_bounded(bar, parity, abort_f, p.status));
       };
       auto copy = [&](uint32_t taddr, uint32_t chunk) {
         if (CG == 2) tmem_cp_scale2(taddr, make_sdesc_scale(chunk));
@@ -276,33 +280,39 @@ __global__ void __launch_bounds__(kThreads, 1)
           // a slot of columns for each stage, so that the copies need not wait for the MMAs of the
           // slice before: 128 values (c) take 4 columns for A and 8 for the two halves of B
           const uint32_t cols = tmem + kScaleCol + stage * 24;
+          if (elect_one()) {
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            copy(cols + c * 12, sf + c * kScaleChunk);
-            copy(cols + c * 12 + 4, sf + (2 + 2 * c) * kScaleChunk);
-            copy(cols + c * 12 + 8, sf + (3 + 2 * c) * kScaleChunk);
-          }
+            for (int c = 0; c < 2; ++c) {
+              copy(cols + c * 12, sf + c * kScaleChunk);
+              copy(cols + c * 12 + 4, sf + (2 + 2 * c) * kScaleChunk);
+              copy(cols + c * 12 + 8, sf + (3 + 2 * c) * kScaleChunk);
+            }
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t ca = cols + (k >> 1) * 12, cb = ca + 4;
-            const uint32_t idesc = (k & 1) ? idesc2 : idesc0, more = (kb | k) != 0;
-            if (CG == 2) umma2_mxf4(tmem, da + 2u * k, db + 2u * k, idesc, ca, cb, more);
-            else umma_mxf4(tmem, da + 2u * k, db + 2u * k, idesc, ca, cb, more);
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t ca = cols + (k >> 1) * 12, cb = ca + 4;
+              const uint32_t idesc = (k & 1) ? idesc2 : idesc0, more = (kb | k) != 0;
+              if (CG == 2) umma2_mxf4(tmem, da + 2u * k, db + 2u * k, idesc, ca, cb, more);
+              else umma_mxf4(tmem, da + 2u * k, db + 2u * k, idesc, ca, cb, more);
+            }
+            if (CG == 2) umma_commit2(empty_bar(stage), 0x3);
+            else umma_commit(empty_bar(stage));
           }
-          if (CG == 2) umma_commit2(empty_bar(stage), 0x3);
-          else umma_commit(empty_bar(stage));
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;
           }
         }
         if (stop) break;
-        if (CG == 2) umma_commit2(tfull, 0x3);
-        else umma_commit(tfull);
+        if (elect_one()) {
+          if (CG == 2) umma_commit2(tfull, 0x3);
+          else umma_commit(tfull);
+        }
       }
       // arrives once every MMA issued above has completed
-      if (CG == 2) umma_commit2(drain_bar, 0x1);
-      else umma_commit(drain_bar);
+      if (elect_one()) {
+        if (CG == 2) umma_commit2(drain_bar, 0x1);
+        else umma_commit(drain_bar);
+      }
       wait_drain(drain_bar, 0);
     }
   } else if (warp < 8) {

@@ -15,6 +15,17 @@
 namespace moe {
 namespace tc {
 
+// One lane of a converged warp.  Roles that issue tensor or TMA instructions run their loops with
+// the whole warp and predicate the instructions on this: descriptors and addresses then stay in
+// uniform registers, where a loop of one lane has to move each of them there.
+static __device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
 constexpr int kScaleChunk = 512;  // bytes: 128 rows x 4 blocks
 
 // Byte offset in a chunk of row r's four scales.

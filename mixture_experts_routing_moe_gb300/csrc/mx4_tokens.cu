@@ -19,18 +19,18 @@
 //   0  every CTA splits its share of x into terms (xq, xs) and computes the logits of its experts;
 //      grid barrier.
 //   1  every CTA selects the top-k of all tokens for itself (the same arithmetic everywhere) and
-//      lists the active experts' tokens in shared memory.
-//   2  units of work: (expert, group of tokens, 64 columns of a) for gate/up, then (expert, group,
-//      128 columns of the output) for down, dealt to the CTAs in turn.  Warp roles as in the
-//      grouped products: weight codes (TMA), token terms (TMA), weight scales, token scales, MMA,
-//      epilogue.  The gate/up epilogue writes a as terms (aq, as) and counts the unit on its
-//      expert; a down unit's weights are loaded ahead, its tokens once that count is full.  The
-//      weight loads never wait for anything but a free slot, from the first unit to the last.
-//   3  the down epilogue writes y (FP32, one row a slot); whoever finishes the last unit of an
-//      output tile adds the slots up in the order j = 0 .. k - 1 and writes out.
+//      lists the active experts' tokens in shared memory, expert by expert.
+//   2  units of work: (expert, 64 columns of a) for gate/up, then (expert, 128 columns of the
+//      output, part of K) for down, dealt to the CTAs in turn.  Warp roles as in the grouped
+//      products: weight codes (TMA), token terms (TMA), weight scales, token scales, MMA, epilogue,
+//      in slices of K = 256.  The gate/up epilogue writes a as terms (aq, as; rows in the order of
+//      the lists) and counts the unit on its expert; a down unit's weights are loaded ahead, its
+//      tokens once that count is full.  The weight loads never wait for anything but a free slot,
+//      from the first unit to the last.
+//   3  the down epilogue writes y (FP32, one row a slot and part); whoever finishes the last unit
+//      of an output tile adds parts and slots up in order and writes out.
 // Waits are bounded; on expiry the status word records the timeout and every role leaves.
-#include <atomic>
-
+//
 #include "launch.h"
 #include "mx4.cuh"
 #include "mx4_mma.cuh"
@@ -43,16 +43,20 @@ using namespace tc;
 using namespace mx4;
 
 constexpr int kThreads = 384, kWarps = kThreads / 32;
-constexpr int kA = 128 * 128;          // bytes of a stage's weights, widened
-constexpr int kMaxStages = 12;
-constexpr int kBarBytes = 512;
-constexpr uint32_t kTmemCols = 512, kScaleCol = 256;
+constexpr int kA = 128 * 128;      // bytes of 128 x 128 weights, widened; a stage has two
+constexpr int kMaxStages = 5;
+constexpr int kMaxN = 192;         // columns of a unit: 64 tokens x 3 terms
+constexpr int kBox = 16;           // rows of token terms a TMA box
+constexpr int kBarBytes = 256;
+// two accumulators, then the scales of each stage: 2 x 4 columns for A, 2 x 8 for B
+constexpr uint32_t kTmemCols = 512, kScaleCol = 2 * kMaxN;
+static_assert(kScaleCol + kMaxStages * 24 <= kTmemCols, "tensor memory");
 constexpr int kExchange = 16 * 64 * 4;  // u of up to 16 tokens x 64 columns
 
-// terms of a token value, columns between two tokens, tokens of a group (N <= 128)
+// terms of a token value
 template <typename T> struct Terms;
-template <> struct Terms<__nv_bfloat16> { static constexpr int P = 2, STRIDE = 2, G = 64; };
-template <> struct Terms<__half> { static constexpr int P = 3, STRIDE = 4, G = 32; };
+template <> struct Terms<__nv_bfloat16> { static constexpr int P = 2; };
+template <> struct Terms<__half> { static constexpr int P = 3; };
 
 struct TokensParams {
   const void* x;
@@ -67,7 +71,8 @@ struct TokensParams {
   void* out;
   uint32_t* idx;
   float* w;
-  int stages, stage_bytes;  // ring
+  int splits;        // parts of K a down unit is cut into
+  int stages, ncap;  // ring: slices, columns of its token tiles
 };
 
 __device__ __forceinline__ unsigned ld_acquire_u32(const unsigned* p) {
@@ -181,15 +186,20 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads, 1)
     moe_mx4_tokens(const __grid_constant__ CUtensorMap mapG, const __grid_constant__ CUtensorMap mapU,
                    const __grid_constant__ CUtensorMap mapD,
+                   const __grid_constant__ CUtensorMap mapX1,
                    const __grid_constant__ CUtensorMap mapX,
                    const __grid_constant__ CUtensorMap mapA, const TokensParams p) {
-  constexpr int P = Terms<T>::P, STRIDE = Terms<T>::STRIDE, G = Terms<T>::G;
+  constexpr int P = Terms<T>::P;
   extern __shared__ uint8_t mx4_smem_raw[];
   const uint32_t raw = smem_u32(mx4_smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
-  uint8_t* at = mx4_smem_raw + (base - raw) + p.stages * p.stage_bytes;
-  const uint32_t sf_base = smem_u32(at);  // a stage's scales: one chunk of A, one of B
-  at += p.stages * 2 * kScaleChunk;
+  const int b_half = p.ncap * 128;               // bytes of 128-deep token terms
+  const int stage_bytes = 2 * kA + 2 * b_half;
+  const int b_chunks = p.ncap > 128 ? 2 : 1;     // scale chunks of 128-deep token terms
+  const int sf_bytes = (2 + 2 * b_chunks) * kScaleChunk;
+  uint8_t* at = mx4_smem_raw + (base - raw) + p.stages * stage_bytes;
+  const uint32_t sf_base = smem_u32(at);  // a stage's scales: two chunks of A, then those of B
+  at += p.stages * sf_bytes;
   uint64_t* bars = reinterpret_cast<uint64_t*>(at);
   at += kBarBytes;
   float* exchange = reinterpret_cast<float*>(at);
@@ -198,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   at += p.E * 8;
   int* start = reinterpret_cast<int*>(at);  // first entry of an expert's tokens in `list`
   at += (p.E + 1) * 4;
-  int* gpref = reinterpret_cast<int*>(at);  // groups of tokens before an expert
+  int* act = reinterpret_cast<int*>(at);  // the experts that have tokens, ascending
   at += (p.E + 1) * 4;
   const int R = p.T * p.k;
   float* sel_w = reinterpret_cast<float*>(at);
@@ -216,8 +226,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kMaxStages + 5);
   volatile int* abort_f = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* last_s = reinterpret_cast<int*>(tmem_slot + 2);
+  int* active_s = reinterpret_cast<int*>(tmem_slot + 3);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s) {
       mbar_init(full_bar(s), 4);  // weights, tokens, weight scales, token scales
@@ -229,10 +240,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(drain_bar, 1);
     *abort_f = 0;
+    *active_s = 0;
     fence_mbar_init();
     tma_prefetch(&mapG);
     tma_prefetch(&mapU);
     tma_prefetch(&mapD);
+    tma_prefetch(&mapX1);
     tma_prefetch(&mapX);
     tma_prefetch(&mapA);
   }
@@ -250,38 +263,53 @@ __global__ void __launch_bounds__(kThreads, 1)
       write_terms<P>(v, p.xq + (int64_t)t * P * p.H + c * 32 + lane, p.H,
                      p.xs + (int64_t)t * P * hb + c, hb, lane);
     }
-    constexpr int TB = 4;  // tokens at a time
-    for (int e = blockIdx.x; e < p.E; e += gridDim.x) {
+    // two experts and four tokens at a time: eight sums from six 16-byte loads
+    constexpr int TB = 4, EB = 2;
+    for (int e = blockIdx.x; e < p.E; e += EB * gridDim.x) {
+      const int e1 = min(e + (int)gridDim.x, p.E - 1);
+      const T* r0 = router + (int64_t)e * p.H;
+      const T* r1 = router + (int64_t)e1 * p.H;
       for (int t0 = 0; t0 < p.T; t0 += TB) {
-        float acc[TB] = {};
+        float acc[EB][TB] = {};
+        const T* xt[TB];
+#pragma unroll
+        for (int i = 0; i < TB; ++i) xt[i] = x + (int64_t)min(t0 + i, p.T - 1) * p.H;
+#pragma unroll 3
         for (int v = threadIdx.x; v < p.H / 8; v += kThreads) {
-          Vec16<T> r;
-          r.u = ld_nc_v4(router + (int64_t)e * p.H + v * 8);
-          float rf[8];
-          r.to_float(rf);
+          Vec16<T> a, b, q[TB];
+          a.u = ld_nc_v4(r0 + v * 8);
+          b.u = ld_nc_v4(r1 + v * 8);
+#pragma unroll
+          for (int i = 0; i < TB; ++i) q[i].u = ld_nc_v4(xt[i] + v * 8);
+          float af[8], bf[8];
+          a.to_float(af);
+          b.to_float(bf);
 #pragma unroll
           for (int i = 0; i < TB; ++i) {
-            if (t0 + i < p.T) {
-              Vec16<T> q;
-              q.u = ld_nc_v4(x + (int64_t)(t0 + i) * p.H + v * 8);
-              float xf[8];
-              q.to_float(xf);
+            float xf[8];
+            q[i].to_float(xf);
 #pragma unroll
-              for (int z = 0; z < 8; ++z) acc[i] = fmaf(xf[z], rf[z], acc[i]);
+            for (int z = 0; z < 8; ++z) {
+              acc[0][i] = fmaf(xf[z], af[z], acc[0][i]);
+              acc[1][i] = fmaf(xf[z], bf[z], acc[1][i]);
             }
           }
         }
 #pragma unroll
         for (int i = 0; i < TB; ++i) {
-          const float s = group_sum<32>(acc[i]);
-          if (lane == 0) red[(t0 + i) * kWarps + warp] = s;
+          const float s0 = group_sum<32>(acc[0][i]), s1 = group_sum<32>(acc[1][i]);
+          if (lane == 0) {
+            red[(t0 + i) * kWarps + warp] = s0;
+            red[(64 + t0 + i) * kWarps + warp] = s1;
+          }
         }
       }
       __syncthreads();
-      if (threadIdx.x < p.T) {
+      const int z = threadIdx.x >> 6, t = threadIdx.x & 63;  // expert of the two, token
+      if (z < EB && t < p.T && e + z * (int)gridDim.x < p.E) {
         float s = 0.f;
-        for (int w = 0; w < kWarps; ++w) s += red[threadIdx.x * kWarps + w];
-        p.logits[(int64_t)threadIdx.x * p.E + e] = s;
+        for (int w = 0; w < kWarps; ++w) s += red[(z * 64 + t) * kWarps + w];
+        p.logits[(int64_t)t * p.E + e + z * gridDim.x] = s;
       }
       __syncthreads();
     }
@@ -300,7 +328,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
 
   // ------------------------------------------------ 1. top-k, lists of the experts' tokens
-  if (!*abort_f) {
+  const bool go = !*abort_f;
+  if (go) {
     for (int t = warp; t < p.T; t += kWarps) {
       const float* row = p.logits + (int64_t)t * p.E;
       uint16_t* ids = sel_id + t * p.k;
@@ -320,24 +349,26 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncthreads();
   if (warp == 0) {
-    int carry = 0, gcarry = 0;
+    int carry = 0, n_act = 0;
     for (int e0 = 0; e0 < p.E; e0 += 32) {
       const int e = e0 + lane;
-      const int n = e < p.E ? __popcll(mask[e]) : 0, g = (n + G - 1) / G;
-      int s = n, sg = g;
+      const int n = e < p.E ? __popcll(mask[e]) : 0;
+      int s = n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xFFFFFFFFu, s, o), yg = __shfl_up_sync(0xFFFFFFFFu, sg, o);
-        if (lane >= o) s += y, sg += yg;
+        const int y = __shfl_up_sync(0xFFFFFFFFu, s, o);
+        if (lane >= o) s += y;
       }
-      if (e < p.E) start[e] = carry + s - n, gpref[e] = gcarry + sg - g;
+      if (e < p.E) start[e] = carry + s - n;
       carry += __shfl_sync(0xFFFFFFFFu, s, 31);
-      gcarry += __shfl_sync(0xFFFFFFFFu, sg, 31);
+      const unsigned has = __ballot_sync(0xFFFFFFFFu, n > 0);
+      if (n > 0) act[n_act + __popc(has & ((1u << lane) - 1))] = e;
+      n_act += __popc(has);
     }
-    if (lane == 0) start[p.E] = carry, gpref[p.E] = gcarry;
+    if (lane == 0) start[p.E] = carry, *active_s = n_act;
   }
   __syncthreads();
-  if (!*abort_f) {
+  if (go) {
     for (int s = threadIdx.x; s < R; s += kThreads) {
       const int e = sel_id[s], t = s / p.k;
       list[start[e] + __popcll(mask[e] & ((1ull << t) - 1))] = (uint16_t)s;
@@ -347,101 +378,131 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // ------------------------------------------------ 2. units
   const int NI = p.I / 64, NH = p.H / 128;
-  const int groups = *abort_f ? 0 : gpref[p.E];
-  const int n1 = groups * NI, total = n1 + groups * NH;
+  const int active = go ? *active_s : 0;
+  const int n1 = active * NI, per_down = NH * p.splits, total = n1 + active * per_down;
   struct Unit {
     bool down;
-    int e, eg, tile;    // expert, group (over all experts), column tile
-    int first, n;       // its tokens: list[first .. first + n)
-    int KB;             // 128-deep slices
+    int e, ai;        // expert, its place among the active ones
+    int tile, split;  // column tile, part of K
+    int first, n;     // its tokens: list[first .. first + n)
+    int k0, k1;       // 128-deep pieces of K
+    // gate/up of an expert that takes many of the tokens multiplies all T of them (their terms
+    // are contiguous); otherwise each token's terms are loaded on their own
+    bool all;
+    int cols;         // columns in use
   };
   auto unit_of = [&](int u) {
     Unit r;
     r.down = u >= n1;
-    const int v = r.down ? u - n1 : u, NT = r.down ? NH : NI;
-    r.eg = v / NT;
-    r.tile = v - r.eg * NT;
-    r.e = find_expert(gpref, p.E, r.eg);
-    r.first = start[r.e] + (r.eg - gpref[r.e]) * G;
-    r.n = min(start[r.e + 1] - r.first, G);
-    r.KB = (r.down ? p.I : p.H) / 128;
+    const int v = r.down ? u - n1 : u, per = r.down ? per_down : NI;
+    r.ai = v / per;
+    const int w = v - r.ai * per;
+    r.tile = r.down ? w / p.splits : w;
+    r.split = r.down ? w - r.tile * p.splits : 0;
+    r.e = act[r.ai];
+    r.first = start[r.e];
+    r.n = start[r.e + 1] - r.first;
+    const int pieces = (r.down ? p.I : p.H) / 128;
+    r.k0 = r.down ? (int)((int64_t)pieces * r.split / p.splits) : 0;
+    r.k1 = r.down ? (int)((int64_t)pieces * (r.split + 1) / p.splits) : pieces;
+    r.all = !r.down && r.n * 8 >= p.T;
+    r.cols = (r.all ? p.T : r.n) * P;
     return r;
   };
-  auto columns = [&](int n) { return (n * STRIDE + 15) / 16 * 16; };  // N of a unit
 
   if (warp == 0) {
-    if (lane == 0) {
-      // -------------------------------------------------------------- weight codes
-      int stage = 0;
-      uint32_t phase = 0;
-      bool stop = false;
-      const uint64_t pol = policy_evict_normal();
-      for (int u = blockIdx.x; u < total && !stop; u += gridDim.x) {
-        const Unit r = unit_of(u);
-        for (int kb = 0; kb < r.KB; ++kb) {
-          if (!wait_bounded(empty_bar(stage), phase ^ 1u, abort_f, p.status)) {
-            stop = true;
-            break;
-          }
-          const uint32_t sa = base + stage * p.stage_bytes, fb = full_bar(stage);
-          mbar_expect_tx(fb, kA / 2);  // counted in packed bytes, not in the widened ones
+    // ---------------------------------------------------------------- weight codes
+    int stage = 0;
+    uint32_t phase = 0;
+    bool stop = false;
+    const uint64_t pol = policy_evict_normal();
+    for (int u = blockIdx.x; u < total && !stop; u += gridDim.x) {
+      const Unit r = unit_of(u);
+      const int row = r.down ? r.e * p.H + r.tile * 128 : r.e * p.I + r.tile * 64;
+      for (int k = r.k0; k < r.k1; k += 2) {
+        if (!__all_sync(0xFFFFFFFFu,
+                        wait_bounded(empty_bar(stage), phase ^ 1u, abort_f, p.status))) {
+          stop = true;
+          break;
+        }
+        const int halves = min(2, r.k1 - k);
+        const uint32_t sa = base + stage * stage_bytes, fb = full_bar(stage);
+        if (elect_one()) {
+          mbar_expect_tx(fb, halves * (kA / 2));  // counted in packed bytes, not the widened ones
           if (r.down) {
-            tma_load_2d(sa, &mapD, fb, kb * 128, r.e * p.H + r.tile * 128, pol);
+            tma_load_2d(sa, &mapD, fb, k * 128, row, pol);
+            if (halves == 2) tma_load_2d(sa + kA, &mapD, fb, k * 128 + 128, row, pol);
           } else {
-            tma_load_2d(sa, &mapG, fb, kb * 128, r.e * p.I + r.tile * 64, pol);
-            tma_load_2d(sa + kA / 2, &mapU, fb, kb * 128, r.e * p.I + r.tile * 64, pol);
+            tma_load_2d(sa, &mapG, fb, k * 128, row, pol);
+            tma_load_2d(sa + kA / 2, &mapU, fb, k * 128, row, pol);
+            if (halves == 2) {
+              tma_load_2d(sa + kA, &mapG, fb, k * 128 + 128, row, pol);
+              tma_load_2d(sa + kA + kA / 2, &mapU, fb, k * 128 + 128, row, pol);
+            }
           }
-          if (++stage == p.stages) {
-            stage = 0;
-            phase ^= 1u;
-          }
+        }
+        if (++stage == p.stages) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      // -------------------------------------------------------------- MMA
-      int stage = 0, acc = 0;
-      uint32_t phase = 0, acc_phase = 0;
-      bool stop = false;
-      for (int u = blockIdx.x; u < total && !stop; u += gridDim.x) {
-        const Unit r = unit_of(u);
-        const int N = columns(r.n);
-        if (!wait_bounded(tempty_bar(acc), acc_phase ^ 1u, abort_f, p.status)) break;
-        tc_fence_after();
-        const uint32_t d = tmem + acc * 128;
-        for (int kb = 0; kb < r.KB; ++kb) {
-          if (!wait_bounded(full_bar(stage), phase, abort_f, p.status)) {
-            stop = true;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t sa = base + stage * p.stage_bytes;
-          const uint32_t sf = sf_base + stage * 2 * kScaleChunk;
-          const uint32_t cols = tmem + kScaleCol + stage * 8;
-          const uint64_t da = make_sdesc(sa), db = make_sdesc(sa + kA);
-          tmem_cp_scale(cols, make_sdesc_scale(sf));
-          tmem_cp_scale(cols + 4, make_sdesc_scale(sf + kScaleChunk));
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            umma_mxf8f6f4(d, da + 2u * kk, db + 2u * kk, make_idesc_mxf4_f8(128, N, kk), cols,
-                          cols + 4, (kb | kk) != 0);
-          umma_commit(empty_bar(stage));
-          if (++stage == p.stages) {
-            stage = 0;
-            phase ^= 1u;
-          }
+    // ---------------------------------------------------------------- MMA
+    int stage = 0, acc = 0;
+    uint32_t phase = 0, acc_phase = 0;
+    bool stop = false;
+    for (int u = blockIdx.x; u < total && !stop; u += gridDim.x) {
+      const Unit r = unit_of(u);
+      const uint32_t idesc = make_idesc_mxf4_f8(128, (r.cols + 15) / 16 * 16, 0);
+      if (!__all_sync(0xFFFFFFFFu,
+                      wait_bounded(tempty_bar(acc), acc_phase ^ 1u, abort_f, p.status)))
+        break;
+      tc_fence_after();
+      const uint32_t d = tmem + acc * kMaxN;
+      for (int k = r.k0; k < r.k1; k += 2) {
+        if (!__all_sync(0xFFFFFFFFu, wait_bounded(full_bar(stage), phase, abort_f, p.status))) {
+          stop = true;
+          break;
         }
-        if (stop) break;
-        umma_commit(tfull_bar(acc));
-        acc ^= 1;
-        if (acc == 0) acc_phase ^= 1u;
+        tc_fence_after();
+        const uint32_t sa = base + stage * stage_bytes, sb = sa + 2 * kA;
+        const uint32_t sf = sf_base + stage * sf_bytes, sfb = sf + 2 * kScaleChunk;
+        const uint32_t cols = tmem + kScaleCol + stage * 24;
+        const int halves = min(2, r.k1 - k);
+        if (elect_one()) {
+          for (int h = 0; h < halves; ++h) {
+            const uint32_t ca = cols + h * 12, cb = ca + 4;
+            tmem_cp_scale(ca, make_sdesc_scale(sf + h * kScaleChunk));
+            tmem_cp_scale(cb, make_sdesc_scale(sfb + h * b_chunks * kScaleChunk));
+            if (b_chunks == 2)
+              tmem_cp_scale(cb + 4, make_sdesc_scale(sfb + (2 * h + 1) * kScaleChunk));
+          }
+          for (int h = 0; h < halves; ++h) {
+            const uint32_t ca = cols + h * 12, cb = ca + 4;
+            const uint64_t da = make_sdesc(sa + h * kA), db = make_sdesc(sb + h * b_half);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)  // the scale ids of A and B are kk
+              umma_mxf8f6f4(d, da + 2u * kk, db + 2u * kk,
+                            idesc | ((uint32_t)kk << 4) | ((uint32_t)kk << 29), ca, cb,
+                            k != r.k0 || h != 0 || kk != 0);
+          }
+          umma_commit(empty_bar(stage));
+        }
+        if (++stage == p.stages) {
+          stage = 0;
+          phase ^= 1u;
+        }
       }
-      umma_commit(drain_bar);
-      wait_drain(drain_bar, 0);
+      if (stop) break;
+      if (elect_one()) umma_commit(tfull_bar(acc));
+      acc ^= 1;
+      if (acc == 0) acc_phase ^= 1u;
     }
+    if (elect_one()) umma_commit(drain_bar);  // arrives once every MMA issued above has completed
+    wait_drain(drain_bar, 0);
   } else if (warp == 2) {
-    // -------------------------------------------------------------- token terms
+    // ---------------------------------------------------------------- token terms
     int stage = 0, armed = 0;
     uint32_t phase = 0;
     bool stop = false;
@@ -451,23 +512,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Unit r = unit_of(u);
       if (r.down) {
         bool ok = true;
-        if (lane == 0) ok = wait_count(p.ready + r.eg, NI, abort_f, p.status);
-        if (!__all_sync(0xFFFFFFFFu, ok)) break;
+        if (lane == 0) ok = wait_count(p.ready + r.ai, NI, abort_f, p.status);
+        if (!__all_sync(0xFFFFFFFFu, ok)) {
+          stop = true;
+          break;
+        }
         fence_proxy_async_all();
       }
-      for (int kb = 0; kb < r.KB; ++kb) {
+      const bool whole = r.down || r.all;                // contiguous rows, boxes of 16
+      const int boxes = whole ? (r.cols + kBox - 1) / kBox : r.n;
+      const int bytes = whole ? kBox * 128 : P * 128;    // of a box
+      const int row0 = r.down ? r.first * P : 0;
+      for (int k = r.k0; k < r.k1; k += 2) {
         if (!__all_sync(0xFFFFFFFFu,
                         wait_bounded(empty_bar(stage), phase ^ 1u, abort_f, p.status))) {
           stop = true;
           break;
         }
-        const uint32_t sb = base + stage * p.stage_bytes + kA, fb = full_bar(stage);
-        if (lane == 0) mbar_expect_tx(fb, r.n * P * 128);
+        const int halves = min(2, r.k1 - k);
+        const uint32_t sb = base + stage * stage_bytes + 2 * kA, fb = full_bar(stage);
+        if (elect_one()) mbar_expect_tx(fb, halves * boxes * bytes);
         __syncwarp();
-        for (int i = lane; i < r.n; i += 32) {
-          const int slot = list[r.first + i];
-          tma_load_2d(sb + i * STRIDE * 128, r.down ? &mapA : &mapX, fb, kb * 128,
-                      (r.down ? slot : slot / p.k) * P, pol);
+        for (int i = 0; i < boxes; ++i) {
+          const int row = whole ? row0 + i * kBox : (int)list[r.first + i] / p.k * P;
+          if (elect_one()) {
+            const CUtensorMap* m = r.down ? &mapA : r.all ? &mapX : &mapX1;
+            tma_load_2d(sb + i * bytes, m, fb, k * 128, row, pol);
+            if (halves == 2) tma_load_2d(sb + b_half + i * bytes, m, fb, k * 128 + 128, row, pol);
+          }
         }
         ++armed;
         if (++stage == p.stages) {
@@ -476,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-    if (*abort_f && lane == 0) {  // let copies still in flight land
+    if (stop) {  // let copies still in flight land
       for (int i = 0; i < min(armed, p.stages); ++i) {
         if (stage == 0) {
           stage = p.stages - 1;
@@ -488,29 +560,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == 4) {
-    // -------------------------------------------------------------- weight scales
-    // lane l holds rows l, l + 32, l + 64, l + 96 of the unit's 128, eight slices (32 bytes) each
+    // ---------------------------------------------------------------- weight scales
+    // lane l holds rows l, l + 32, l + 64, l + 96 of the unit's 128, eight pieces (32 bytes) each
     int stage = 0;
     uint32_t phase = 0;
     bool stop = false;
     uint32_t next[4][8];
     auto load = [&](int u, int part) {
       const Unit r = unit_of(u);
-      const int pitch = r.KB * 4;
-      const bool vec = p.scales_vec && (pitch & 15) == 0;
+      const int pitch = (r.down ? p.I : p.H) / 32;
+      const int at0 = r.k0 * 4 + part * 32, left = r.k1 * 4 - at0;
+      const bool vec = p.scales_vec && ((pitch | at0) & 15) == 0;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const uint8_t* src =
             r.down ? p.ds + ((int64_t)r.e * p.H + r.tile * 128 + 32 * j + lane) * pitch
                    : (j < 2 ? p.gs : p.us) +
                          ((int64_t)r.e * p.I + r.tile * 64 + 32 * (j & 1) + lane) * pitch;
-        src += part * 32;
-        const int left = pitch - part * 32;
+        src += at0;
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
-          if (vec) {
-            uint4 q = make_uint4(0, 0, 0, 0);
-            if (16 * z < left) q = ld_nc_v4(src + 16 * z);
+          if (vec && 16 * z + 16 <= left) {
+            const uint4 q = ld_nc_v4(src + 16 * z);
             next[j][4 * z] = q.x, next[j][4 * z + 1] = q.y;
             next[j][4 * z + 2] = q.z, next[j][4 * z + 3] = q.w;
           } else {
@@ -524,7 +595,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     if (blockIdx.x < total) load(blockIdx.x, 0);
     for (int u = blockIdx.x; u < total && !stop; u += gridDim.x) {
-      const int KB = unit_of(u).KB, parts = (KB + 7) / 8;
+      const Unit r = unit_of(u);
+      const int pieces = r.k1 - r.k0, parts = (pieces + 7) / 8;
       for (int part = 0; part < parts && !stop; ++part) {
         uint32_t now[4][8];
 #pragma unroll
@@ -534,18 +606,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (part + 1 < parts) load(u, part + 1);
         else if (u + (int)gridDim.x < total) load(u + gridDim.x, 0);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (part * 8 + i >= KB || stop) continue;
+        for (int i = 0; i < 8; i += 2) {
+          if (part * 8 + i >= pieces || stop) continue;
           if (!__all_sync(0xFFFFFFFFu,
                           wait_bounded(empty_bar(stage), phase ^ 1u, abort_f, p.status))) {
             stop = true;
             continue;
           }
-          st_shared_v4(sf_base + stage * 2 * kScaleChunk + lane * 16, now[0][i], now[1][i],
-                       now[2][i], now[3][i]);
+          const uint32_t sf = sf_base + stage * sf_bytes + lane * 16;
+          st_shared_v4(sf, now[0][i], now[1][i], now[2][i], now[3][i]);
+          st_shared_v4(sf + kScaleChunk, now[0][i + 1], now[1][i + 1], now[2][i + 1],
+                       now[3][i + 1]);
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(full_bar(stage));
+          if (elect_one()) mbar_arrive(full_bar(stage));
           if (++stage == p.stages) {
             stage = 0;
             phase ^= 1u;
@@ -554,8 +628,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == 5) {
-    // -------------------------------------------------------------- token scales
-    // lane l holds the terms in columns l, l + 32, l + 64, l + 96, four slices each
+    // ---------------------------------------------------------------- token scales
+    // lane l holds the terms in columns l, l + 32, ..., l + 160, four pieces of K each
+    constexpr int J = kMaxN / 32;
     int stage = 0;
     uint32_t phase = 0;
     bool stop = false;
@@ -563,51 +638,58 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Unit r = unit_of(u);
       if (r.down) {
         bool ok = true;
-        if (lane == 0) ok = wait_count(p.ready + r.eg, NI, abort_f, p.status);
+        if (lane == 0) ok = wait_count(p.ready + r.ai, NI, abort_f, p.status);
         if (!__all_sync(0xFFFFFFFFu, ok)) break;
       }
-      const int pitch = r.KB * 4;
-      const uint8_t* src[4];
+      const int pitch = (r.down ? p.I : p.H) / 32;
+      const uint8_t* src[J];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int c = 32 * j + lane, i = c / STRIDE, term = c % STRIDE;
+      for (int j = 0; j < J; ++j) {
+        const int c = 32 * j + lane;
         src[j] = nullptr;
-        if (i < r.n && term < P) {
-          const int slot = list[r.first + i];
-          src[j] = r.down ? p.as + ((int64_t)slot * P + term) * pitch
-                          : p.xs + ((int64_t)(slot / p.k) * P + term) * pitch;
+        if (c < r.cols) {
+          const int i = c / P, term = c - i * P;
+          const int row = r.down ? (r.first + i) * P + term
+                                 : (r.all ? i : (int)list[r.first + i] / p.k) * P + term;
+          src[j] = (r.down ? p.as : p.xs) + (int64_t)row * pitch;
         }
       }
-      uint32_t next[4][4];
-      auto load = [&](int quad) {
+      uint32_t next[J][4];
+      auto load = [&](int k) {  // pieces k .. k + 3
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < J; ++j)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            next[j][i] = src[j] && quad * 4 + i < r.KB ? ld_cg_u32(src[j] + quad * 16 + i * 4) : 0u;
+            next[j][i] = src[j] && k + i < r.k1 ? ld_cg_u32(src[j] + (k + i) * 4) : 0u;
       };
-      load(0);
-      const int quads = (r.KB + 3) / 4;
-      for (int quad = 0; quad < quads && !stop; ++quad) {
-        uint32_t now[4][4];
+      load(r.k0);
+      for (int k = r.k0; k < r.k1 && !stop; k += 4) {
+        uint32_t now[J][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < J; ++j)
 #pragma unroll
           for (int i = 0; i < 4; ++i) now[j][i] = next[j][i];
-        if (quad + 1 < quads) load(quad + 1);
+        if (k + 4 < r.k1) load(k + 4);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (quad * 4 + i >= r.KB || stop) continue;
+        for (int i = 0; i < 4; i += 2) {
+          if (k + i >= r.k1 || stop) continue;
           if (!__all_sync(0xFFFFFFFFu,
                           wait_bounded(empty_bar(stage), phase ^ 1u, abort_f, p.status))) {
             stop = true;
             continue;
           }
-          st_shared_v4(sf_base + (stage * 2 + 1) * kScaleChunk + lane * 16, now[0][i], now[1][i],
-                       now[2][i], now[3][i]);
+          const uint32_t sf = sf_base + stage * sf_bytes + 2 * kScaleChunk + lane * 16;
+          const uint32_t half = b_chunks * kScaleChunk;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            st_shared_v4(sf + h * half, now[0][i + h], now[1][i + h], now[2][i + h],
+                         now[3][i + h]);
+            if (b_chunks == 2)
+              st_shared_v4(sf + h * half + kScaleChunk, now[4][i + h], now[5][i + h], 0u, 0u);
+          }
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(full_bar(stage));
+          if (elect_one()) mbar_arrive(full_bar(stage));
           if (++stage == p.stages) {
             stage = 0;
             phase ^= 1u;
@@ -616,8 +698,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp >= 8) {
-    // -------------------------------------------------------------- epilogue
-    constexpr int PER = 32 / STRIDE;  // tokens in 32 columns
+    // ---------------------------------------------------------------- epilogue
+    constexpr int PER = P == 2 ? 16 : 8;  // tokens at a time (32 or 24 columns)
     const int q = warp & 3;
     int acc = 0;
     uint32_t acc_phase = 0;
@@ -637,20 +719,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the four warps give up together, as the barriers below need all of them
       if (any_of_epilogue(!wait_bounded(tfull_bar(acc), acc_phase, abort_f, p.status))) break;
       tc_fence_after();
-      const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + acc * 128;
-      for (int i0 = 0; i0 < r.n; i0 += PER) {
+      const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + acc * kMaxN;
+      const unsigned long long has = mask[r.e];
+      const int columns = r.all ? p.T : r.n;  // tokens that have columns
+      for (int i0 = 0; i0 < columns; i0 += PER) {
         uint32_t v[32];
-        tmem_ld32(taddr + i0 * STRIDE, v);
+        tmem_ld32(taddr + i0 * P, v);
         tmem_wait_ld();
         float s[PER];
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
           s[i] = 0.f;
 #pragma unroll
-          for (int term = P - 1; term >= 0; --term) s[i] += __uint_as_float(v[i * STRIDE + term]);
+          for (int term = P - 1; term >= 0; --term) s[i] += __uint_as_float(v[i * P + term]);
         }
         if (r.down) {
-          float* y = p.y + r.tile * 128 + q * 32 + lane;
+          float* y = p.y + (int64_t)r.split * R * p.H + r.tile * 128 + q * 32 + lane;
 #pragma unroll
           for (int i = 0; i < PER; ++i)
             if (i0 + i < r.n) y[(int64_t)list[r.first + i0 + i] * p.H] = s[i];
@@ -665,13 +749,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int ib = p.I / 32, col = r.tile * 64 + q * 32;
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
-              if (i0 + i >= r.n) continue;
+              const int t = i0 + i;
+              if (t >= columns || (r.all && !(has >> t & 1))) continue;
+              const int pos = r.first + (r.all ? __popcll(has & ((1ull << t) - 1)) : t);
               const float g = s[i];
               const float up = exchange[i * 64 + q * 32 + lane];
               const float a = Dt<T>::to_f(Dt<T>::from_f(g / (1.f + expf(-g)) * up));
-              const int64_t row = (int64_t)list[r.first + i0 + i] * P;
-              write_terms<P>(a, p.aq + row * p.I + col + lane, p.I, p.as + row * ib + col / 32, ib,
-                             lane);
+              write_terms<P>(a, p.aq + (int64_t)pos * P * p.I + col + lane, p.I,
+                             p.as + (int64_t)pos * P * ib + col / 32, ib, lane);
             }
           }
           sync_epilogue();
@@ -686,13 +771,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_proxy_async_all();  // aq is read by TMA
         __threadfence();
         sync_epilogue();
-        if (threadIdx.x == 8 * 32) atomicAdd(p.ready + r.eg, 1u);
+        if (threadIdx.x == 8 * 32) atomicAdd(p.ready + r.ai, 1u);
         continue;
       }
       __threadfence();
       sync_epilogue();
       if (threadIdx.x == 8 * 32)
-        *last_s = atomicAdd(p.done + r.tile, 1u) + 1 == (unsigned)groups;
+        *last_s = atomicAdd(p.done + r.tile, 1u) + 1 == (unsigned)(active * p.splits);
       sync_epilogue();
       if (*last_s) {
         __threadfence();
@@ -702,7 +787,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           float s = 0.f;
           const float* y = p.y + (int64_t)t * p.k * p.H + h;
 #pragma unroll 8
-          for (int j = 0; j < p.k; ++j) s = fmaf(sel_w[t * p.k + j], __ldcg(y + (int64_t)j * p.H), s);
+          for (int j = 0; j < p.k; ++j) {
+            float v = __ldcg(y + (int64_t)j * p.H);
+            for (int z = 1; z < p.splits; ++z) v += __ldcg(y + ((int64_t)z * R + j) * p.H);
+            s = fmaf(sel_w[t * p.k + j], v, s);
+          }
           out[(int64_t)t * p.H] = Dt<T>::from_f(s);
         }
       }
@@ -722,9 +811,18 @@ size_t fixed_smem(int E, int R) {
   return 1024 + kBarBytes + kExchange + (size_t)E * 8 + 2 * (size_t)(E + 1) * 4 + (size_t)R * 8;
 }
 
+// Parts of K that a down unit is cut into: enough units for four to a CTA (a CTA's last unit is
+// then a quarter of its share), of at least four slices each.
+int down_splits(int64_t T, int64_t E, int64_t H, int64_t I, int k) {
+  const int64_t slots = T * k, units = (E < slots ? E : slots) * (H / 128);
+  int64_t s = units > 0 ? (4 * 152 + units - 1) / units : 1;
+  if (s > I / 1024) s = I / 1024;
+  return (int)(s < 1 ? 1 : s > 8 ? 8 : s);
+}
+
 template <typename T>
 cudaError_t launch_t(const Mx4TokensArgs& a, cudaStream_t s) {
-  constexpr int P = Terms<T>::P, STRIDE = Terms<T>::STRIDE, G = Terms<T>::G;
+  constexpr int P = Terms<T>::P;
   int dev = 0, sms = 0, most = 0;
   cudaError_t err = cudaGetDevice(&dev);
   if (err == cudaSuccess)
@@ -745,8 +843,7 @@ cudaError_t launch_t(const Mx4TokensArgs& a, cudaStream_t s) {
   p.gs = a.gate.scales;
   p.us = a.up.scales;
   p.ds = a.down.scales;
-  p.scales_vec =
-      (((uintptr_t)p.gs | (uintptr_t)p.us | (uintptr_t)p.ds) & 15u) == 0;
+  p.scales_vec = (((uintptr_t)p.gs | (uintptr_t)p.us | (uintptr_t)p.ds) & 15u) == 0;
   p.status = (unsigned*)a.ws;
   p.grid_count = (unsigned*)(a.ws + 64);
   p.ready = (unsigned*)(a.ws + l.ready);
@@ -760,21 +857,23 @@ cudaError_t launch_t(const Mx4TokensArgs& a, cudaStream_t s) {
   p.out = a.out;
   p.idx = a.idx;
   p.w = a.w;
+  p.splits = down_splits(a.T, a.E, a.H, a.I, a.k);
   const int R = a.T * a.k;
-  // the ring: as many slices as fit, each with room for the columns of the largest group
-  const int n = a.T < G ? a.T : G;
-  p.stage_bytes = kA + (n * STRIDE + 15) / 16 * 16 * 128;
+  // the ring: as many slices as fit, each with room for the columns of all T tokens
+  p.ncap = (a.T * P + kBox - 1) / kBox * kBox;
   const size_t fixed = fixed_smem(a.E, R);
-  p.stages = (int)(((size_t)most - fixed) / (p.stage_bytes + 2 * kScaleChunk));
+  const size_t stage = 2 * kA + 2 * (size_t)p.ncap * 128 + (p.ncap > 128 ? 6 : 4) * kScaleChunk;
+  p.stages = (int)(((size_t)most - fixed) / stage);
   if (p.stages > kMaxStages) p.stages = kMaxStages;
-  const size_t smem = fixed + (size_t)p.stages * (p.stage_bytes + 2 * kScaleChunk);
+  const size_t smem = fixed + (size_t)p.stages * stage;
 
-  CUtensorMap mg, mu, md, mx, ma;
+  CUtensorMap mg, mu, md, mx1, mx, ma;
   if (!make_map_codes(&mg, a.gate.codes, a.H, (int64_t)a.E * a.I, 64) ||
       !make_map_codes(&mu, a.up.codes, a.H, (int64_t)a.E * a.I, 64) ||
       !make_map_codes(&md, a.down.codes, a.I, (int64_t)a.E * a.H, 128) ||
-      !make_map_bytes(&mx, p.xq, a.H, (int64_t)a.T * P, P) ||
-      !make_map_bytes(&ma, p.aq, a.I, (int64_t)R * P, P))
+      !make_map_bytes(&mx1, p.xq, a.H, (int64_t)a.T * P, P) ||
+      !make_map_bytes(&mx, p.xq, a.H, (int64_t)a.T * P, kBox) ||
+      !make_map_bytes(&ma, p.aq, a.I, (int64_t)R * P, kBox))
     return cudaErrorInvalidValue;
   auto kern = moe_mx4_tokens<T>;
   err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -791,7 +890,7 @@ cudaError_t launch_t(const Mx4TokensArgs& a, cudaStream_t s) {
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, mg, mu, md, mx, ma, p);
+  return cudaLaunchKernelEx(&cfg, kern, mg, mu, md, mx1, mx, ma, p);
 }
 
 }  // namespace
@@ -813,7 +912,7 @@ Mx4TokensLayout mx4_tokens_layout(int64_t T, int64_t E, int64_t H, int64_t I, in
   l.xs = take((size_t)T * P * (H / 32));
   l.aq = take((size_t)R * P * I);
   l.as = take((size_t)R * P * (I / 32));
-  l.y = take((size_t)R * H * 4);
+  l.y = take((size_t)R * H * 4 * down_splits(T, E, H, I, k));
   l.total = off;
   return l;
 }
