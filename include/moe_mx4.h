@@ -90,12 +90,13 @@ int moe_mx4_experts_forward_dispatched(const void* x_d, int xdt, const int32_t* 
  *   a = silu(x gate[e]^T) (x up[e]^T) in FP32, rounded once to dt,
  *   out[t] = sum_j w[t, j] (a_j down[e_j]^T), FP32 in the order j = 0 .. top_k-1, rounded once.
  * x [T, H], router [E, H] and out [T, H] of dtype dt (f16 / bf16), weights as for the experts
- * above; the activations are not quantised.  A token holding an infinity or a NaN gets NaN.
+ * above.  The activations are not quantised: they enter the products to within 2^-14 of the
+ * largest value of their block of 32.  A token holding an infinity or a NaN gets NaN.
  * idx [T, top_k] uint32 and w [T, top_k] float receive the selection; either may be NULL.
  * One cooperative launch (after a small memset of the workspace's counters); if its CTAs cannot
  * all be resident (another context holds SMs) the call returns MOE_ERR_CUDA.
  * Limits: T <= 64, top_k <= min(E, 32), T * top_k <= 1024 (else MOE_ERR_SHAPE); H and I multiples
- * of 128, x and router 16-byte and codes 32-byte aligned (else MOE_ERR_ALIGN).
+ * of 128, x and router 16-byte aligned (else MOE_ERR_ALIGN).
  * ws: at least moe_mx4_tokens_workspace_bytes(...) bytes (0 for sizes out of range), 256-byte
  * aligned.
  */

@@ -92,7 +92,7 @@ struct Mx4TokensLayout {
   size_t ready, done, zeroed;      // counters behind the header
   size_t logits, xq, xs, aq, as, y, total;
 };
-Mx4TokensLayout mx4_tokens_layout(int64_t T, int64_t E, int64_t H, int64_t I, int k, int dt);
+Mx4TokensLayout mx4_tokens_layout(int64_t T, int64_t E, int64_t H, int64_t I, int k);
 struct Mx4TokensArgs {
   const void* x;
   const void* router;

@@ -159,7 +159,7 @@ int moe_mx4_experts_forward_dispatched(const void* x_d, int xdt, const int32_t* 
 size_t moe_mx4_tokens_workspace_bytes(int64_t T, int64_t E, int64_t H, int64_t I, int top_k,
                                       int dt) {
   if (check_tokens_shape(T, E, H, I, top_k, dt) != MOE_OK) return 0;
-  return mx4_tokens_layout(T, E, H, I, top_k, dt).total;
+  return mx4_tokens_layout(T, E, H, I, top_k).total;
 }
 
 int moe_mx4_forward_tokens(const void* x, const void* router, int dt, const uint8_t* gate_codes,
@@ -175,11 +175,10 @@ int moe_mx4_forward_tokens(const void* x, const void* router, int dt, const uint
   if (!router) return MOE_ERR_NULL;
   if (T == 0) return MOE_OK;
   if (!x || !out) return MOE_ERR_NULL;
-  if (!aligned(x, 16) || !aligned(router, 16) || !aligned(gate_codes, 32) ||
-      !aligned(up_codes, 32) || !aligned(down_codes, 32) || !aligned(out, 2) || !aligned(idx, 4) ||
+  if (!aligned(x, 16) || !aligned(router, 16) || !aligned(out, 2) || !aligned(idx, 4) ||
       !aligned(w, 4))
     return MOE_ERR_ALIGN;
-  if (int st = check_ws(ws, ws_bytes, mx4_tokens_layout(T, E, H, I, top_k, dt).total)) return st;
+  if (int st = check_ws(ws, ws_bytes, mx4_tokens_layout(T, E, H, I, top_k).total)) return st;
   Mx4TokensArgs a{};
   a.x = x;
   a.router = router;

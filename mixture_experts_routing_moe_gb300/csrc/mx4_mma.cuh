@@ -77,26 +77,6 @@ static __device__ __forceinline__ void umma2_mxf4(uint32_t d_tmem, uint64_t ades
       : "memory");
 }
 
-// kind::mxf8f6f4 takes operands of different small types: here A is e2m1 (5), each code in a byte of
-// its own as the 16U4_ALIGN16B tensor maps lay them out (16 codes in 8 bytes, then 8 bytes of
-// padding; 128 codes a 128-byte row), and B is e4m3 (0).  One instruction takes K = 32 and one scale
-// a row: byte sf_id of the four of a chunk.
-static __host__ __device__ constexpr uint32_t make_idesc_mxf4_f8(int M, int N, int sf_id) {
-  return ((uint32_t)sf_id << 4) | (5u << 7) | (0u << 10) | ((uint32_t)(N >> 3) << 17) |
-         (1u << 23) | ((uint32_t)(M >> 7) << 27) | ((uint32_t)sf_id << 29);
-}
-static __device__ __forceinline__ void umma_mxf8f6f4(uint32_t d_tmem, uint64_t adesc,
-                                                     uint64_t bdesc, uint32_t idesc, uint32_t sfa,
-                                                     uint32_t sfb, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], "
-      "[%5], p;\n\t}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-      : "memory");
-}
-
 // Register budget of the calling warpgroup (every warp of it executes this).
 template <int N>
 static __device__ __forceinline__ void set_max_regs_dec() {
@@ -160,21 +140,6 @@ static inline bool make_map_bytes(CUtensorMap* m, const void* ptr, int64_t pitch
   cuuint32_t estr[2] = {1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// 2-D map over rows of K e2m1 codes (K a multiple of 128, the base of 32 bytes), box 128 codes x
-// box_rows, each code widened to a byte of shared memory, 128-byte swizzle.
-static inline bool make_map_codes(CUtensorMap* m, const void* ptr, int64_t K, int64_t rows,
-                                  int box_rows) {
-  EncodeTiledFn enc = encode_fn();
-  if (!enc) return false;
-  cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
-  cuuint64_t strides[1] = {(cuuint64_t)K / 2};
-  cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
-  cuuint32_t estr[2] = {1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 2, const_cast<void*>(ptr), dims, strides,
-             box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

@@ -6,14 +6,17 @@
 //
 // The layer reads each active expert's weights once, 17/32 of a byte a weight, and that is its
 // floor, so nothing may be spent on the weights but the copy.  The tensor cores decode them:
-// tcgen05.mma kind::mxf8f6f4 takes e2m1 weights (M = 128 weight rows, widened to a byte in shared
-// memory by the tensor map) against e4m3 tokens, and applies the weights' block scales.  The
-// tokens keep their 16 bits: e4m3 has four significant bits, so a bf16 value (eight) is the exact
-// sum of two e4m3 terms and an f16 value (eleven) of three, each in blocks of 32 with a scale of
-// its own, 2^-4 of the one before.  The terms are separate columns (N) of the MMA, and the
-// epilogue adds them up.  (Exact for values down to 2^-13 of their block's largest; below that the
-// error is under 2^-22 of that largest.)  N is small, so the extra columns cost no time: a K = 128
-// slice of 128 weight rows takes the MMAs about 130 cycles and the memory about 370.
+// tcgen05.mma kind::mxf4 multiplies the packed codes (M = 128 weight rows) by e2m1 tokens and
+// applies the block scales of both.  The tokens stay what they are: each block of 32 values is the
+// sum of five e2m1 terms, each with a scale 2^-3 of the one before (a value scaled to at most 4 is
+// within 1/2 of a code, so a term takes three bits off).  What five leave is at most 2^-14 of the
+// block's largest value, far under the 16-bit rounding of that value itself, and nothing where
+// the value's bits end above that.  The terms are separate columns (N) of the MMA, and the
+// epilogue adds them up.  N is small, so they cost no time: a 256-deep slice of 128 weight rows
+// keeps the tensor pipe about 300 cycles and the memory about 700.
+// (Two e4m3 terms under kind::mxf8f6f4 are exact for bf16, but the weights then widen to a byte in
+// shared memory: the TMA unit handles rows of 64 packed bytes, and half as many bytes are in
+// flight.  The layer of 256 experts took 1.08 ms that way.)
 //
 // Steps.  One CTA per SM, all resident; grid-wide hand-overs go through counters in global memory:
 //   0  every CTA splits its share of x into terms (xq, xs) and computes the logits of its experts;
@@ -43,20 +46,18 @@ using namespace tc;
 using namespace mx4;
 
 constexpr int kThreads = 384, kWarps = kThreads / 32;
-constexpr int kA = 128 * 128;      // bytes of 128 x 128 weights, widened; a stage has two
-constexpr int kMaxStages = 5;
-constexpr int kMaxN = 192;         // columns of a unit: 64 tokens x 3 terms
+constexpr int P = 5;               // terms of a token value
+constexpr int kG = 38;             // tokens of a unit
+constexpr int kMaxN = 192;         // columns of a unit
+static_assert(kG * P <= kMaxN, "columns of a group");
+constexpr int kA = 128 * 128;      // bytes of a slice's weights (128 rows, 256 deep)
+constexpr int kMaxStages = 10;
 constexpr int kBox = 16;           // rows of token terms a TMA box
 constexpr int kBarBytes = 256;
-// two accumulators, then the scales of each stage: 2 x 4 columns for A, 2 x 8 for B
+// two accumulators, then the scales of two slices: 2 x 4 columns for A, 2 x 8 for B
 constexpr uint32_t kTmemCols = 512, kScaleCol = 2 * kMaxN;
-static_assert(kScaleCol + kMaxStages * 24 <= kTmemCols, "tensor memory");
+static_assert(kScaleCol + 2 * 24 <= kTmemCols, "tensor memory");
 constexpr int kExchange = 16 * 64 * 4;  // u of up to 16 tokens x 64 columns
-
-// terms of a token value
-template <typename T> struct Terms;
-template <> struct Terms<__nv_bfloat16> { static constexpr int P = 2; };
-template <> struct Terms<__half> { static constexpr int P = 3; };
 
 struct TokensParams {
   const void* x;
@@ -98,27 +99,30 @@ __device__ __forceinline__ void fence_proxy_async_all() {
   asm volatile("fence.proxy.async;" ::: "memory");
 }
 
-// A warp writes one block of 32 values (one a lane) as P e4m3 terms: term p of the lane's value at
-// q[p * pitch], the scale bytes at sc[p * sc_pitch] (lane 0).  With the largest magnitude in
-// [2^n, 2^(n + 1)) the first scale is 2^(n - 7), so scaled values stay under 2^8 < 448; each
-// remainder is at most 8 of the first grid's sixteenths and is scaled up by 16.
-template <int P>
+// A warp writes one block of 32 values (one a lane) as P e2m1 terms: term p's 16 bytes at
+// q + p * pitch, its scale byte at sc + p * sc_pitch.  With the largest magnitude in
+// [2^n, 2^(n + 1)) the first scale is 2^(n - 1), so scaled values stay under 4; a remainder is at
+// most 1/2 and is scaled up by 8 for the next term.
 __device__ __forceinline__ void write_terms(float v, uint8_t* q, int64_t pitch, uint8_t* sc,
                                             int64_t sc_pitch, int lane) {
   const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v) & 0x7FFFFFFFu);
   const int f = (int)(top >> 23);
   const bool bad = f == 255;
-  const int b0 = max(f - 7, 4 * (P - 1));
-  float r = bad ? 0.f : v * __uint_as_float((uint32_t)(254 - min(b0, 253)) << 23);
+  const int b0 = max(min(f, 254) - 1, 3 * (P - 1));
+  float r = bad ? 0.f : v * __uint_as_float((uint32_t)(254 - b0) << 23);
 #pragma unroll
   for (int p = 0; p < P; ++p) {
-    uint16_t h;
-    uint32_t back;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h) : "f"(0.f), "f"(r));
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(h));
-    q[p * pitch] = (uint8_t)(h & 0xFFu);
-    if (lane == 0) sc[p * sc_pitch] = (uint8_t)(bad ? 255 : b0 - 4 * p);
-    r = (r - __low2float(*reinterpret_cast<const __half2*>(&back))) * 16.f;
+    uint32_t c, back;
+    asm("{\n\t.reg .b8 b, z;\n\tmov.b32 {z, z, z, z}, 0;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b, %2, %3;\n\t"
+        "mov.b32 %0, {b, z, z, z};\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b;\n\t}"
+        : "=r"(c), "=r"(back)
+        : "f"(0.f), "f"(r));
+    const uint32_t next = __shfl_down_sync(0xFFFFFFFFu, c, 1);
+    if ((lane & 1) == 0) q[p * pitch + (lane >> 1)] = (uint8_t)(c | (next << 4));
+    if (lane == 0) sc[p * sc_pitch] = (uint8_t)(bad ? 255 : b0 - 3 * p);
+    r = (r - __low2float(*reinterpret_cast<const __half2*>(&back))) * 8.f;
   }
 }
 
@@ -189,13 +193,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                    const __grid_constant__ CUtensorMap mapX1,
                    const __grid_constant__ CUtensorMap mapX,
                    const __grid_constant__ CUtensorMap mapA, const TokensParams p) {
-  constexpr int P = Terms<T>::P;
   extern __shared__ uint8_t mx4_smem_raw[];
   const uint32_t raw = smem_u32(mx4_smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
-  const int b_half = p.ncap * 128;               // bytes of 128-deep token terms
-  const int stage_bytes = 2 * kA + 2 * b_half;
-  const int b_chunks = p.ncap > 128 ? 2 : 1;     // scale chunks of 128-deep token terms
+  const int stage_bytes = kA + p.ncap * 128;
+  const int b_chunks = p.ncap > 128 ? 2 : 1;  // scale chunks of 128-deep token terms
   const int sf_bytes = (2 + 2 * b_chunks) * kScaleChunk;
   uint8_t* at = mx4_smem_raw + (base - raw) + p.stages * stage_bytes;
   const uint32_t sf_base = smem_u32(at);  // a stage's scales: two chunks of A, then those of B
@@ -208,8 +210,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   at += p.E * 8;
   int* start = reinterpret_cast<int*>(at);  // first entry of an expert's tokens in `list`
   at += (p.E + 1) * 4;
-  int* act = reinterpret_cast<int*>(at);  // the experts that have tokens, ascending
-  at += (p.E + 1) * 4;
+  int* act = reinterpret_cast<int*>(at);  // expert | group << 16 of each group of tokens
+  at += 2 * p.E * 4;
   const int R = p.T * p.k;
   float* sel_w = reinterpret_cast<float*>(at);
   at += R * 4;
@@ -260,8 +262,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int b = blockIdx.x * kWarps + warp; b < p.T * hb; b += gridDim.x * kWarps) {
       const int t = b / hb, c = b - t * hb;
       const float v = Dt<T>::to_f(x[(int64_t)t * p.H + c * 32 + lane]);
-      write_terms<P>(v, p.xq + (int64_t)t * P * p.H + c * 32 + lane, p.H,
-                     p.xs + (int64_t)t * P * hb + c, hb, lane);
+      write_terms(v, p.xq + (int64_t)t * P * (p.H / 2) + c * 16, p.H / 2,
+                  p.xs + (int64_t)t * P * hb + c, hb, lane);
     }
     // two experts and four tokens at a time: eight sums from six 16-byte loads
     constexpr int TB = 4, EB = 2;
@@ -352,18 +354,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     int carry = 0, n_act = 0;
     for (int e0 = 0; e0 < p.E; e0 += 32) {
       const int e = e0 + lane;
-      const int n = e < p.E ? __popcll(mask[e]) : 0;
-      int s = n;
+      const int n = e < p.E ? __popcll(mask[e]) : 0, g = (n + kG - 1) / kG;  // g <= 2
+      int s = n, sg = g;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xFFFFFFFFu, s, o);
-        if (lane >= o) s += y;
+        const int y = __shfl_up_sync(0xFFFFFFFFu, s, o), yg = __shfl_up_sync(0xFFFFFFFFu, sg, o);
+        if (lane >= o) s += y, sg += yg;
       }
       if (e < p.E) start[e] = carry + s - n;
+      for (int i = 0; i < g; ++i) act[n_act + sg - g + i] = e | i << 16;
       carry += __shfl_sync(0xFFFFFFFFu, s, 31);
-      const unsigned has = __ballot_sync(0xFFFFFFFFu, n > 0);
-      if (n > 0) act[n_act + __popc(has & ((1u << lane) - 1))] = e;
-      n_act += __popc(has);
+      n_act += __shfl_sync(0xFFFFFFFFu, sg, 31);
     }
     if (lane == 0) start[p.E] = carry, *active_s = n_act;
   }
@@ -382,10 +383,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int n1 = active * NI, per_down = NH * p.splits, total = n1 + active * per_down;
   struct Unit {
     bool down;
-    int e, ai;        // expert, its place among the active ones
+    int e, ai;        // expert, place in `act`
     int tile, split;  // column tile, part of K
     int first, n;     // its tokens: list[first .. first + n)
-    int k0, k1;       // 128-deep pieces of K
+    int k0, k1;       // 256-deep slices
     // gate/up of an expert that takes many of the tokens multiplies all T of them (their terms
     // are contiguous); otherwise each token's terms are loaded on their own
     bool all;
@@ -399,13 +400,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int w = v - r.ai * per;
     r.tile = r.down ? w / p.splits : w;
     r.split = r.down ? w - r.tile * p.splits : 0;
-    r.e = act[r.ai];
-    r.first = start[r.e];
-    r.n = start[r.e + 1] - r.first;
-    const int pieces = (r.down ? p.I : p.H) / 128;
-    r.k0 = r.down ? (int)((int64_t)pieces * r.split / p.splits) : 0;
-    r.k1 = r.down ? (int)((int64_t)pieces * (r.split + 1) / p.splits) : pieces;
-    r.all = !r.down && r.n * 8 >= p.T;
+    const int a = act[r.ai];
+    r.e = a & 0xFFFF;
+    r.first = start[r.e] + (a >> 16) * kG;
+    r.n = min(start[r.e + 1] - r.first, kG);
+    const int slices = ((r.down ? p.I : p.H) + 255) / 256;
+    r.k0 = r.down ? slices * r.split / p.splits : 0;
+    r.k1 = r.down ? slices * (r.split + 1) / p.splits : slices;
+    r.all = !r.down && p.T <= kG && r.n * 8 >= p.T;
     r.cols = (r.all ? p.T : r.n) * P;
     return r;
   };
@@ -419,26 +421,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int u = blockIdx.x; u < total && !stop; u += gridDim.x) {
       const Unit r = unit_of(u);
       const int row = r.down ? r.e * p.H + r.tile * 128 : r.e * p.I + r.tile * 64;
-      for (int k = r.k0; k < r.k1; k += 2) {
+      for (int k = r.k0; k < r.k1; ++k) {
         if (!__all_sync(0xFFFFFFFFu,
                         wait_bounded(empty_bar(stage), phase ^ 1u, abort_f, p.status))) {
           stop = true;
           break;
         }
-        const int halves = min(2, r.k1 - k);
         const uint32_t sa = base + stage * stage_bytes, fb = full_bar(stage);
         if (elect_one()) {
-          mbar_expect_tx(fb, halves * (kA / 2));  // counted in packed bytes, not the widened ones
+          mbar_expect_tx(fb, kA);
           if (r.down) {
             tma_load_2d(sa, &mapD, fb, k * 128, row, pol);
-            if (halves == 2) tma_load_2d(sa + kA, &mapD, fb, k * 128 + 128, row, pol);
           } else {
             tma_load_2d(sa, &mapG, fb, k * 128, row, pol);
             tma_load_2d(sa + kA / 2, &mapU, fb, k * 128, row, pol);
-            if (halves == 2) {
-              tma_load_2d(sa + kA, &mapG, fb, k * 128 + 128, row, pol);
-              tma_load_2d(sa + kA + kA / 2, &mapU, fb, k * 128 + 128, row, pol);
-            }
           }
         }
         if (++stage == p.stages) {
@@ -454,38 +450,36 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool stop = false;
     for (int u = blockIdx.x; u < total && !stop; u += gridDim.x) {
       const Unit r = unit_of(u);
-      const uint32_t idesc = make_idesc_mxf4_f8(128, (r.cols + 15) / 16 * 16, 0);
+      const uint32_t idesc = make_idesc_mxf4(128, (r.cols + 15) / 16 * 16, 0);
       if (!__all_sync(0xFFFFFFFFu,
                       wait_bounded(tempty_bar(acc), acc_phase ^ 1u, abort_f, p.status)))
         break;
       tc_fence_after();
       const uint32_t d = tmem + acc * kMaxN;
-      for (int k = r.k0; k < r.k1; k += 2) {
+      for (int k = r.k0; k < r.k1; ++k) {
         if (!__all_sync(0xFFFFFFFFu, wait_bounded(full_bar(stage), phase, abort_f, p.status))) {
           stop = true;
           break;
         }
         tc_fence_after();
-        const uint32_t sa = base + stage * stage_bytes, sb = sa + 2 * kA;
+        const uint32_t sa = base + stage * stage_bytes;
         const uint32_t sf = sf_base + stage * sf_bytes, sfb = sf + 2 * kScaleChunk;
-        const uint32_t cols = tmem + kScaleCol + stage * 24;
-        const int halves = min(2, r.k1 - k);
+        const uint32_t cols = tmem + kScaleCol + (stage & 1) * 24;
+        const uint64_t da = make_sdesc(sa), db = make_sdesc(sa + kA);
         if (elect_one()) {
-          for (int h = 0; h < halves; ++h) {
-            const uint32_t ca = cols + h * 12, cb = ca + 4;
-            tmem_cp_scale(ca, make_sdesc_scale(sf + h * kScaleChunk));
-            tmem_cp_scale(cb, make_sdesc_scale(sfb + h * b_chunks * kScaleChunk));
-            if (b_chunks == 2)
-              tmem_cp_scale(cb + 4, make_sdesc_scale(sfb + (2 * h + 1) * kScaleChunk));
-          }
-          for (int h = 0; h < halves; ++h) {
-            const uint32_t ca = cols + h * 12, cb = ca + 4;
-            const uint64_t da = make_sdesc(sa + h * kA), db = make_sdesc(sb + h * b_half);
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)  // the scale ids of A and B are kk
-              umma_mxf8f6f4(d, da + 2u * kk, db + 2u * kk,
-                            idesc | ((uint32_t)kk << 4) | ((uint32_t)kk << 29), ca, cb,
-                            k != r.k0 || h != 0 || kk != 0);
+          for (int c = 0; c < 2; ++c) {
+            tmem_cp_scale(cols + c * 12, make_sdesc_scale(sf + c * kScaleChunk));
+            tmem_cp_scale(cols + c * 12 + 4, make_sdesc_scale(sfb + c * b_chunks * kScaleChunk));
+            if (b_chunks == 2)
+              tmem_cp_scale(cols + c * 12 + 8, make_sdesc_scale(sfb + (2 * c + 1) * kScaleChunk));
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t ca = cols + (i >> 1) * 12;
+            umma_mxf4(d, da + 2u * i, db + 2u * i,
+                      (i & 1) ? idesc | (2u << 4) | (2u << 29) : idesc, ca, ca + 4,
+                      k != r.k0 || i != 0);
           }
           umma_commit(empty_bar(stage));
         }
@@ -523,23 +517,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int boxes = whole ? (r.cols + kBox - 1) / kBox : r.n;
       const int bytes = whole ? kBox * 128 : P * 128;    // of a box
       const int row0 = r.down ? r.first * P : 0;
-      for (int k = r.k0; k < r.k1; k += 2) {
+      for (int k = r.k0; k < r.k1; ++k) {
         if (!__all_sync(0xFFFFFFFFu,
                         wait_bounded(empty_bar(stage), phase ^ 1u, abort_f, p.status))) {
           stop = true;
           break;
         }
-        const int halves = min(2, r.k1 - k);
-        const uint32_t sb = base + stage * stage_bytes + 2 * kA, fb = full_bar(stage);
-        if (elect_one()) mbar_expect_tx(fb, halves * boxes * bytes);
+        const uint32_t sb = base + stage * stage_bytes + kA, fb = full_bar(stage);
+        const CUtensorMap* m = r.down ? &mapA : r.all ? &mapX : &mapX1;
+        if (elect_one()) mbar_expect_tx(fb, boxes * bytes);
         __syncwarp();
         for (int i = 0; i < boxes; ++i) {
           const int row = whole ? row0 + i * kBox : (int)list[r.first + i] / p.k * P;
-          if (elect_one()) {
-            const CUtensorMap* m = r.down ? &mapA : r.all ? &mapX : &mapX1;
-            tma_load_2d(sb + i * bytes, m, fb, k * 128, row, pol);
-            if (halves == 2) tma_load_2d(sb + b_half + i * bytes, m, fb, k * 128 + 128, row, pol);
-          }
+          if (elect_one()) tma_load_2d(sb + i * bytes, m, fb, k * 128, row, pol);
         }
         ++armed;
         if (++stage == p.stages) {
@@ -561,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 4) {
     // ---------------------------------------------------------------- weight scales
-    // lane l holds rows l, l + 32, l + 64, l + 96 of the unit's 128, eight pieces (32 bytes) each
+    // lane l holds rows l, l + 32, l + 64, l + 96 of the unit's 128, four slices (32 bytes) each
     int stage = 0;
     uint32_t phase = 0;
     bool stop = false;
@@ -569,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto load = [&](int u, int part) {
       const Unit r = unit_of(u);
       const int pitch = (r.down ? p.I : p.H) / 32;
-      const int at0 = r.k0 * 4 + part * 32, left = r.k1 * 4 - at0;
+      const int at0 = r.k0 * 8 + part * 32, left = min(r.k1 * 8, pitch) - at0;
       const bool vec = p.scales_vec && ((pitch | at0) & 15) == 0;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -596,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (blockIdx.x < total) load(blockIdx.x, 0);
     for (int u = blockIdx.x; u < total && !stop; u += gridDim.x) {
       const Unit r = unit_of(u);
-      const int pieces = r.k1 - r.k0, parts = (pieces + 7) / 8;
+      const int slices = r.k1 - r.k0, parts = (slices + 3) / 4;
       for (int part = 0; part < parts && !stop; ++part) {
         uint32_t now[4][8];
 #pragma unroll
@@ -607,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         else if (u + (int)gridDim.x < total) load(u + gridDim.x, 0);
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
-          if (part * 8 + i >= pieces || stop) continue;
+          if (part * 4 + i / 2 >= slices || stop) continue;
           if (!__all_sync(0xFFFFFFFFu,
                           wait_bounded(empty_bar(stage), phase ^ 1u, abort_f, p.status))) {
             stop = true;
@@ -629,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 5) {
     // ---------------------------------------------------------------- token scales
-    // lane l holds the terms in columns l, l + 32, ..., l + 160, four pieces of K each
+    // lane l holds the terms in columns l, l + 32, ..., l + 160, two slices (16 bytes) each
     constexpr int J = kMaxN / 32;
     int stage = 0;
     uint32_t phase = 0;
@@ -655,24 +645,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       uint32_t next[J][4];
-      auto load = [&](int k) {  // pieces k .. k + 3
+      const bool vec = (pitch & 15) == 0 && (r.k0 & 1) == 0;
+      auto load = [&](int k) {  // slices k, k + 1
 #pragma unroll
-        for (int j = 0; j < J; ++j)
+        for (int j = 0; j < J; ++j) {
+          next[j][0] = next[j][1] = next[j][2] = next[j][3] = 0u;
+          if (32 * j >= r.cols || !src[j]) continue;
+          if (vec) {
+            const uint4 v = ld_cg_v4(src[j] + k * 8);
+            next[j][0] = v.x, next[j][1] = v.y, next[j][2] = v.z, next[j][3] = v.w;
+          } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            next[j][i] = src[j] && k + i < r.k1 ? ld_cg_u32(src[j] + (k + i) * 4) : 0u;
+            for (int i = 0; i < 4; ++i)
+              if (k * 8 + i * 4 < pitch) next[j][i] = ld_cg_u32(src[j] + k * 8 + i * 4);
+          }
+        }
       };
       load(r.k0);
-      for (int k = r.k0; k < r.k1 && !stop; k += 4) {
+      for (int k = r.k0; k < r.k1 && !stop; k += 2) {
         uint32_t now[J][4];
 #pragma unroll
         for (int j = 0; j < J; ++j)
 #pragma unroll
           for (int i = 0; i < 4; ++i) now[j][i] = next[j][i];
-        if (k + 4 < r.k1) load(k + 4);
+        if (k + 2 < r.k1) load(k + 2);
 #pragma unroll
         for (int i = 0; i < 4; i += 2) {
-          if (k + i >= r.k1 || stop) continue;
+          if (k + i / 2 >= r.k1 || stop) continue;
           if (!__all_sync(0xFFFFFFFFu,
                           wait_bounded(empty_bar(stage), phase ^ 1u, abort_f, p.status))) {
             stop = true;
@@ -699,7 +698,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp >= 8) {
     // ---------------------------------------------------------------- epilogue
-    constexpr int PER = P == 2 ? 16 : 8;  // tokens at a time (32 or 24 columns)
+    constexpr int PER = 32 / P;  // tokens at a time
     const int q = warp & 3;
     int acc = 0;
     uint32_t acc_phase = 0;
@@ -755,8 +754,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               const float g = s[i];
               const float up = exchange[i * 64 + q * 32 + lane];
               const float a = Dt<T>::to_f(Dt<T>::from_f(g / (1.f + expf(-g)) * up));
-              write_terms<P>(a, p.aq + (int64_t)pos * P * p.I + col + lane, p.I,
-                             p.as + (int64_t)pos * P * ib + col / 32, ib, lane);
+              write_terms(a, p.aq + (int64_t)pos * P * (p.I / 2) + col / 2, p.I / 2,
+                          p.as + (int64_t)pos * P * ib + col / 32, ib, lane);
             }
           }
           sync_epilogue();
@@ -808,7 +807,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Bytes of shared memory beside the ring.
 size_t fixed_smem(int E, int R) {
-  return 1024 + kBarBytes + kExchange + (size_t)E * 8 + 2 * (size_t)(E + 1) * 4 + (size_t)R * 8;
+  return 1024 + kBarBytes + kExchange + (size_t)E * 20 + 4 + (size_t)R * 8;
 }
 
 // Parts of K that a down unit is cut into: enough units for four to a CTA (a CTA's last unit is
@@ -822,7 +821,6 @@ int down_splits(int64_t T, int64_t E, int64_t H, int64_t I, int k) {
 
 template <typename T>
 cudaError_t launch_t(const Mx4TokensArgs& a, cudaStream_t s) {
-  constexpr int P = Terms<T>::P;
   int dev = 0, sms = 0, most = 0;
   cudaError_t err = cudaGetDevice(&dev);
   if (err == cudaSuccess)
@@ -830,7 +828,7 @@ cudaError_t launch_t(const Mx4TokensArgs& a, cudaStream_t s) {
   if (err == cudaSuccess)
     err = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
   if (err != cudaSuccess) return err;
-  const Mx4TokensLayout l = mx4_tokens_layout(a.T, a.E, a.H, a.I, a.k, a.dt);
+  const Mx4TokensLayout l = mx4_tokens_layout(a.T, a.E, a.H, a.I, a.k);
   TokensParams p{};
   p.x = a.x;
   p.router = a.router;
@@ -859,21 +857,21 @@ cudaError_t launch_t(const Mx4TokensArgs& a, cudaStream_t s) {
   p.w = a.w;
   p.splits = down_splits(a.T, a.E, a.H, a.I, a.k);
   const int R = a.T * a.k;
-  // the ring: as many slices as fit, each with room for the columns of all T tokens
-  p.ncap = (a.T * P + kBox - 1) / kBox * kBox;
+  // the ring: as many slices as fit, each with room for the columns of the largest unit
+  p.ncap = ((a.T < kG ? a.T : kG) * P + kBox - 1) / kBox * kBox;
   const size_t fixed = fixed_smem(a.E, R);
-  const size_t stage = 2 * kA + 2 * (size_t)p.ncap * 128 + (p.ncap > 128 ? 6 : 4) * kScaleChunk;
+  const size_t stage = kA + (size_t)p.ncap * 128 + (p.ncap > 128 ? 6 : 4) * kScaleChunk;
   p.stages = (int)(((size_t)most - fixed) / stage);
   if (p.stages > kMaxStages) p.stages = kMaxStages;
   const size_t smem = fixed + (size_t)p.stages * stage;
 
   CUtensorMap mg, mu, md, mx1, mx, ma;
-  if (!make_map_codes(&mg, a.gate.codes, a.H, (int64_t)a.E * a.I, 64) ||
-      !make_map_codes(&mu, a.up.codes, a.H, (int64_t)a.E * a.I, 64) ||
-      !make_map_codes(&md, a.down.codes, a.I, (int64_t)a.E * a.H, 128) ||
-      !make_map_bytes(&mx1, p.xq, a.H, (int64_t)a.T * P, P) ||
-      !make_map_bytes(&mx, p.xq, a.H, (int64_t)a.T * P, kBox) ||
-      !make_map_bytes(&ma, p.aq, a.I, (int64_t)R * P, kBox))
+  if (!make_map_bytes(&mg, a.gate.codes, a.H / 2, (int64_t)a.E * a.I, 64) ||
+      !make_map_bytes(&mu, a.up.codes, a.H / 2, (int64_t)a.E * a.I, 64) ||
+      !make_map_bytes(&md, a.down.codes, a.I / 2, (int64_t)a.E * a.H, 128) ||
+      !make_map_bytes(&mx1, p.xq, a.H / 2, (int64_t)a.T * P, P) ||
+      !make_map_bytes(&mx, p.xq, a.H / 2, (int64_t)a.T * P, kBox) ||
+      !make_map_bytes(&ma, p.aq, a.I / 2, (int64_t)R * P, kBox))
     return cudaErrorInvalidValue;
   auto kern = moe_mx4_tokens<T>;
   err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -895,8 +893,8 @@ cudaError_t launch_t(const Mx4TokensArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-Mx4TokensLayout mx4_tokens_layout(int64_t T, int64_t E, int64_t H, int64_t I, int k, int dt) {
-  const int64_t R = T * k, P = dt == MOE_F16 ? Terms<__half>::P : Terms<__nv_bfloat16>::P;
+Mx4TokensLayout mx4_tokens_layout(int64_t T, int64_t E, int64_t H, int64_t I, int k) {
+  const int64_t R = T * k;
   Mx4TokensLayout l;
   size_t off = kWsHeader;
   auto take = [&](size_t bytes) {
@@ -908,9 +906,9 @@ Mx4TokensLayout mx4_tokens_layout(int64_t T, int64_t E, int64_t H, int64_t I, in
   l.done = take((size_t)(H / 128) * 4);
   l.zeroed = off;
   l.logits = take((size_t)T * E * 4);
-  l.xq = take((size_t)T * P * H);
+  l.xq = take((size_t)T * P * (H / 2));
   l.xs = take((size_t)T * P * (H / 32));
-  l.aq = take((size_t)R * P * I);
+  l.aq = take((size_t)R * P * (I / 2));
   l.as = take((size_t)R * P * (I / 32));
   l.y = take((size_t)R * H * 4 * down_splits(T, E, H, I, k));
   l.total = off;

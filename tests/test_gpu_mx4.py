@@ -315,23 +315,24 @@ def tokens_reference(x, router, packed, idx, w):
     xs, wt = np64(x), [M.values(p[2], p[3]) for p in packed]
     T, H, I = xs.shape[0], xs.shape[1], wt[0].shape[1]
     out, tol = np.zeros((T, H)), np.zeros((T, H))
-    u = 2.0 ** -23
+    u, term = 2.0 ** -23, 2.0 ** -14
     for t in range(T):
         for j, e in enumerate(idx[t]):
             gate, up, down = (m[e] for m in wt)
             g, v = gate @ xs[t], up @ xs[t]
-            # sums of 3 K products (the terms of x) in FP32, and terms that are exact to 2^-22 of
-            # their block's largest value
+            # sums of 5 K products (the terms of x) in FP32, and terms that together are within
+            # 2^-14 of their block's largest value: a value scaled to at most 4 is within 1/2 of a
+            # code, five terms eight times apart leave 2^-13, and the largest is at least 2
             top = np.repeat(np.abs(xs[t]).reshape(-1, 32).max(-1), 32)
-            mag_g = (3 * H + 64) * u * (np.abs(gate) @ np.abs(xs[t])) + 2 * u * (np.abs(gate) @ top)
-            mag_v = (3 * H + 64) * u * (np.abs(up) @ np.abs(xs[t])) + 2 * u * (np.abs(up) @ top)
+            mag_g = (5 * H + 64) * u * (np.abs(gate) @ np.abs(xs[t])) + term * (np.abs(gate) @ top)
+            mag_v = (5 * H + 64) * u * (np.abs(up) @ np.abs(xs[t])) + term * (np.abs(up) @ top)
             a = M.silu_mul(g, v)
             da = 1.1 * mag_g * np.abs(v) + np.abs(M.silu_mul(g, 1.0)) * mag_v + 1.1 * mag_g * mag_v
             da += eps / 2 * (np.abs(a) + da) + torch.finfo(dtype).tiny   # rounded to the type
             ar = torch.from_numpy(a).to(dtype).double().numpy()
             y = down @ a
             top = np.repeat(np.abs(ar).reshape(-1, 32).max(-1), 32)
-            dy = np.abs(down) @ (da + 2 * u * top) + (3 * I + 64) * u * (np.abs(down) @ np.abs(a))
+            dy = np.abs(down) @ (da + term * top) + (5 * I + 64) * u * (np.abs(down) @ np.abs(a))
             out[t] += w[t, j] * y
             tol[t] += w[t, j] * (dy + 64 * u * np.abs(y))
     return out, tol

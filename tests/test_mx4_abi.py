@@ -97,7 +97,7 @@ def test_tokens_rejects(L):
                 dict(E=64, k=33), dict(T=64, k=17, E=64), dict(H=0), dict(I=0),
                 dict(E=1024, H=1 << 22)):
         assert f(**bad) == 2, bad
-    assert f(H=192) == 4 and f(I=448) == 4 and f(x=FAKE + 8) == 4 and f(g=FAKE + 16) == 4
+    assert f(H=192) == 4 and f(I=448) == 4 and f(x=FAKE + 8) == 4 and f(g=FAKE + 8) == 4
     assert f(idx=FAKE + 2) == 4 and f(w=FAKE + 1) == 4
     for k in ("x", "r", "g", "gs", "out"):
         assert f(**{k: None}) == 1, k
