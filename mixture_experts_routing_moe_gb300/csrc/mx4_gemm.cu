@@ -238,6 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (stop && leader) {  // let copies still in flight land
+        const long long until = clock64() + kWaitLimit;
         for (int i = 0; i < min(armed, STAGES); ++i) {
           if (stage == 0) {
             stage = STAGES - 1;
@@ -245,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           } else {
             --stage;
           }
-          wait_drain(full_bar(stage), phase);
+          wait_until(full_bar(stage), phase, until);
         }
       }
     }

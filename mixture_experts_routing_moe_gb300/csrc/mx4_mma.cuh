@@ -77,6 +77,12 @@ static __device__ __forceinline__ void umma2_mxf4(uint32_t d_tmem, uint64_t ades
       : "memory");
 }
 
+// Waits for a phase, or until clock64() reaches `until` (after an abort, while copies land).
+static __device__ __forceinline__ void wait_until(uint32_t bar, uint32_t parity, long long until) {
+  while (!mbar_try_wait(bar, parity) && clock64() < until) {
+  }
+}
+
 // Register budget of the calling warpgroup (every warp of it executes this).
 template <int N>
 static __device__ __forceinline__ void set_max_regs_dec() {

@@ -30,8 +30,10 @@
 //      the lists) and counts the unit on its expert; a down unit's weights are loaded ahead, its
 //      tokens once that count is full.  The weight loads never wait for anything but a free slot,
 //      from the first unit to the last.
-//   3  the down epilogue writes y (FP32, one row a slot and part); whoever finishes the last unit
-//      of an output tile adds parts and slots up in order and writes out.
+//   3  the down epilogue writes y (FP32, one row a slot and part); once every CTA has counted its
+//      last unit, all of them add parts and slots up in order and write out.  (Letting whoever
+//      finished an output tile's last unit add it up put several such sums, 20 to 70 us each, on
+//      the CTAs that were late already: 775 to 1045 us for the layer of 256 experts.)
 // Waits are bounded; on expiry the status word records the timeout and every role leaves.
 //
 #include "launch.h"
@@ -95,6 +97,25 @@ __device__ __forceinline__ bool wait_count(const unsigned* c, unsigned want, vol
   }
   return true;
 }
+// A role's place in the ring.
+struct RingPos {
+  int stage = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void step(int n, int stages) {
+    stage += n;
+    while (stage >= stages) {
+      stage -= stages;
+      phase ^= 1u;
+    }
+  }
+  __device__ __forceinline__ void back(int stages) {
+    if (stage == 0) {
+      stage = stages;
+      phase ^= 1u;
+    }
+    --stage;
+  }
+};
 __device__ __forceinline__ void fence_proxy_async_all() {
   asm volatile("fence.proxy.async;" ::: "memory");
 }
@@ -227,8 +248,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t drain_bar = bar0 + 8u * (2 * kMaxStages + 4);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kMaxStages + 5);
   volatile int* abort_f = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int* last_s = reinterpret_cast<int*>(tmem_slot + 2);
-  int* active_s = reinterpret_cast<int*>(tmem_slot + 3);
+  int* active_s = reinterpret_cast<int*>(tmem_slot + 2);
+  const bool out_vec = ((uintptr_t)p.out & 7u) == 0;
 
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -412,6 +433,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     return r;
   };
 
+  // a down unit's tokens: its group's gate/up units have all been counted (every lane calls)
+  auto unit_ready = [&](int ai) {
+    bool ok = true;
+    if (lane == 0) ok = wait_count(p.ready + ai, NI, abort_f, p.status);
+    ok = __all_sync(0xFFFFFFFFu, ok);
+    fence_proxy_async_all();
+    return ok;
+  };
+
+  // Roles with two warps: each warp waits only for the slots of the slices it takes, by parity.  A
+  // slice c needs slice c - S to be consumed (S slots); the parity cannot be that of c - 2 S as
+  // long as the warp has seen c - 2 S consumed before, that is as long as its last wait was for
+  // slice c - S or later: it may leave out at most S - 1 slices at a time.  (It must not wait for
+  // the others' slots either: those move on without it, and a parity would come round again.)
+
   if (warp == 0) {
     // ---------------------------------------------------------------- weight codes
     int stage = 0;
@@ -495,71 +531,76 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (elect_one()) umma_commit(drain_bar);  // arrives once every MMA issued above has completed
     wait_drain(drain_bar, 0);
-  } else if (warp == 2) {
+  } else if (warp == 2 || warp == 3) {
     // ---------------------------------------------------------------- token terms
-    int stage = 0, armed = 0;
-    uint32_t phase = 0;
+    // the two warps take the slices in turn: what one does for a slice (a wait, the barrier, the
+    // loads) is a chain of some 600 cycles
+    const int mine = warp - 2;
+    RingPos at;
+    int armed = 0, turn = 0;
     bool stop = false;
     const uint64_t pol = policy_evict_normal();
     fence_proxy_async_all();  // xq was written by other CTAs before the grid barrier
     for (int u = blockIdx.x; u < total && !stop; u += gridDim.x) {
       const Unit r = unit_of(u);
-      if (r.down) {
-        bool ok = true;
-        if (lane == 0) ok = wait_count(p.ready + r.ai, NI, abort_f, p.status);
-        if (!__all_sync(0xFFFFFFFFu, ok)) {
-          stop = true;
-          break;
-        }
-        fence_proxy_async_all();
+      if (r.down && !unit_ready(r.ai)) {
+        stop = true;
+        break;
       }
-      const bool whole = r.down || r.all;                // contiguous rows, boxes of 16
+      const bool whole = r.down || r.all;              // contiguous rows, boxes of 16
       const int boxes = whole ? (r.cols + kBox - 1) / kBox : r.n;
-      const int bytes = whole ? kBox * 128 : P * 128;    // of a box
-      const int row0 = r.down ? r.first * P : 0;
-      for (int k = r.k0; k < r.k1; ++k) {
+      const int bytes = whole ? kBox * 128 : P * 128;  // of a box
+      // first rows of boxes lane and lane + 32 (at most kG boxes)
+      int box_row[2];
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        const int i = lane + 32 * z;
+        box_row[z] = whole ? (r.down ? r.first * P : 0) + i * kBox
+                     : i < r.n ? (int)list[r.first + i] / p.k * P : 0;
+      }
+      const CUtensorMap* m = r.down ? &mapA : r.all ? &mapX : &mapX1;
+      for (int k = r.k0; k < r.k1; ++k, turn ^= 1) {
+        if (turn != mine) {
+          at.step(1, p.stages);
+          continue;
+        }
         if (!__all_sync(0xFFFFFFFFu,
-                        wait_bounded(empty_bar(stage), phase ^ 1u, abort_f, p.status))) {
+                        wait_bounded(empty_bar(at.stage), at.phase ^ 1u, abort_f, p.status))) {
           stop = true;
           break;
         }
-        const uint32_t sb = base + stage * stage_bytes + kA, fb = full_bar(stage);
-        const CUtensorMap* m = r.down ? &mapA : r.all ? &mapX : &mapX1;
+        const uint32_t sb = base + at.stage * stage_bytes + kA, fb = full_bar(at.stage);
         if (elect_one()) mbar_expect_tx(fb, boxes * bytes);
         __syncwarp();
         for (int i = 0; i < boxes; ++i) {
-          const int row = whole ? row0 + i * kBox : (int)list[r.first + i] / p.k * P;
+          const int row = __shfl_sync(0xFFFFFFFFu, i < 32 ? box_row[0] : box_row[1], i & 31);
           if (elect_one()) tma_load_2d(sb + i * bytes, m, fb, k * 128, row, pol);
         }
         ++armed;
-        if (++stage == p.stages) {
-          stage = 0;
-          phase ^= 1u;
-        }
+        at.step(1, p.stages);
       }
     }
     if (stop) {  // let copies still in flight land
-      for (int i = 0; i < min(armed, p.stages); ++i) {
-        if (stage == 0) {
-          stage = p.stages - 1;
-          phase ^= 1u;
-        } else {
-          --stage;
-        }
-        wait_drain(full_bar(stage), phase);
+      const long long until = clock64() + kWaitLimit;
+      for (int i = 0; i < p.stages && armed > 0; ++i) {
+        at.back(p.stages);
+        wait_until(full_bar(at.stage), at.phase, until);
       }
     }
-  } else if (warp == 4) {
+  } else if (warp == 4 || warp == 6) {
     // ---------------------------------------------------------------- weight scales
-    // lane l holds rows l, l + 32, l + 64, l + 96 of the unit's 128, four slices (32 bytes) each
-    int stage = 0;
-    uint32_t phase = 0;
+    // lane l holds rows l, l + 32, l + 64, l + 96 of the unit's 128, four slices (32 bytes) each;
+    // the two warps take these parts in turn, and each loads its next part ahead; with fewer than
+    // five slots a part is two slices
+    const int mine = warp == 6, per = p.stages >= 5 ? 4 : 2;
+    RingPos at;
+    int turn = 0;
     bool stop = false;
     uint32_t next[4][8];
     auto load = [&](int u, int part) {
       const Unit r = unit_of(u);
       const int pitch = (r.down ? p.I : p.H) / 32;
-      const int at0 = r.k0 * 8 + part * 32, left = min(r.k1 * 8, pitch) - at0;
+      const int at0 = r.k0 * 8 + part * per * 8, left = min(r.k1 * 8, pitch) - at0;
       const bool vec = p.scales_vec && ((pitch | at0) & 15) == 0;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -583,54 +624,68 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     };
-    if (blockIdx.x < total) load(blockIdx.x, 0);
+    auto parts_of = [&](int u) {
+      const Unit r = unit_of(u);
+      return (r.k1 - r.k0 + per - 1) / per;
+    };
+    // the next part of this warp: (un, pn), two parts on from the last; false past the end
+    int un = blockIdx.x, pn = mine, left_n = un < total ? parts_of(un) : 0;
+    auto settle = [&]() {
+      while (un < total && pn >= left_n) {
+        pn -= left_n;
+        un += gridDim.x;
+        if (un < total) left_n = parts_of(un);
+      }
+      return un < total;
+    };
+    if (settle()) load(un, pn);
     for (int u = blockIdx.x; u < total && !stop; u += gridDim.x) {
       const Unit r = unit_of(u);
-      const int slices = r.k1 - r.k0, parts = (slices + 3) / 4;
-      for (int part = 0; part < parts && !stop; ++part) {
+      const int slices = r.k1 - r.k0, parts = (slices + per - 1) / per;
+      for (int part = 0; part < parts && !stop; ++part, turn ^= 1) {
+        const int count = min(per, slices - part * per);
+        if (turn != mine) {
+          at.step(count, p.stages);
+          continue;
+        }
         uint32_t now[4][8];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
           for (int i = 0; i < 8; ++i) now[j][i] = next[j][i];
-        if (part + 1 < parts) load(u, part + 1);
-        else if (u + (int)gridDim.x < total) load(u + gridDim.x, 0);
+        pn += 2;
+        if (settle()) load(un, pn);
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
-          if (part * 4 + i / 2 >= slices || stop) continue;
+          if (i / 2 >= count || stop) continue;
           if (!__all_sync(0xFFFFFFFFu,
-                          wait_bounded(empty_bar(stage), phase ^ 1u, abort_f, p.status))) {
+                          wait_bounded(empty_bar(at.stage), at.phase ^ 1u, abort_f, p.status))) {
             stop = true;
             continue;
           }
-          const uint32_t sf = sf_base + stage * sf_bytes + lane * 16;
+          const uint32_t sf = sf_base + at.stage * sf_bytes + lane * 16;
           st_shared_v4(sf, now[0][i], now[1][i], now[2][i], now[3][i]);
           st_shared_v4(sf + kScaleChunk, now[0][i + 1], now[1][i + 1], now[2][i + 1],
                        now[3][i + 1]);
           fence_proxy_async_smem();
           __syncwarp();
-          if (elect_one()) mbar_arrive(full_bar(stage));
-          if (++stage == p.stages) {
-            stage = 0;
-            phase ^= 1u;
-          }
+          if (elect_one()) mbar_arrive(full_bar(at.stage));
+          at.step(1, p.stages);
         }
       }
     }
-  } else if (warp == 5) {
+  } else if (warp == 5 || warp == 7) {
     // ---------------------------------------------------------------- token scales
-    // lane l holds the terms in columns l, l + 32, ..., l + 160, two slices (16 bytes) each
+    // lane l holds the terms in columns l, l + 32, ..., l + 160, two slices (16 bytes) each; the
+    // two warps take these pairs in turn
     constexpr int J = kMaxN / 32;
-    int stage = 0;
-    uint32_t phase = 0;
+    const int mine = warp == 7;
+    RingPos at;
+    int turn = 0;
     bool stop = false;
     for (int u = blockIdx.x; u < total && !stop; u += gridDim.x) {
       const Unit r = unit_of(u);
-      if (r.down) {
-        bool ok = true;
-        if (lane == 0) ok = wait_count(p.ready + r.ai, NI, abort_f, p.status);
-        if (!__all_sync(0xFFFFFFFFu, ok)) break;
-      }
+      if (r.down && !unit_ready(r.ai)) break;
       const int pitch = (r.down ? p.I : p.H) / 32;
       const uint8_t* src[J];
 #pragma unroll
@@ -661,23 +716,28 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       };
-      load(r.k0);
-      for (int k = r.k0; k < r.k1 && !stop; k += 2) {
+      const int ahead = turn == mine ? r.k0 : r.k0 + 2;  // this warp's first pair
+      if (ahead < r.k1) load(ahead);
+      for (int k = r.k0; k < r.k1 && !stop; k += 2, turn ^= 1) {
+        if (turn != mine) {
+          at.step(min(2, r.k1 - k), p.stages);
+          continue;
+        }
         uint32_t now[J][4];
 #pragma unroll
         for (int j = 0; j < J; ++j)
 #pragma unroll
           for (int i = 0; i < 4; ++i) now[j][i] = next[j][i];
-        if (k + 2 < r.k1) load(k + 2);
+        if (k + 4 < r.k1) load(k + 4);
 #pragma unroll
         for (int i = 0; i < 4; i += 2) {
           if (k + i / 2 >= r.k1 || stop) continue;
           if (!__all_sync(0xFFFFFFFFu,
-                          wait_bounded(empty_bar(stage), phase ^ 1u, abort_f, p.status))) {
+                          wait_bounded(empty_bar(at.stage), at.phase ^ 1u, abort_f, p.status))) {
             stop = true;
             continue;
           }
-          const uint32_t sf = sf_base + stage * sf_bytes + 2 * kScaleChunk + lane * 16;
+          const uint32_t sf = sf_base + at.stage * sf_bytes + 2 * kScaleChunk + lane * 16;
           const uint32_t half = b_chunks * kScaleChunk;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -688,11 +748,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           fence_proxy_async_smem();
           __syncwarp();
-          if (elect_one()) mbar_arrive(full_bar(stage));
-          if (++stage == p.stages) {
-            stage = 0;
-            phase ^= 1u;
-          }
+          if (elect_one()) mbar_arrive(full_bar(at.stage));
+          at.step(1, p.stages);
         }
       }
     }
@@ -773,25 +830,47 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (threadIdx.x == 8 * 32) atomicAdd(p.ready + r.ai, 1u);
         continue;
       }
+    }
+    // 3. every CTA's y is written: the sums over slots, four columns a thread
+    __threadfence();
+    sync_epilogue();
+    bool ok = true;
+    if (threadIdx.x == 8 * 32) {
+      atomicAdd(p.done, 1u);
+      ok = wait_count(p.done, gridDim.x, abort_f, p.status);
+    }
+    if (!any_of_epilogue(!ok)) {
       __threadfence();
-      sync_epilogue();
-      if (threadIdx.x == 8 * 32)
-        *last_s = atomicAdd(p.done + r.tile, 1u) + 1 == (unsigned)(active * p.splits);
-      sync_epilogue();
-      if (*last_s) {
-        __threadfence();
-        const int h = r.tile * 128 + (int)threadIdx.x - 8 * 32;
-        T* out = (T*)p.out + h;
-        for (int t = 0; t < p.T; ++t) {
-          float s = 0.f;
-          const float* y = p.y + (int64_t)t * p.k * p.H + h;
+      const int quads = p.H / 4, threads = gridDim.x * 128;
+      const int64_t split = (int64_t)R * p.H;
+      for (int i = blockIdx.x * 128 + (int)threadIdx.x - 8 * 32; i < p.T * quads; i += threads) {
+        const int t = i / quads, h = (i - t * quads) * 4;
+        const float* y = p.y + (int64_t)t * p.k * p.H + h;
+        const float* w = sel_w + t * p.k;
+        float s[4] = {};
 #pragma unroll 8
-          for (int j = 0; j < p.k; ++j) {
-            float v = __ldcg(y + (int64_t)j * p.H);
-            for (int z = 1; z < p.splits; ++z) v += __ldcg(y + ((int64_t)z * R + j) * p.H);
-            s = fmaf(sel_w[t * p.k + j], v, s);
+        for (int j = 0; j < p.k; ++j) {
+          float4 v = __ldcg(reinterpret_cast<const float4*>(y + (int64_t)j * p.H));
+          for (int z = 1; z < p.splits; ++z) {
+            const float4 q =
+                __ldcg(reinterpret_cast<const float4*>(y + z * split + (int64_t)j * p.H));
+            v.x += q.x, v.y += q.y, v.z += q.z, v.w += q.w;
           }
-          out[(int64_t)t * p.H] = Dt<T>::from_f(s);
+          s[0] = fmaf(w[j], v.x, s[0]), s[1] = fmaf(w[j], v.y, s[1]);
+          s[2] = fmaf(w[j], v.z, s[2]), s[3] = fmaf(w[j], v.w, s[3]);
+        }
+        T* out = (T*)p.out + (int64_t)t * p.H + h;
+        if (out_vec) {
+          union {
+            uint2 u;
+            T e[4];
+          } o;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) o.e[c] = Dt<T>::from_f(s[c]);
+          *reinterpret_cast<uint2*>(out) = o.u;
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) out[c] = Dt<T>::from_f(s[c]);
         }
       }
     }
@@ -863,6 +942,7 @@ cudaError_t launch_t(const Mx4TokensArgs& a, cudaStream_t s) {
   const size_t stage = kA + (size_t)p.ncap * 128 + (p.ncap > 128 ? 6 : 4) * kScaleChunk;
   p.stages = (int)(((size_t)most - fixed) / stage);
   if (p.stages > kMaxStages) p.stages = kMaxStages;
+  if (p.stages < 3) return cudaErrorInvalidConfiguration;  // (roles leave out two slices at a time)
   const size_t smem = fixed + (size_t)p.stages * stage;
 
   CUtensorMap mg, mu, md, mx1, mx, ma;
@@ -903,7 +983,7 @@ Mx4TokensLayout mx4_tokens_layout(int64_t T, int64_t E, int64_t H, int64_t I, in
     return o;
   };
   l.ready = take((size_t)R * 4);
-  l.done = take((size_t)(H / 128) * 4);
+  l.done = take(4);
   l.zeroed = off;
   l.logits = take((size_t)T * E * 4);
   l.xq = take((size_t)T * P * (H / 2));

@@ -373,7 +373,8 @@ def check_tokens(T, E, H, I, k, dtype, renorm, seed):
     (1, 1, 128, 128, 1, True), (1, 8, 256, 384, 2, True), (3, 5, 640, 128, 5, False),
     (8, 16, 512, 256, 4, True), (9, 33, 128, 640, 3, False), (33, 2, 256, 128, 2, True),
     (64, 6, 384, 256, 2, True), (64, 64, 128, 128, 16, True), (17, 200, 256, 128, 8, True),
-    (5, 1024, 128, 128, 32, False), (40, 1, 1152, 1280, 1, True)])
+    (5, 1024, 128, 128, 32, False), (40, 1, 1152, 1280, 1, True),
+    (64, 1, 256, 384, 1, True), (39, 3, 128, 2176, 2, True), (38, 2, 640, 1152, 1, False)])
 def test_tokens(dtype, T, E, H, I, k, renorm):
     check_tokens(T, E, H, I, k, dtype, renorm, T * 1000 + E + H + I)
 
