@@ -93,8 +93,8 @@ int moe_mx4_experts_forward_dispatched(const void* x_d, int xdt, const int32_t* 
  * above.  The activations are not quantised: they enter the products to within 2^-14 of the
  * largest value of their block of 32.  A token holding an infinity or a NaN gets NaN.
  * idx [T, top_k] uint32 and w [T, top_k] float receive the selection; either may be NULL.
- * One cooperative launch (after a small memset of the workspace's counters); if its CTAs cannot
- * all be resident (another context holds SMs) the call returns MOE_ERR_CUDA.
+ * Two launches, the second a cooperative one; if its CTAs cannot all be resident (another context
+ * holds SMs) the call returns MOE_ERR_CUDA.
  * Limits: T <= 64, top_k <= min(E, 32), T * top_k <= 1024 (else MOE_ERR_SHAPE); H and I multiples
  * of 128, x and router 16-byte aligned (else MOE_ERR_ALIGN).
  * ws: at least moe_mx4_tokens_workspace_bytes(...) bytes (0 for sizes out of range), 256-byte

@@ -86,8 +86,8 @@ cudaError_t launch_mx4_gate_up(Mx4Rows a, int64_t rows, Mx4Rows gate, Mx4Rows up
                                uint8_t* scales, unsigned* status, cudaStream_t s);
 
 
-// The whole layer for a few tokens (one cooperative launch).  ws holds tokens_layout().total bytes;
-// its first `zeroed` bytes are cleared by the launch.
+// The whole layer for a few tokens.  ws holds tokens_layout().total bytes; its first `zeroed` bytes
+// are cleared by the first launch.
 struct Mx4TokensLayout {
   size_t ready, done, zeroed;      // counters behind the header
   size_t logits, xq, xs, aq, as, y, total;

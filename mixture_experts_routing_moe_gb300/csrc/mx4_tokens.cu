@@ -1,5 +1,5 @@
-// A whole MoE layer for a few tokens with microscaled 4-bit expert weights, in one cooperative
-// launch: router logits, top-k, gate/up, SwiGLU, down and combine.
+// A whole MoE layer for a few tokens with microscaled 4-bit expert weights, in two launches: the
+// router logits; then top-k, gate/up, SwiGLU, down and combine in a cooperative one.
 //
 //   logits[t, e] = x[t] . router[e];  idx, w as moe_route (softmax over all experts, ties to the
 //   lower id);  a = round16(silu(x gate_e^T) * (x up_e^T));  out[t] = sum_j w[t, j] (a_j down_e^T)
@@ -18,9 +18,10 @@
 // shared memory: the TMA unit handles rows of 64 packed bytes, and half as many bytes are in
 // flight.  The layer of 256 experts took 1.08 ms that way.)
 //
-// Steps.  One CTA per SM, all resident; grid-wide hand-overs go through counters in global memory:
-//   0  every CTA splits its share of x into terms (xq, xs) and computes the logits of its experts;
-//      grid barrier.
+// Steps.
+//   0  (first launch) terms of x (xq, xs), router logits, counters cleared.
+// The second launch has one CTA per SM, all resident; hand-overs between CTAs go through counters
+// in global memory.
 //   1  every CTA selects the top-k of all tokens for itself (the same arithmetic everywhere) and
 //      lists the active experts' tokens in shared memory, expert by expert.
 //   2  units of work: (expert, 64 columns of a) for gate/up, then (expert, 128 columns of the
@@ -70,7 +71,8 @@ struct TokensParams {
   float* logits;
   uint8_t *xq, *xs, *aq, *as;
   float* y;
-  unsigned *status, *grid_count, *ready, *done;
+  unsigned *status, *ready, *done;
+  size_t zeroed;  // words of counters behind `status`
   void* out;
   uint32_t* idx;
   float* w;
@@ -207,6 +209,74 @@ __device__ __forceinline__ void select_row(const float* row, int E, int k, int r
   if (lane < k) ws[lane] = mine / (renorm ? sel : s);
 }
 
+// Step 0: CTAs below logit_ctas compute the logits of kEB experts and kTB tokens, its warps an
+// eighth of H each; the others write the terms of x, a block of 32 values a warp.  CTA 0 clears
+// the counters.
+constexpr int kEB = 4, kTB = 8, kFirstWarps = 8;
+template <typename T>
+__global__ void __launch_bounds__(kFirstWarps * 32)
+    moe_mx4_tokens_first(const TokensParams p, int logit_ctas) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (blockIdx.x == 0)
+    for (size_t i = threadIdx.x; i < p.zeroed; i += kFirstWarps * 32) p.status[i] = 0;
+  const T* x = (const T*)p.x;
+  if ((int)blockIdx.x >= logit_ctas) {
+    const int hb = p.H / 32, b = ((int)blockIdx.x - logit_ctas) * kFirstWarps + warp;
+    if (b >= p.T * hb) return;
+    const int t = b / hb, c = b - t * hb;
+    const float v = Dt<T>::to_f(x[(int64_t)t * p.H + c * 32 + lane]);
+    write_terms(v, p.xq + (int64_t)t * P * (p.H / 2) + c * 16, p.H / 2,
+                p.xs + (int64_t)t * P * hb + c, hb, lane);
+    return;
+  }
+  __shared__ float red[kFirstWarps][kEB * kTB];
+  const int eb = (p.E + kEB - 1) / kEB;
+  const int e0 = blockIdx.x % eb * kEB, t0 = blockIdx.x / eb * kTB;
+  const T* router = (const T*)p.router;
+  const T *r[kEB], *xt[kTB];
+#pragma unroll
+  for (int i = 0; i < kEB; ++i) r[i] = router + (int64_t)min(e0 + i, p.E - 1) * p.H;
+#pragma unroll
+  for (int i = 0; i < kTB; ++i) xt[i] = x + (int64_t)min(t0 + i, p.T - 1) * p.H;
+  const int nt = min(kTB, p.T - t0);
+  float acc[kEB][kTB] = {};
+  for (int v = threadIdx.x; v < p.H / 8; v += kFirstWarps * 32) {
+    Vec16<T> a[kEB], q[kTB];
+#pragma unroll
+    for (int i = 0; i < kEB; ++i) a[i].u = ld_nc_v4(r[i] + v * 8);
+#pragma unroll
+    for (int i = 0; i < kTB; ++i)
+      if (i < nt) q[i].u = ld_nc_v4(xt[i] + v * 8);
+#pragma unroll
+    for (int i = 0; i < kTB; ++i) {
+      if (i >= nt) continue;
+      float xf[8];
+      q[i].to_float(xf);
+#pragma unroll
+      for (int j = 0; j < kEB; ++j) {
+#pragma unroll
+        for (int z = 0; z < 8; ++z) acc[j][i] = fmaf(xf[z], Dt<T>::to_f(a[j].e[z]), acc[j][i]);
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kEB; ++j)
+#pragma unroll
+    for (int i = 0; i < kTB; ++i) {
+      if (i >= nt) continue;
+      const float s = group_sum<32>(acc[j][i]);
+      if (lane == 0) red[warp][j * kTB + i] = s;
+    }
+  __syncthreads();
+  const int j = threadIdx.x / kTB, i = threadIdx.x % kTB;
+  if (j < kEB && e0 + j < p.E && i < nt) {
+    float s = 0.f;
+#pragma unroll
+    for (int w = 0; w < kFirstWarps; ++w) s += red[w][threadIdx.x];
+    p.logits[(int64_t)(t0 + i) * p.E + e0 + j] = s;
+  }
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 1)
     moe_mx4_tokens(const __grid_constant__ CUtensorMap mapG, const __grid_constant__ CUtensorMap mapU,
@@ -238,7 +308,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   at += R * 4;
   uint16_t* sel_id = reinterpret_cast<uint16_t*>(at);
   uint16_t* list = sel_id + R;  // slots t * k + j, expert by expert, by token
-  float* red = reinterpret_cast<float*>(mx4_smem_raw + (base - raw));  // step 0 only: in the ring
 
   const uint32_t bar0 = smem_u32(bars);
   auto full_bar = [&](int s) { return bar0 + 8u * s; };
@@ -275,98 +344,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_alloc(smem_u32(tmem_slot), kTmemCols);
   for (int e = threadIdx.x; e < p.E; e += kThreads) mask[e] = 0;
 
-  // ------------------------------------------------ 0. terms of x, router logits
-  const T* x = (const T*)p.x;
-  const T* router = (const T*)p.router;
-  {
-    const int hb = p.H / 32;
-    for (int b = blockIdx.x * kWarps + warp; b < p.T * hb; b += gridDim.x * kWarps) {
-      const int t = b / hb, c = b - t * hb;
-      const float v = Dt<T>::to_f(x[(int64_t)t * p.H + c * 32 + lane]);
-      write_terms(v, p.xq + (int64_t)t * P * (p.H / 2) + c * 16, p.H / 2,
-                  p.xs + (int64_t)t * P * hb + c, hb, lane);
-    }
-    // two experts and four tokens at a time: eight sums from six 16-byte loads
-    constexpr int TB = 4, EB = 2;
-    for (int e = blockIdx.x; e < p.E; e += EB * gridDim.x) {
-      const int e1 = min(e + (int)gridDim.x, p.E - 1);
-      const T* r0 = router + (int64_t)e * p.H;
-      const T* r1 = router + (int64_t)e1 * p.H;
-      for (int t0 = 0; t0 < p.T; t0 += TB) {
-        float acc[EB][TB] = {};
-        const T* xt[TB];
-#pragma unroll
-        for (int i = 0; i < TB; ++i) xt[i] = x + (int64_t)min(t0 + i, p.T - 1) * p.H;
-#pragma unroll 3
-        for (int v = threadIdx.x; v < p.H / 8; v += kThreads) {
-          Vec16<T> a, b, q[TB];
-          a.u = ld_nc_v4(r0 + v * 8);
-          b.u = ld_nc_v4(r1 + v * 8);
-#pragma unroll
-          for (int i = 0; i < TB; ++i) q[i].u = ld_nc_v4(xt[i] + v * 8);
-          float af[8], bf[8];
-          a.to_float(af);
-          b.to_float(bf);
-#pragma unroll
-          for (int i = 0; i < TB; ++i) {
-            float xf[8];
-            q[i].to_float(xf);
-#pragma unroll
-            for (int z = 0; z < 8; ++z) {
-              acc[0][i] = fmaf(xf[z], af[z], acc[0][i]);
-              acc[1][i] = fmaf(xf[z], bf[z], acc[1][i]);
-            }
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < TB; ++i) {
-          const float s0 = group_sum<32>(acc[0][i]), s1 = group_sum<32>(acc[1][i]);
-          if (lane == 0) {
-            red[(t0 + i) * kWarps + warp] = s0;
-            red[(64 + t0 + i) * kWarps + warp] = s1;
-          }
-        }
-      }
-      __syncthreads();
-      const int z = threadIdx.x >> 6, t = threadIdx.x & 63;  // expert of the two, token
-      if (z < EB && t < p.T && e + z * (int)gridDim.x < p.E) {
-        float s = 0.f;
-        for (int w = 0; w < kWarps; ++w) s += red[(z * 64 + t) * kWarps + w];
-        p.logits[(int64_t)t * p.E + e + z * gridDim.x] = s;
-      }
-      __syncthreads();
-    }
-  }
-  fence_proxy_async_all();  // xq is read by TMA
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    __threadfence();
-    atomicAdd(p.grid_count, 1u);
-    wait_count(p.grid_count, gridDim.x, abort_f, p.status);
-    __threadfence();
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
   // ------------------------------------------------ 1. top-k, lists of the experts' tokens
-  const bool go = !*abort_f;
-  if (go) {
-    for (int t = warp; t < p.T; t += kWarps) {
-      const float* row = p.logits + (int64_t)t * p.E;
-      uint16_t* ids = sel_id + t * p.k;
-      float* ws = sel_w + t * p.k;
-      if (p.E <= 128) select_row<4>(row, p.E, p.k, p.renorm, lane, ids, ws);
-      else if (p.E <= 256) select_row<8>(row, p.E, p.k, p.renorm, lane, ids, ws);
-      else select_row<32>(row, p.E, p.k, p.renorm, lane, ids, ws);
-      __syncwarp();
-      if (lane < p.k) {
-        atomicOr(mask + ids[lane], 1ull << t);
-        if (blockIdx.x == 0) {
-          if (p.idx) p.idx[t * p.k + lane] = ids[lane];
-          if (p.w) p.w[t * p.k + lane] = ws[lane];
-        }
+  for (int t = warp; t < p.T; t += kWarps) {
+    const float* row = p.logits + (int64_t)t * p.E;
+    uint16_t* ids = sel_id + t * p.k;
+    float* ws = sel_w + t * p.k;
+    if (p.E <= 128) select_row<4>(row, p.E, p.k, p.renorm, lane, ids, ws);
+    else if (p.E <= 256) select_row<8>(row, p.E, p.k, p.renorm, lane, ids, ws);
+    else select_row<32>(row, p.E, p.k, p.renorm, lane, ids, ws);
+    __syncwarp();
+    if (lane < p.k) {
+      atomicOr(mask + ids[lane], 1ull << t);
+      if (blockIdx.x == 0) {
+        if (p.idx) p.idx[t * p.k + lane] = ids[lane];
+        if (p.w) p.w[t * p.k + lane] = ws[lane];
       }
     }
   }
@@ -390,17 +386,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) start[p.E] = carry, *active_s = n_act;
   }
   __syncthreads();
-  if (go) {
-    for (int s = threadIdx.x; s < R; s += kThreads) {
-      const int e = sel_id[s], t = s / p.k;
-      list[start[e] + __popcll(mask[e] & ((1ull << t) - 1))] = (uint16_t)s;
-    }
+  for (int s = threadIdx.x; s < R; s += kThreads) {
+    const int e = sel_id[s], t = s / p.k;
+    list[start[e] + __popcll(mask[e] & ((1ull << t) - 1))] = (uint16_t)s;
   }
   __syncthreads();
 
   // ------------------------------------------------ 2. units
   const int NI = p.I / 64, NH = p.H / 128;
-  const int active = go ? *active_s : 0;
+  const int active = *active_s;
   const int n1 = active * NI, per_down = NH * p.splits, total = n1 + active * per_down;
   struct Unit {
     bool down;
@@ -540,7 +534,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     int armed = 0, turn = 0;
     bool stop = false;
     const uint64_t pol = policy_evict_normal();
-    fence_proxy_async_all();  // xq was written by other CTAs before the grid barrier
     for (int u = blockIdx.x; u < total && !stop; u += gridDim.x) {
       const Unit r = unit_of(u);
       if (r.down && !unit_ready(r.ai)) {
@@ -828,7 +821,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         __threadfence();
         sync_epilogue();
         if (threadIdx.x == 8 * 32) atomicAdd(p.ready + r.ai, 1u);
-        continue;
       }
     }
     // 3. every CTA's y is written: the sums over slots, four columns a thread
@@ -922,7 +914,6 @@ cudaError_t launch_t(const Mx4TokensArgs& a, cudaStream_t s) {
   p.ds = a.down.scales;
   p.scales_vec = (((uintptr_t)p.gs | (uintptr_t)p.us | (uintptr_t)p.ds) & 15u) == 0;
   p.status = (unsigned*)a.ws;
-  p.grid_count = (unsigned*)(a.ws + 64);
   p.ready = (unsigned*)(a.ws + l.ready);
   p.done = (unsigned*)(a.ws + l.done);
   p.logits = (float*)(a.ws + l.logits);
@@ -931,6 +922,7 @@ cudaError_t launch_t(const Mx4TokensArgs& a, cudaStream_t s) {
   p.aq = a.ws + l.aq;
   p.as = a.ws + l.as;
   p.y = (float*)(a.ws + l.y);
+  p.zeroed = l.zeroed / 4;
   p.out = a.out;
   p.idx = a.idx;
   p.w = a.w;
@@ -956,7 +948,11 @@ cudaError_t launch_t(const Mx4TokensArgs& a, cudaStream_t s) {
   auto kern = moe_mx4_tokens<T>;
   err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return err;
-  err = cudaMemsetAsync(a.ws, 0, l.zeroed, s);
+  const int logit_ctas = (a.E + kEB - 1) / kEB * ((a.T + kTB - 1) / kTB);
+  const int64_t blocks = (int64_t)a.T * (a.H / 32);
+  const int split_ctas = (int)((blocks + kFirstWarps - 1) / kFirstWarps);
+  moe_mx4_tokens_first<T><<<logit_ctas + split_ctas, kFirstWarps * 32, 0, s>>>(p, logit_ctas);
+  err = cudaGetLastError();
   if (err != cudaSuccess) return err;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeCooperative;
