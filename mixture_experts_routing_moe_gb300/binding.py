@@ -8,6 +8,7 @@ in libmoe's kernels; there is no CPU path.  A missing or unbuilt library raises 
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 
@@ -119,8 +120,10 @@ def _ptr(t):
 
 
 def _stream(stream):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return s.cuda_stream
+    # the current stream's handle without a Stream object around it (3 us a call)
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream
 
 
 def _cuda(*ts):
@@ -399,6 +402,9 @@ def moe_device_status(ws, stream=None) -> int:
 
 
 # ------------------------------------------------------------- microscaled 4-bit (moe_mx4.h)
+# Small calls take a few microseconds on the GPU, so the checks below are kept to the attributes
+# they need; sizes that follow from other sizes are remembered.
+@functools.lru_cache(maxsize=4096)
 def _mx4_pitch(K: int):
     """(bytes of codes, bytes of scales) of a row of K values."""
     blocks = -(-K // 32)
@@ -406,13 +412,31 @@ def _mx4_pitch(K: int):
 
 
 def _mx4_rows(codes, scales, K: int, where: str):
-    """Checks one operand in blocks: [..., rows] rows of K values."""
-    _cuda(codes, scales)
+    """Checks one operand in blocks, [..., rows] rows of K values; returns the shape of codes."""
+    if not (codes.is_cuda and scales.is_cuda and codes.is_contiguous() and scales.is_contiguous()):
+        raise ValueError("libmoe takes contiguous CUDA tensors")
     if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
         raise MoeError(3, f"{where}: codes and scales are uint8")
-    pc, ps = _mx4_pitch(K)
-    if codes.shape[-1] != pc or scales.shape != codes.shape[:-1] + (ps,):
-        raise MoeError(2, f"{where}: rows of {K} values have {pc} code bytes and {ps} scale bytes")
+    shape = codes.shape
+    if (shape[-1], scales.shape[-1]) != _mx4_pitch(K) or scales.shape[:-1] != shape[:-1]:
+        raise MoeError(2, f"{where}: rows of {K} values have {_mx4_pitch(K)} bytes of codes and "
+                          "scales")
+    return shape
+
+
+def _mx4_leading(t, K: int, where: str) -> int:
+    """Elements from one row of K consecutive values to the next."""
+    if t.is_cuda:
+        if t.is_contiguous():
+            return K
+        if t.dim() == 2 and t.stride(1) == 1 and t.stride(0) >= K:
+            return t.stride(0)
+    raise ValueError(f"{where} takes CUDA rows of consecutive values")
+
+
+def _mx4_dtype(t) -> int:
+    code = DTYPE_CODE.get(t.dtype)
+    return _code(t) if code is None else code
 
 
 def _mx4_ws(ws, need: int, device):
@@ -425,42 +449,47 @@ def _mx4_ws(ws, need: int, device):
 def moe_mx4_quantize(x, codes=None, scales=None, stream=None):
     """Rows of x [..., K] to blocks -> (codes uint8 [..., 16 ceil(K/32)], scales uint8
     [..., 4 ceil(K/128)]).  x is contiguous, or two-dimensional with rows a stride apart."""
-    K = x.shape[-1]
-    if not x.is_cuda or not (x.is_contiguous() or (x.dim() == 2 and x.stride(1) == 1
-                                                   and x.stride(0) >= K)):
-        raise ValueError("moe_mx4_quantize takes CUDA rows of consecutive values")
-    dt = _code(x)
-    rows = x.numel() // K if K else 0
+    shape = x.shape
+    K = shape[-1]
+    ld = _mx4_leading(x, K, "moe_mx4_quantize")
+    dt = _mx4_dtype(x)
+    given = codes is not None or scales is not None
     pc, ps = _mx4_pitch(K)
-    lead = x.shape[:-1]
+    lead = (shape[0],) if len(shape) == 2 else shape[:-1]
     if codes is None:
-        codes = torch.empty(lead + (pc,), dtype=torch.uint8, device=x.device)
+        codes = torch.empty((*lead, pc), dtype=torch.uint8, device=x.device)
     if scales is None:
-        scales = torch.empty(lead + (ps,), dtype=torch.uint8, device=x.device)
-    _mx4_rows(codes, scales, K, "moe_mx4_quantize")
-    if codes.shape[:-1] != lead:
+        scales = torch.empty((*lead, ps), dtype=torch.uint8, device=x.device)
+    if given and _mx4_rows(codes, scales, K, "moe_mx4_quantize")[:-1] != shape[:-1]:
         raise MoeError(2, "moe_mx4_quantize: codes have other rows than x")
-    ld = K if x.is_contiguous() else x.stride(0)
-    _check(lib().moe_mx4_quantize(x.data_ptr(), dt, rows, K, ld, codes.data_ptr(),
-                                  scales.data_ptr(), _stream(stream)), "moe_mx4_quantize")
+    _check(lib().moe_mx4_quantize(x.data_ptr(), dt, x.numel() // K if K else 0, K, ld,
+                                  codes.data_ptr(), scales.data_ptr(), _stream(stream)),
+           "moe_mx4_quantize")
     return codes, scales
 
 
 def moe_mx4_dequantize(codes, scales, K: int, dtype=torch.bfloat16, out=None, stream=None):
     """The values of rows of K values in blocks -> out [..., K] of dtype."""
-    _mx4_rows(codes, scales, K, "moe_mx4_dequantize")
+    shape = _mx4_rows(codes, scales, K, "moe_mx4_dequantize")
     if out is None:
-        out = torch.empty(codes.shape[:-1] + (K,), dtype=dtype, device=codes.device)
-    elif out.shape != codes.shape[:-1] + (K,):
-        raise MoeError(2, "moe_mx4_dequantize: out has another shape")
-    elif not out.is_cuda or not (out.is_contiguous() or (out.dim() == 2 and out.stride(1) == 1
-                                                         and out.stride(0) >= K)):
-        raise ValueError("moe_mx4_dequantize writes CUDA rows of consecutive values")
-    rows = out.numel() // K if K else 0
-    ld = K if out.is_contiguous() else out.stride(0)
-    _check(lib().moe_mx4_dequantize(codes.data_ptr(), scales.data_ptr(), rows, K, out.data_ptr(),
-                                    _code(out), ld, _stream(stream)), "moe_mx4_dequantize")
+        lead = (shape[0],) if len(shape) == 2 else shape[:-1]
+        out = torch.empty((*lead, K), dtype=dtype, device=codes.device)
+        ld = K
+    else:
+        if out.shape != (*shape[:-1], K):
+            raise MoeError(2, "moe_mx4_dequantize: out has another shape")
+        ld = _mx4_leading(out, K, "moe_mx4_dequantize")
+    _check(lib().moe_mx4_dequantize(codes.data_ptr(), scales.data_ptr(),
+                                    out.numel() // K if K else 0, K, out.data_ptr(),
+                                    _mx4_dtype(out), ld, _stream(stream)), "moe_mx4_dequantize")
     return out
+
+
+def _mx4_offsets(offsets, E: int, where: str):
+    _cuda(offsets)
+    if offsets.dtype != torch.int32 or offsets.numel() != E + 1:
+        raise MoeError(2, f"{where}: offsets are int32 [E + 1]")
+    return offsets.data_ptr()
 
 
 def moe_mx4_product(a_codes, a_scales, b_codes, b_scales, offsets=None, dtype=torch.bfloat16,
@@ -468,48 +497,41 @@ def moe_mx4_product(a_codes, a_scales, b_codes, b_scales, offsets=None, dtype=to
     """A [rows] times B [E, N] (or [N]) by groups of rows -> out [rows, N] of dtype.  The rows of A
     and B hold the same number of blocks; offsets int32 [E + 1] on the device, or None for one
     group."""
+    where = "moe_mx4_product"
     K = 2 * a_codes.shape[-1]
-    _mx4_rows(a_codes, a_scales, K, "moe_mx4_product")
-    _mx4_rows(b_codes, b_scales, K, "moe_mx4_product")
-    if a_codes.dim() != 2 or b_codes.dim() not in (2, 3):
+    sa = _mx4_rows(a_codes, a_scales, K, where)
+    sb = _mx4_rows(b_codes, b_scales, K, where)
+    if len(sa) != 2 or len(sb) not in (2, 3):
         raise MoeError(2, "moe_mx4_product: A is [rows, bytes], B [N, bytes] or [E, N, bytes]")
-    rows, N = a_codes.shape[0], b_codes.shape[-2]
-    E = b_codes.shape[0] if b_codes.dim() == 3 else 1
-    if offsets is not None:
-        _offsets(offsets, E, "moe_mx4_product")
+    rows, N = sa[0], sb[-2]
+    E = sb[0] if len(sb) == 3 else 1
+    off = None if offsets is None else _mx4_offsets(offsets, E, where)
     if out is None:
-        out = torch.empty(rows, N, dtype=dtype, device=a_codes.device)
+        out = torch.empty((rows, N), dtype=dtype, device=a_codes.device)
     elif out.shape != (rows, N):
         raise MoeError(2, "moe_mx4_product: out has another shape")
-    _cuda(out)
+    else:
+        _cuda(out)
     ws = _mx4_ws(ws, 256, a_codes.device)
     _check(lib().moe_mx4_product(a_codes.data_ptr(), a_scales.data_ptr(), rows,
-                                 b_codes.data_ptr(), b_scales.data_ptr(), _ptr(offsets), E, N, K,
-                                 out.data_ptr(), _code(out), ws.data_ptr(), ws.numel(),
-                                 _stream(stream)), "moe_mx4_product")
+                                 b_codes.data_ptr(), b_scales.data_ptr(), off, E, N, K,
+                                 out.data_ptr(), _mx4_dtype(out), ws.data_ptr(), ws.numel(),
+                                 _stream(stream)), where)
     return out
-
-
-def _offsets(offsets, E: int, where: str):
-    _cuda(offsets)
-    if offsets.dtype != torch.int32 or offsets.numel() != E + 1:
-        raise MoeError(2, f"{where}: offsets are int32 [E + 1]")
 
 
 def _mx4_expert_weights(gate, up, down, H: int, where: str):
     """Checks (codes, scales) of gate, up [E, I] rows of H and down [E, H] rows of I -> (E, I)."""
-    for m in (gate, up, down):
-        if m[0].dim() != 3:
-            raise MoeError(2, f"{where}: expert weights are [E, rows, bytes]")
-    E, I = gate[0].shape[:2]
-    _mx4_rows(*gate, H, where)
-    _mx4_rows(*up, H, where)
-    _mx4_rows(*down, I, where)
-    if up[0].shape[:2] != (E, I) or down[0].shape[:2] != (E, H):
+    sg = _mx4_rows(*gate, H, where)
+    if len(sg) != 3:
+        raise MoeError(2, f"{where}: expert weights are [E, rows, bytes]")
+    E, I = sg[0], sg[1]
+    if _mx4_rows(*up, H, where) != sg or _mx4_rows(*down, I, where)[:-1] != (E, H):
         raise MoeError(2, f"{where}: gate, up and down do not belong together")
     return E, I
 
 
+@functools.lru_cache(maxsize=4096)
 def mx4_experts_workspace_bytes(rows: int, H: int, I: int) -> int:
     return lib().moe_mx4_experts_workspace_bytes(rows, H, I)
 
@@ -518,25 +540,28 @@ def moe_mx4_experts_forward_dispatched(x_d, offsets, gate, up, down, y=None, ws=
                                        stream=None):
     """SwiGLU experts with weights and activations in blocks -> y [rows, H] in x_d's dtype.
     gate, up, down: (codes, scales) of [E, I, H], [E, I, H] and [E, H, I]."""
+    where = "moe_mx4_experts_forward_dispatched"
     _cuda(x_d)
     rows, H = x_d.shape
-    E, I = _mx4_expert_weights(gate, up, down, H, "moe_mx4_experts_forward_dispatched")
-    _offsets(offsets, E, "moe_mx4_experts_forward_dispatched")
-    y = torch.empty_like(x_d) if y is None else y
-    if y.shape != x_d.shape or y.dtype != x_d.dtype:
-        raise MoeError(2, "moe_mx4_experts_forward_dispatched: y is not like x_d")
-    _cuda(y)
+    E, I = _mx4_expert_weights(gate, up, down, H, where)
+    off = _mx4_offsets(offsets, E, where)
+    if y is None:
+        y = torch.empty_like(x_d)
+    elif y.shape != x_d.shape or y.dtype != x_d.dtype:
+        raise MoeError(2, f"{where}: y is not like x_d")
+    else:
+        _cuda(y)
     ws = _mx4_ws(ws, mx4_experts_workspace_bytes(rows, H, I), x_d.device)
     _check(lib().moe_mx4_experts_forward_dispatched(
-        x_d.data_ptr(), _code(x_d), offsets.data_ptr(), rows, gate[0].data_ptr(),
-        gate[1].data_ptr(), up[0].data_ptr(), up[1].data_ptr(), down[0].data_ptr(),
-        down[1].data_ptr(), E, H, I, y.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream)),
-        "moe_mx4_experts_forward_dispatched")
+        x_d.data_ptr(), _mx4_dtype(x_d), off, rows, gate[0].data_ptr(), gate[1].data_ptr(),
+        up[0].data_ptr(), up[1].data_ptr(), down[0].data_ptr(), down[1].data_ptr(), E, H, I,
+        y.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream)), where)
     return y
 
 
+@functools.lru_cache(maxsize=4096)
 def mx4_tokens_workspace_bytes(T: int, E: int, H: int, I: int, top_k: int, dtype) -> int:
-    return lib().moe_mx4_tokens_workspace_bytes(T, E, H, I, top_k, DTYPE_CODE[dtype])
+    return lib().moe_mx4_tokens_workspace_bytes(T, E, H, I, top_k, DTYPE_CODE.get(dtype, -1))
 
 
 def moe_mx4_forward_tokens(x, router, gate, up, down, top_k: int, renormalize: bool = True,
@@ -553,16 +578,15 @@ def moe_mx4_forward_tokens(x, router, gate, up, down, top_k: int, renormalize: b
     if (idx is not None and (idx.dtype != torch.uint32 or idx.shape != (T, top_k))) or (
             w is not None and (w.dtype != torch.float32 or w.shape != (T, top_k))):
         raise MoeError(2, f"{where}: idx is uint32 [T, top_k], w float32 [T, top_k]")
-    out = torch.empty_like(x) if out is None else out
-    if out.shape != x.shape or out.dtype != x.dtype:
+    if out is None:
+        out = torch.empty_like(x)
+    elif out.shape != x.shape or out.dtype != x.dtype:
         raise MoeError(2, f"{where}: out is not like x")
-    _cuda(out)
-    if ws is None:
-        ws = torch.empty(max(lib().moe_mx4_tokens_workspace_bytes(T, E, H, I, top_k, _code(x)), 256),
-                         dtype=torch.uint8, device=x.device)
-    _cuda(ws)
+    else:
+        _cuda(out)
+    ws = _mx4_ws(ws, max(mx4_tokens_workspace_bytes(T, E, H, I, top_k, x.dtype), 256), x.device)
     _check(lib().moe_mx4_forward_tokens(
-        x.data_ptr(), router.data_ptr(), _code(x), gate[0].data_ptr(), gate[1].data_ptr(),
+        x.data_ptr(), router.data_ptr(), _mx4_dtype(x), gate[0].data_ptr(), gate[1].data_ptr(),
         up[0].data_ptr(), up[1].data_ptr(), down[0].data_ptr(), down[1].data_ptr(), T, E, H, I,
         top_k, int(bool(renormalize)), out.data_ptr(), _ptr(idx), _ptr(w), ws.data_ptr(),
         ws.numel(), _stream(stream)), where)
