@@ -361,25 +361,40 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int w = 0; w < 8; ++w) now[j][w] = next[j][w];
         if (quad + 1 < quads) load_quad(t, quad + 1);
         else if (t + step < total) load_quad(t + step, 0);
+        // two slices at a time: a fence between the proxies and the arrivals behind it are a chain
+        // of several hundred cycles, as long as a slice's MMAs
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (quad * 4 + k >= p.KB || stop) continue;
-          // (every lane waits: the warp's threads write together)
-          if (!__all_sync(0xFFFFFFFFu,
-                          wait_bounded(empty_bar(stage), phase ^ 1u, abort_f, p.status))) {
-            stop = true;
-            continue;
+        for (int k = 0; k < 4; k += 2) {
+          const int n = min(2, p.KB - quad * 4 - k);
+          if (n <= 0 || stop) continue;
+          uint32_t bar[2];
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+            if (z >= n || stop) continue;
+            // (every lane waits: the warp's threads write together)
+            if (!__all_sync(0xFFFFFFFFu,
+                            wait_bounded(empty_bar(stage), phase ^ 1u, abort_f, p.status))) {
+              stop = true;
+              continue;
+            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const int w = 2 * (k + z) + c;
+              st_shared_v4(dst + stage * SF_BYTES + c * chunk_step, now[0][w], now[1][w],
+                           now[2][w], now[3][w]);
+            }
+            bar[z] = full_bar(stage);
+            if (++stage == STAGES) {
+              stage = 0;
+              phase ^= 1u;
+            }
           }
-#pragma unroll
-          for (int c = 0; c < 2; ++c)
-            st_shared_v4(dst + stage * SF_BYTES + c * chunk_step, now[0][2 * k + c],
-                         now[1][2 * k + c], now[2][2 * k + c], now[3][2 * k + c]);
+          if (stop) continue;
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) arrive_leader(full_bar(stage));
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1u;
+          if (elect_one()) {
+            arrive_leader(bar[0]);
+            if (n == 2) arrive_leader(bar[1]);
           }
         }
       }
@@ -417,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
               const float g = __uint_as_float(acc[c][i]), u = __uint_as_float(acc[c + 2][i]);
-              a[i] = blk * 32 + i < p.N ? g / (1.f + expf(-g)) * u : 0.f;
+              a[i] = blk * 32 + i < p.N ? __fdividef(g, 1.f + __expf(-g)) * u : 0.f;
               top = max(top, __float_as_uint(a[i]) & 0x7FFFFFFFu);
             }
             const uint32_t b = scale_byte(top);
