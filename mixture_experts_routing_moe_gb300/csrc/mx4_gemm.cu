@@ -329,26 +329,34 @@ __global__ void __launch_bounds__(kThreads, 1)
     // quads of slices over all of this CTA's tiles; the next quad's words are loaded ahead
     const int quads = (p.KB + 3) / 4;
     uint32_t next[4][8];
-    auto load_quad = [&](int t, int quad) {
+    const uint8_t* src[4];
+    auto point = [&](int t) {  // src: this lane's four rows of tile t
       const Tile x = tile_of(t);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int i = 32 * j + lane;
-        const uint8_t* src;
         if (part == 0) {
-          src = p.a_scales + min((int64_t)x.r0 + i, p.rows - 1) * pitch;
+          src[j] = p.a_scales + min((int64_t)x.r0 + i, p.rows - 1) * pitch;
         } else {
           const int h = part - 1;
           int n = GATEUP ? x.n * (BN / 2) + h * 64 + (i & 63) : x.n * BN + h * 128 + i;
           n = min(n, p.N - 1);
           const uint8_t* b = GATEUP && j >= 2 ? p.b2_scales : p.b_scales;
-          src = b + ((int64_t)x.e * p.N + n) * pitch;
+          src[j] = b + ((int64_t)x.e * p.N + n) * pitch;
         }
-        if (vec) load_scales<true>(src, quad * 32, pitch, next[j]);
-        else load_scales<false>(src, quad * 32, pitch, next[j]);
       }
     };
-    if (first < total && !stop) load_quad(first, 0);
+    auto load_quad = [&](int quad) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (vec) load_scales<true>(src[j], quad * 32, pitch, next[j]);
+        else load_scales<false>(src[j], quad * 32, pitch, next[j]);
+      }
+    };
+    if (first < total && !stop) {
+      point(first);
+      load_quad(0);
+    }
     // chunk (c, half) of B is chunk 2 + 2 c + half of a slice, chunk c of A is chunk c
     const uint32_t dst = sf_base + (part == 0 ? 0 : 1 + part) * kScaleChunk + lane * 16;
     const uint32_t chunk_step = (part == 0 ? 1 : 2) * kScaleChunk;
@@ -359,8 +367,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; j < 4; ++j)
 #pragma unroll
           for (int w = 0; w < 8; ++w) now[j][w] = next[j][w];
-        if (quad + 1 < quads) load_quad(t, quad + 1);
-        else if (t + step < total) load_quad(t + step, 0);
+        if (quad + 1 < quads) {
+          load_quad(quad + 1);
+        } else if (t + step < total) {
+          point(t + step);
+          load_quad(0);
+        }
         // two slices at a time: a fence between the proxies and the arrivals behind it are a chain
         // of several hundred cycles, as long as a slice's MMAs
 #pragma unroll
