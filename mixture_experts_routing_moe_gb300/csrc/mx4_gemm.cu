@@ -59,7 +59,7 @@ struct Params {
   const uint8_t* b_scales;   // gate for the gate/up product
   const uint8_t* b2_scales;  // up
   int64_t scale_pitch;       // of a row of K values
-  int scales_vec;            // every scale base is a multiple of 16 bytes
+  int scales_align;          // see load_scales()
   int E, N, KB, NT;          // N: rows of one expert's B (gate/up: I); KB: 256-deep slices
   void* out;
   uint8_t* codes;            // gate/up: rows of N values in blocks
@@ -69,10 +69,20 @@ struct Params {
 };
 
 // 32 consecutive bytes of a row's scales from byte `at` (a multiple of 32) on; bytes past the row
-// are zero.  VEC: the pitch and the base are multiples of 16 bytes.
-template <bool VEC>
-__device__ __forceinline__ void load_scales(const uint8_t* row, int at, int pitch, uint32_t* w) {
-  if (VEC) {
+// are zero.  align: the largest of 32, 16 and 4 that divides the pitch and the bases.  One 32-byte
+// load a row asks L2 once a sector; two of 16 bytes ask twice, as the little L1 that the ring
+// leaves does not hold the tile's 384 lines between them.
+__device__ __forceinline__ void load_scales(const uint8_t* row, int at, int pitch, int align,
+                                            uint32_t* w) {
+  if (align == 32) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = 0u;
+    if (at < pitch)
+      asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                   : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]),
+                     "=r"(w[6]), "=r"(w[7])
+                   : "l"(row + at));
+  } else if (align == 16) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       uint4 v = make_uint4(0, 0, 0, 0);
@@ -322,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // rows l, l + 32, l + 64, l + 96, whose words are 16 consecutive bytes of a chunk
     const int part = warp - 4;
     const int pitch = (int)p.scale_pitch;
-    const bool vec = (pitch & 15) == 0 && p.scales_vec;
+    const int align = p.scales_align;
     int stage = 0;
     uint32_t phase = 0;
     bool stop = part == 3;
@@ -349,8 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto load_quad = [&](int quad) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        if (vec) load_scales<true>(src[j], quad * 32, pitch, next[j]);
-        else load_scales<false>(src[j], quad * 32, pitch, next[j]);
+        load_scales(src[j], quad * 32, pitch, align, next[j]);
       }
     };
     if (first < total && !stop) {
@@ -527,7 +536,11 @@ cudaError_t launch(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap
                                 : launch_cg<1, GATEUP, T>(a, b, b2, p, sms, s);
 }
 
-bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+// Of 32, 16 and 4, the largest that divides the pitch and the three bases.
+int scales_align(int64_t pitch, const void* a, const void* b, const void* c) {
+  const uintptr_t all = (uintptr_t)pitch | (uintptr_t)a | (uintptr_t)b | (uintptr_t)c;
+  return all % 32 == 0 ? 32 : all % 16 == 0 ? 16 : 4;
+}
 
 Params make_params(Mx4Rows a, int64_t rows, const int32_t* offsets, int E, int N, int K, int cols,
                    unsigned* status) {
@@ -556,7 +569,7 @@ cudaError_t launch_mx4_product(Mx4Rows a, int64_t rows, Mx4Rows b, const int32_t
     return cudaErrorInvalidValue;
   Params p = make_params(a, rows, offsets, E, N, K, BN, status);
   p.b_scales = b.scales;
-  p.scales_vec = aligned16(a.scales) && aligned16(b.scales);
+  p.scales_align = scales_align(p.scale_pitch, a.scales, b.scales, b.scales);
   p.out = out;
   p.zero_status = zero_status;
   switch (odt) {
@@ -579,7 +592,7 @@ cudaError_t launch_mx4_gate_up(Mx4Rows a, int64_t rows, Mx4Rows gate, Mx4Rows up
   Params p = make_params(a, rows, offsets, E, I, H, BN / 2, status);
   p.b_scales = gate.scales;
   p.b2_scales = up.scales;
-  p.scales_vec = aligned16(a.scales) && aligned16(gate.scales) && aligned16(up.scales);
+  p.scales_align = scales_align(p.scale_pitch, a.scales, gate.scales, up.scales);
   p.codes = codes;
   p.scales = scales;
   return launch<true, float>(ma, mg, mu, p, s);
