@@ -48,7 +48,7 @@ namespace {
 using namespace tc;
 using namespace mx4;
 
-constexpr int kThreads = 384, kWarps = kThreads / 32;
+constexpr int kThreads = 416, kWarps = kThreads / 32;
 constexpr int P = 5;               // terms of a token value
 constexpr int kG = 38;             // tokens of a unit
 constexpr int kMaxN = 192;         // columns of a unit
@@ -318,6 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kMaxStages + 5);
   volatile int* abort_f = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* active_s = reinterpret_cast<int*>(tmem_slot + 2);
+  volatile int* written = reinterpret_cast<volatile int*>(tmem_slot + 3);  // gate/up units
   const bool out_vec = ((uintptr_t)p.out & 7u) == 0;
 
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -333,6 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(drain_bar, 1);
     *abort_f = 0;
     *active_s = 0;
+    *written = 0;
     fence_mbar_init();
     tma_prefetch(&mapG);
     tma_prefetch(&mapU);
@@ -746,11 +748,32 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
+  } else if (warp == 12) {
+    // ---------------------------------------------------------------- counts of gate/up units
+    // The fence before a count reaches other SMs takes a thousand cycles or more, which the
+    // epilogue does not have to spare (wide experts: 160 us with it there).
+    int seen = 0;
+    bool stop = false;
+    for (int u = blockIdx.x; u < n1 && !stop; u += gridDim.x) {
+      const long long t0 = clock64();
+      while (*written <= seen) {
+        if (*abort_f || clock64() - t0 > kWaitLimit) {
+          stop = true;  // (the epilogue's own wait has recorded a timeout, or will)
+          break;
+        }
+        __nanosleep(20);
+      }
+      ++seen;
+      __syncwarp();
+      __threadfence();          // the epilogue's writes, which its barrier ordered before the word
+      fence_proxy_async_all();  // aq is read by TMA
+      if (!stop && elect_one()) atomicAdd(p.ready + unit_of(u).ai, 1u);
+    }
   } else if (warp >= 8) {
     // ---------------------------------------------------------------- epilogue
     constexpr int PER = 32 / P;  // tokens at a time
     const int q = warp & 3;
-    int acc = 0;
+    int acc = 0, count = 0;
     uint32_t acc_phase = 0;
     auto any_of_epilogue = [&](bool v) {
       uint32_t r;
@@ -788,25 +811,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < PER; ++i)
             if (i0 + i < r.n) y[(int64_t)list[r.first + i0 + i] * p.H] = s[i];
         } else {
-          // warps of quarters 0 and 1 hold 64 gate rows, 2 and 3 the same up rows
-          if (q >= 2) {
+          // Quarters 0 and 1 hold 64 gate rows, 2 and 3 the same up rows: the first two take the
+          // even tokens, the other two the odd ones, and each hands over what it does not need.
+          const int odd = q >> 1, part = (q & 1) * 32;
 #pragma unroll
-            for (int i = 0; i < PER; ++i) exchange[i * 64 + (q - 2) * 32 + lane] = s[i];
-          }
+          for (int i = 0; i < PER; ++i)
+            if ((i & 1) != odd) exchange[i * 64 + part + lane] = s[i];
           sync_epilogue();
-          if (q < 2) {
-            const int ib = p.I / 32, col = r.tile * 64 + q * 32;
+          const int ib = p.I / 32, col = r.tile * 64 + part;
 #pragma unroll
-            for (int i = 0; i < PER; ++i) {
-              const int t = i0 + i;
-              if (t >= columns || (r.all && !(has >> t & 1))) continue;
-              const int pos = r.first + (r.all ? __popcll(has & ((1ull << t) - 1)) : t);
-              const float g = s[i];
-              const float up = exchange[i * 64 + q * 32 + lane];
-              const float a = Dt<T>::to_f(Dt<T>::from_f(g / (1.f + expf(-g)) * up));
-              write_terms(a, p.aq + (int64_t)pos * P * (p.I / 2) + col / 2, p.I / 2,
-                          p.as + (int64_t)pos * P * ib + col / 32, ib, lane);
-            }
+          for (int i = 0; i < PER; ++i) {
+            const int t = i0 + i;
+            if ((i & 1) != odd || t >= columns || (r.all && !(has >> t & 1))) continue;
+            const int pos = r.first + (r.all ? __popcll(has & ((1ull << t) - 1)) : t);
+            const float other = exchange[i * 64 + part + lane];
+            const float g = odd ? other : s[i], up = odd ? s[i] : other;
+            const float a = Dt<T>::to_f(Dt<T>::from_f(g / (1.f + expf(-g)) * up));
+            write_terms(a, p.aq + (int64_t)pos * P * (p.I / 2) + col / 2, p.I / 2,
+                        p.as + (int64_t)pos * P * ib + col / 32, ib, lane);
           }
           sync_epilogue();
         }
@@ -816,11 +838,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(tempty_bar(acc));
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1u;
-      if (!r.down) {
-        fence_proxy_async_all();  // aq is read by TMA
-        __threadfence();
-        sync_epilogue();
-        if (threadIdx.x == 8 * 32) atomicAdd(p.ready + r.ai, 1u);
+      if (!r.down && threadIdx.x == 8 * 32) {  // behind the last barrier above
+        __threadfence_block();
+        *written = ++count;
       }
     }
     // 3. every CTA's y is written: the sums over slots, four columns a thread
