@@ -96,6 +96,32 @@ static __device__ __forceinline__ void set_max_regs_inc() {
 static __device__ __forceinline__ void st_shared_u32(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
+// Scale bytes on their way from global memory to the chunk layout wait as raw rows of 32 bytes, 16-
+// byte half h of row i at i * 32 + 16 (h ^ (i / 4 % 2)), so that eight lanes read eight rows' halves
+// without bank conflicts.  One warp copies them in, asynchronously, and another one writes the
+// chunks: the fence between the proxies that follows each chunk waits for the issuing warp's own
+// global accesses, so a warp that did both would wait for its next rows at every slice.
+static __device__ __forceinline__ uint32_t raw_offset(int row, int half) {
+  return (uint32_t)(row * 32 + ((half ^ (row >> 2 & 1)) * 16));
+}
+// Sixteen (past L1) or four bytes; zeros where `in` is false (nothing is read then).
+static __device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(in ? 16 : 0)
+               : "memory");
+}
+static __device__ __forceinline__ void cp_async4_or_zero(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
+               "r"(in ? 4 : 0)
+               : "memory");
+}
+// One arrival on `bar` once this thread's copies so far have landed.
+static __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+static __device__ __forceinline__ void cp_async_wait_all() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
 // Arrival on a barrier of another CTA of the cluster that releases this thread's (and, by
 // cumulativity, its warp's) shared-memory writes only: a full release at cluster scope also waits
 // for the warp's global accesses in flight.

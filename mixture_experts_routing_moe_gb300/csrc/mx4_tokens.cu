@@ -26,8 +26,8 @@
 //      lists the active experts' tokens in shared memory, expert by expert.
 //   2  units of work: (expert, 64 columns of a) for gate/up, then (expert, 128 columns of the
 //      output, part of K) for down, dealt to the CTAs in turn.  Warp roles as in the grouped
-//      products: weight codes (TMA), token terms (TMA), weight scales, token scales, MMA, epilogue,
-//      in slices of K = 256.  The gate/up epilogue writes a as terms (aq, as; rows in the order of
+//      products: weight codes (TMA), token terms (TMA), raw scales, scales, MMA, epilogue, in slices
+//      of K = 256.  The gate/up epilogue writes a as terms (aq, as; rows in the order of
 //      the lists) and counts the unit on its expert; a down unit's weights are loaded ahead, its
 //      tokens once that count is full.  The weight loads never wait for anything but a free slot,
 //      from the first unit to the last.
@@ -56,7 +56,8 @@ static_assert(kG * P <= kMaxN, "columns of a group");
 constexpr int kA = 128 * 128;      // bytes of a slice's weights (128 rows, 256 deep)
 constexpr int kMaxStages = 10;
 constexpr int kBox = 16;           // rows of token terms a TMA box
-constexpr int kBarBytes = 256;
+constexpr int kBarBytes = 512;
+constexpr int kRaw = 3;            // raw scale slots (four slices each) of weights and of tokens
 // two accumulators, then the scales of two slices: 2 x 4 columns for A, 2 x 8 for B
 constexpr uint32_t kTmemCols = 512, kScaleCol = 2 * kMaxN;
 static_assert(kScaleCol + 2 * 24 <= kTmemCols, "tensor memory");
@@ -78,6 +79,7 @@ struct TokensParams {
   float* w;
   int splits;        // parts of K a down unit is cut into
   int stages, ncap;  // ring: slices, columns of its token tiles
+  int ncap_raw;      // ncap rounded up to 32
 };
 
 __device__ __forceinline__ unsigned ld_acquire_u32(const unsigned* p) {
@@ -295,6 +297,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   at += p.stages * sf_bytes;
   uint64_t* bars = reinterpret_cast<uint64_t*>(at);
   at += kBarBytes;
+  const uint32_t rawa_base = smem_u32(at), rawb_base = rawa_base + kRaw * 128 * 32;
+  at += kRaw * (128 + p.ncap_raw) * 32;
   float* exchange = reinterpret_cast<float*>(at);
   at += kExchange;
   unsigned long long* mask = reinterpret_cast<unsigned long long*>(at);  // tokens of an expert
@@ -315,7 +319,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto tfull_bar = [&](int a) { return bar0 + 8u * (2 * kMaxStages + a); };
   auto tempty_bar = [&](int a) { return bar0 + 8u * (2 * kMaxStages + 2 + a); };
   const uint32_t drain_bar = bar0 + 8u * (2 * kMaxStages + 4);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kMaxStages + 5);
+  // raw scales: full, then empty 8 bytes on
+  auto rawa_bar = [&](int s) { return bar0 + 8u * (2 * kMaxStages + 5 + 2 * s); };
+  auto rawb_bar = [&](int s) { return rawa_bar(kRaw + s); };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kMaxStages + 5 + 4 * kRaw);
   volatile int* abort_f = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* active_s = reinterpret_cast<int*>(tmem_slot + 2);
   volatile int* written = reinterpret_cast<volatile int*>(tmem_slot + 3);  // gate/up units
@@ -332,6 +339,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(tempty_bar(a), 4);
     }
     mbar_init(drain_bar, 1);
+    for (int s = 0; s < 2 * kRaw; ++s) {
+      mbar_init(rawa_bar(s), 32);
+      mbar_init(rawa_bar(s) + 8, 1);
+    }
     *abort_f = 0;
     *active_s = 0;
     *written = 0;
@@ -422,8 +433,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     r.first = start[r.e] + (a >> 16) * kG;
     r.n = min(start[r.e + 1] - r.first, kG);
     const int slices = ((r.down ? p.I : p.H) + 255) / 256;
-    r.k0 = r.down ? slices * r.split / p.splits : 0;
-    r.k1 = r.down ? slices * (r.split + 1) / p.splits : slices;
+    const int pairs = (slices + 1) / 2;  // parts begin at even slices, 16 bytes of scales
+    r.k0 = r.down ? 2 * (pairs * r.split / p.splits) : 0;
+    r.k1 = r.down ? min(slices, 2 * (pairs * (r.split + 1) / p.splits)) : slices;
     r.all = !r.down && p.T <= kG && r.n * 8 >= p.T;
     r.cols = (r.all ? p.T : r.n) * P;
     return r;
@@ -437,12 +449,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_proxy_async_all();
     return ok;
   };
-
-  // Roles with two warps: each warp waits only for the slots of the slices it takes, by parity.  A
-  // slice c needs slice c - S to be consumed (S slots); the parity cannot be that of c - 2 S as
-  // long as the warp has seen c - 2 S consumed before, that is as long as its last wait was for
-  // slice c - S or later: it may leave out at most S - 1 slices at a time.  (It must not wait for
-  // the others' slots either: those move on without it, and a parity would come round again.)
 
   if (warp == 0) {
     // ---------------------------------------------------------------- weight codes
@@ -555,6 +561,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const CUtensorMap* m = r.down ? &mapA : r.all ? &mapX : &mapX1;
       for (int k = r.k0; k < r.k1; ++k, turn ^= 1) {
+        // Each warp waits only for the slots of the slices it takes, by parity.  A slice c needs
+        // slice c - S to be consumed (S >= 3 slots); the parity cannot be taken for that of
+        // c - 2 S, since the warp's last wait was for c - 2, later than c - S.  (It must not wait
+        // for the other's slots: those move on without it, and a parity would come round again.)
         if (turn != mine) {
           at.step(1, p.stages);
           continue;
@@ -582,164 +592,117 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait_until(full_bar(at.stage), at.phase, until);
       }
     }
-  } else if (warp == 4 || warp == 6) {
-    // ---------------------------------------------------------------- weight scales
-    // lane l holds rows l, l + 32, l + 64, l + 96 of the unit's 128, four slices (32 bytes) each;
-    // the two warps take these parts in turn, and each loads its next part ahead; with fewer than
-    // five slots a part is two slices
-    const int mine = warp == 6, per = p.stages >= 5 ? 4 : 2;
-    RingPos at;
-    int turn = 0;
-    bool stop = false;
-    uint32_t next[4][8];
-    auto load = [&](int u, int part) {
-      const Unit r = unit_of(u);
-      const int pitch = (r.down ? p.I : p.H) / 32;
-      const int at0 = r.k0 * 8 + part * per * 8, left = min(r.k1 * 8, pitch) - at0;
-      const bool vec = p.scales_vec && ((pitch | at0) & 15) == 0;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint8_t* src =
-            r.down ? p.ds + ((int64_t)r.e * p.H + r.tile * 128 + 32 * j + lane) * pitch
-                   : (j < 2 ? p.gs : p.us) +
-                         ((int64_t)r.e * p.I + r.tile * 64 + 32 * (j & 1) + lane) * pitch;
-        src += at0;
-#pragma unroll
-        for (int z = 0; z < 2; ++z) {
-          if (vec && 16 * z + 16 <= left) {
-            const uint4 q = ld_nc_v4(src + 16 * z);
-            next[j][4 * z] = q.x, next[j][4 * z + 1] = q.y;
-            next[j][4 * z + 2] = q.z, next[j][4 * z + 3] = q.w;
-          } else {
-#pragma unroll
-            for (int i = 4 * z; i < 4 * z + 4; ++i)
-              next[j][i] =
-                  4 * i < left ? __ldg(reinterpret_cast<const uint32_t*>(src + 4 * i)) : 0u;
-          }
-        }
-      }
-    };
-    auto parts_of = [&](int u) {
-      const Unit r = unit_of(u);
-      return (r.k1 - r.k0 + per - 1) / per;
-    };
-    // the next part of this warp: (un, pn), two parts on from the last; false past the end
-    int un = blockIdx.x, pn = mine, left_n = un < total ? parts_of(un) : 0;
-    auto settle = [&]() {
-      while (un < total && pn >= left_n) {
-        pn -= left_n;
-        un += gridDim.x;
-        if (un < total) left_n = parts_of(un);
-      }
-      return un < total;
-    };
-    if (settle()) load(un, pn);
-    for (int u = blockIdx.x; u < total && !stop; u += gridDim.x) {
-      const Unit r = unit_of(u);
-      const int slices = r.k1 - r.k0, parts = (slices + per - 1) / per;
-      for (int part = 0; part < parts && !stop; ++part, turn ^= 1) {
-        const int count = min(per, slices - part * per);
-        if (turn != mine) {
-          at.step(count, p.stages);
-          continue;
-        }
-        uint32_t now[4][8];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) now[j][i] = next[j][i];
-        pn += 2;
-        if (settle()) load(un, pn);
-#pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-          if (i / 2 >= count || stop) continue;
-          if (!__all_sync(0xFFFFFFFFu,
-                          wait_bounded(empty_bar(at.stage), at.phase ^ 1u, abort_f, p.status))) {
-            stop = true;
-            continue;
-          }
-          const uint32_t sf = sf_base + at.stage * sf_bytes + lane * 16;
-          st_shared_v4(sf, now[0][i], now[1][i], now[2][i], now[3][i]);
-          st_shared_v4(sf + kScaleChunk, now[0][i + 1], now[1][i + 1], now[2][i + 1],
-                       now[3][i + 1]);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (elect_one()) mbar_arrive(full_bar(at.stage));
-          at.step(1, p.stages);
-        }
-      }
-    }
-  } else if (warp == 5 || warp == 7) {
-    // ---------------------------------------------------------------- token scales
-    // lane l holds the terms in columns l, l + 32, ..., l + 160, two slices (16 bytes) each; the
-    // two warps take these pairs in turn
+  } else if (warp == 6 || warp == 7) {
+    // ---------------------------------------------------------------- raw scales
+    // warp 6: the unit's 128 weight rows; warp 7: its columns' token terms; four slices (32 bytes
+    // of a row) at a time.  Lane l copies rows l, l + 32, ...
     constexpr int J = kMaxN / 32;
-    const int mine = warp == 7;
+    const bool tokens = warp == 7;
     RingPos at;
-    int turn = 0;
     bool stop = false;
     for (int u = blockIdx.x; u < total && !stop; u += gridDim.x) {
       const Unit r = unit_of(u);
-      if (r.down && !unit_ready(r.ai)) break;
-      const int pitch = (r.down ? p.I : p.H) / 32;
+      if (tokens && r.down && !unit_ready(r.ai)) break;
+      const int pitch = (r.down ? p.I : p.H) / 32, end = min(r.k1 * 8, pitch);
+      const bool vec = (pitch & 15) == 0 && (tokens || p.scales_vec);
+      const int lanes_j = tokens ? (r.cols + 31) / 32 : 4;
       const uint8_t* src[J];
 #pragma unroll
       for (int j = 0; j < J; ++j) {
-        const int c = 32 * j + lane;
         src[j] = nullptr;
-        if (c < r.cols) {
+        const int c = 32 * j + lane;
+        if (tokens && c < r.cols) {
           const int i = c / P, term = c - i * P;
           const int row = r.down ? (r.first + i) * P + term
                                  : (r.all ? i : (int)list[r.first + i] / p.k) * P + term;
           src[j] = (r.down ? p.as : p.xs) + (int64_t)row * pitch;
+        } else if (!tokens && j < 4) {
+          src[j] = r.down ? p.ds + ((int64_t)r.e * p.H + r.tile * 128 + c) * pitch
+                          : (j < 2 ? p.gs : p.us) +
+                                ((int64_t)r.e * p.I + r.tile * 64 + (c & 63)) * pitch;
         }
       }
-      uint32_t next[J][4];
-      const bool vec = (pitch & 15) == 0 && (r.k0 & 1) == 0;
-      auto load = [&](int k) {  // slices k, k + 1
+      for (int k = r.k0; k < r.k1; k += 4) {
+        const uint32_t rb = tokens ? rawb_bar(at.stage) : rawa_bar(at.stage);
+        if (!__all_sync(0xFFFFFFFFu, wait_bounded(rb + 8, at.phase ^ 1u, abort_f, p.status))) {
+          stop = true;
+          break;
+        }
+        const uint32_t slot = tokens ? rawb_base + at.stage * (p.ncap_raw * 32)
+                                     : rawa_base + at.stage * (128 * 32);
 #pragma unroll
         for (int j = 0; j < J; ++j) {
-          next[j][0] = next[j][1] = next[j][2] = next[j][3] = 0u;
-          if (32 * j >= r.cols || !src[j]) continue;
+          if (j >= lanes_j || !src[j]) continue;
+          const int row = 32 * j + lane;
           if (vec) {
-            const uint4 v = ld_cg_v4(src[j] + k * 8);
-            next[j][0] = v.x, next[j][1] = v.y, next[j][2] = v.z, next[j][3] = v.w;
-          } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (k * 8 + i * 4 < pitch) next[j][i] = ld_cg_u32(src[j] + k * 8 + i * 4);
+            for (int h = 0; h < 2; ++h)
+              cp_async16_or_zero(slot + raw_offset(row, h), src[j] + k * 8 + h * 16,
+                                 k * 8 + h * 16 < end);
+          } else {
+            // (four bytes cannot be copied past L1, which may hold a line of `as` from before it
+            // was written: loads past it, then stores)
+#pragma unroll
+            for (int w = 0; w < 8; ++w)
+              st_shared_u32(slot + raw_offset(row, w >> 2) + (w & 3) * 4,
+                            k * 8 + w * 4 < end ? ld_cg_u32(src[j] + k * 8 + w * 4) : 0u);
           }
         }
-      };
-      const int ahead = turn == mine ? r.k0 : r.k0 + 2;  // this warp's first pair
-      if (ahead < r.k1) load(ahead);
-      for (int k = r.k0; k < r.k1 && !stop; k += 2, turn ^= 1) {
-        if (turn != mine) {
-          at.step(min(2, r.k1 - k), p.stages);
-          continue;
+        if (vec) cp_async_arrive(rb);
+        else mbar_arrive(rb);
+        at.step(1, kRaw);
+      }
+    }
+    cp_async_wait_all();  // nothing is on its way when the CTA leaves
+  } else if (warp == 4 || warp == 5) {
+    // ---------------------------------------------------------------- scales
+    // raw rows to the chunks of each slice: warp 4 the weights', warp 5 the tokens'
+    constexpr int J = kMaxN / 32;
+    const bool tokens = warp == 5;
+    RingPos at, raw_at;
+    bool stop = false;
+    for (int u = blockIdx.x; u < total && !stop; u += gridDim.x) {
+      const Unit r = unit_of(u);
+      for (int k = r.k0; k < r.k1 && !stop; k += 4) {
+        const uint32_t rb = tokens ? rawb_bar(raw_at.stage) : rawa_bar(raw_at.stage);
+        if (!__all_sync(0xFFFFFFFFu, wait_bounded(rb, raw_at.phase, abort_f, p.status))) {
+          stop = true;
+          break;
         }
-        uint32_t now[J][4];
+        const uint32_t slot = tokens ? rawb_base + raw_at.stage * (p.ncap_raw * 32)
+                                     : rawa_base + raw_at.stage * (128 * 32);
+        uint32_t now[J][8];
 #pragma unroll
         for (int j = 0; j < J; ++j)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) now[j][i] = next[j][i];
-        if (k + 4 < r.k1) load(k + 4);
+          for (int h = 0; h < 2; ++h) {
+            uint4 v = make_uint4(0, 0, 0, 0);
+            // (rows past the unit's columns hold old bytes: any finite or NaN scale of a column
+            // that is not read)
+            if (tokens ? 32 * j < r.cols : j < 4) v = ld_shared_v4(slot + raw_offset(32 * j + lane, h));
+            now[j][4 * h] = v.x, now[j][4 * h + 1] = v.y;
+            now[j][4 * h + 2] = v.z, now[j][4 * h + 3] = v.w;
+          }
+        __syncwarp();
+        if (elect_one()) mbar_arrive(rb + 8);
+        raw_at.step(1, kRaw);
 #pragma unroll
-        for (int i = 0; i < 4; i += 2) {
-          if (k + i / 2 >= r.k1 || stop) continue;
+        for (int i = 0; i < 4; ++i) {
+          if (k + i >= r.k1 || stop) continue;
           if (!__all_sync(0xFFFFFFFFu,
                           wait_bounded(empty_bar(at.stage), at.phase ^ 1u, abort_f, p.status))) {
             stop = true;
             continue;
           }
-          const uint32_t sf = sf_base + at.stage * sf_bytes + 2 * kScaleChunk + lane * 16;
-          const uint32_t half = b_chunks * kScaleChunk;
+          const uint32_t sf =
+              sf_base + at.stage * sf_bytes + (tokens ? 2 * kScaleChunk : 0) + lane * 16;
+          const uint32_t half = tokens ? b_chunks * kScaleChunk : kScaleChunk;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            st_shared_v4(sf + h * half, now[0][i + h], now[1][i + h], now[2][i + h],
-                         now[3][i + h]);
-            if (b_chunks == 2)
-              st_shared_v4(sf + h * half + kScaleChunk, now[4][i + h], now[5][i + h], 0u, 0u);
+            const int w = 2 * i + h;
+            st_shared_v4(sf + h * half, now[0][w], now[1][w], now[2][w], now[3][w]);
+            if (tokens && b_chunks == 2)
+              st_shared_v4(sf + h * half + kScaleChunk, now[4][w], now[5][w], 0u, 0u);
           }
           fence_proxy_async_smem();
           __syncwarp();
@@ -897,8 +860,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Bytes of shared memory beside the ring.
-size_t fixed_smem(int E, int R) {
-  return 1024 + kBarBytes + kExchange + (size_t)E * 20 + 4 + (size_t)R * 8;
+size_t fixed_smem(int E, int R, int ncap_raw) {
+  return 1024 + kBarBytes + kRaw * (128 + (size_t)ncap_raw) * 32 + kExchange + (size_t)E * 20 + 4 +
+         (size_t)R * 8;
 }
 
 // Parts of K that a down unit is cut into: enough units for four to a CTA (a CTA's last unit is
@@ -950,11 +914,12 @@ cudaError_t launch_t(const Mx4TokensArgs& a, cudaStream_t s) {
   const int R = a.T * a.k;
   // the ring: as many slices as fit, each with room for the columns of the largest unit
   p.ncap = ((a.T < kG ? a.T : kG) * P + kBox - 1) / kBox * kBox;
-  const size_t fixed = fixed_smem(a.E, R);
+  p.ncap_raw = (p.ncap + 31) / 32 * 32;
+  const size_t fixed = fixed_smem(a.E, R, p.ncap_raw);
   const size_t stage = kA + (size_t)p.ncap * 128 + (p.ncap > 128 ? 6 : 4) * kScaleChunk;
   p.stages = (int)(((size_t)most - fixed) / stage);
   if (p.stages > kMaxStages) p.stages = kMaxStages;
-  if (p.stages < 3) return cudaErrorInvalidConfiguration;  // (roles leave out two slices at a time)
+  if (p.stages < 3) return cudaErrorInvalidConfiguration;  // (the token warps take turns)
   const size_t smem = fixed + (size_t)p.stages * stage;
 
   CUtensorMap mg, mu, md, mx1, mx, ma;
