@@ -283,7 +283,6 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads, 1)
     moe_mx4_tokens(const __grid_constant__ CUtensorMap mapG, const __grid_constant__ CUtensorMap mapU,
                    const __grid_constant__ CUtensorMap mapD,
-                   const __grid_constant__ CUtensorMap mapX1,
                    const __grid_constant__ CUtensorMap mapX,
                    const __grid_constant__ CUtensorMap mapA, const TokensParams p) {
   extern __shared__ uint8_t mx4_smem_raw[];
@@ -350,7 +349,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch(&mapG);
     tma_prefetch(&mapU);
     tma_prefetch(&mapD);
-    tma_prefetch(&mapX1);
     tma_prefetch(&mapX);
     tma_prefetch(&mapA);
   }
@@ -415,9 +413,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     int tile, split;  // column tile, part of K
     int first, n;     // its tokens: list[first .. first + n)
     int k0, k1;       // 256-deep slices
-    // gate/up of an expert that takes many of the tokens multiplies all T of them (their terms
-    // are contiguous); otherwise each token's terms are loaded on their own
-    bool all;
     int cols;         // columns in use
   };
   auto unit_of = [&](int u) {
@@ -436,8 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int pairs = (slices + 1) / 2;  // parts begin at even slices, 16 bytes of scales
     r.k0 = r.down ? 2 * (pairs * r.split / p.splits) : 0;
     r.k1 = r.down ? min(slices, 2 * (pairs * (r.split + 1) / p.splits)) : slices;
-    r.all = !r.down && p.T <= kG && r.n * 8 >= p.T;
-    r.cols = (r.all ? p.T : r.n) * P;
+    r.cols = r.n * P;
     return r;
   };
 
@@ -548,18 +542,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         stop = true;
         break;
       }
-      const bool whole = r.down || r.all;              // contiguous rows, boxes of 16
-      const int boxes = whole ? (r.cols + kBox - 1) / kBox : r.n;
-      const int bytes = whole ? kBox * 128 : P * 128;  // of a box
+      // A group's rows of aq are contiguous: boxes of 16.  Its tokens' rows of xq are not: a box
+      // each.  (Multiplying all T tokens of x, contiguous too, by every expert that takes many of
+      // them was slower throughout: 7 tokens, 8 wide experts 150 us against 124, 32 tokens 4 of 8
+      // 96 against 94, 32 tokens 4 of 32 172 against 160.)
+      const int boxes = r.down ? (r.cols + kBox - 1) / kBox : r.n;
+      const int bytes = r.down ? kBox * 128 : P * 128;  // of a box
       // first rows of boxes lane and lane + 32 (at most kG boxes)
       int box_row[2];
 #pragma unroll
       for (int z = 0; z < 2; ++z) {
         const int i = lane + 32 * z;
-        box_row[z] = whole ? (r.down ? r.first * P : 0) + i * kBox
+        box_row[z] = r.down ? r.first * P + i * kBox
                      : i < r.n ? (int)list[r.first + i] / p.k * P : 0;
       }
-      const CUtensorMap* m = r.down ? &mapA : r.all ? &mapX : &mapX1;
+      const CUtensorMap* m = r.down ? &mapA : &mapX;
       for (int k = r.k0; k < r.k1; ++k, turn ^= 1) {
         // Each warp waits only for the slots of the slices it takes, by parity.  A slice c needs
         // slice c - S to be consumed (S >= 3 slots); the parity cannot be taken for that of
@@ -614,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (tokens && c < r.cols) {
           const int i = c / P, term = c - i * P;
           const int row = r.down ? (r.first + i) * P + term
-                                 : (r.all ? i : (int)list[r.first + i] / p.k) * P + term;
+                                 : (int)list[r.first + i] / p.k * P + term;
           src[j] = (r.down ? p.as : p.xs) + (int64_t)row * pitch;
         } else if (!tokens && j < 4) {
           src[j] = r.down ? p.ds + ((int64_t)r.e * p.H + r.tile * 128 + c) * pitch
@@ -755,9 +752,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (any_of_epilogue(!wait_bounded(tfull_bar(acc), acc_phase, abort_f, p.status))) break;
       tc_fence_after();
       const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + acc * kMaxN;
-      const unsigned long long has = mask[r.e];
-      const int columns = r.all ? p.T : r.n;  // tokens that have columns
-      for (int i0 = 0; i0 < columns; i0 += PER) {
+      for (int i0 = 0; i0 < r.n; i0 += PER) {
         uint32_t v[32];
         tmem_ld32(taddr + i0 * P, v);
         tmem_wait_ld();
@@ -784,9 +779,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int ib = p.I / 32, col = r.tile * 64 + part;
 #pragma unroll
           for (int i = 0; i < PER; ++i) {
-            const int t = i0 + i;
-            if ((i & 1) != odd || t >= columns || (r.all && !(has >> t & 1))) continue;
-            const int pos = r.first + (r.all ? __popcll(has & ((1ull << t) - 1)) : t);
+            if ((i & 1) != odd || i0 + i >= r.n) continue;
+            const int pos = r.first + i0 + i;
             const float other = exchange[i * 64 + part + lane];
             const float g = odd ? other : s[i], up = odd ? s[i] : other;
             const float a = Dt<T>::to_f(Dt<T>::from_f(g / (1.f + expf(-g)) * up));
@@ -922,12 +916,11 @@ cudaError_t launch_t(const Mx4TokensArgs& a, cudaStream_t s) {
   if (p.stages < 3) return cudaErrorInvalidConfiguration;  // (the token warps take turns)
   const size_t smem = fixed + (size_t)p.stages * stage;
 
-  CUtensorMap mg, mu, md, mx1, mx, ma;
+  CUtensorMap mg, mu, md, mx, ma;
   if (!make_map_bytes(&mg, a.gate.codes, a.H / 2, (int64_t)a.E * a.I, 64) ||
       !make_map_bytes(&mu, a.up.codes, a.H / 2, (int64_t)a.E * a.I, 64) ||
       !make_map_bytes(&md, a.down.codes, a.I / 2, (int64_t)a.E * a.H, 128) ||
-      !make_map_bytes(&mx1, p.xq, a.H / 2, (int64_t)a.T * P, P) ||
-      !make_map_bytes(&mx, p.xq, a.H / 2, (int64_t)a.T * P, kBox) ||
+      !make_map_bytes(&mx, p.xq, a.H / 2, (int64_t)a.T * P, P) ||
       !make_map_bytes(&ma, p.aq, a.I / 2, (int64_t)R * P, kBox))
     return cudaErrorInvalidValue;
   auto kern = moe_mx4_tokens<T>;
@@ -949,7 +942,7 @@ cudaError_t launch_t(const Mx4TokensArgs& a, cudaStream_t s) {
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, mg, mu, md, mx1, mx, ma, p);
+  return cudaLaunchKernelEx(&cfg, kern, mg, mu, md, mx, ma, p);
 }
 
 }  // namespace
