@@ -445,6 +445,92 @@ def test_tokens_none():
     assert out.shape == (0, 128)
 
 
+# -------------------------------------------------------------------- other layouts and sizes
+def shifted(t, by):
+    """A contiguous copy of t that starts `by` bytes after a 256-byte boundary."""
+    flat = torch.empty(t.numel() + 256, dtype=torch.uint8, device=DEV)
+    view = flat[by:by + t.numel()].view(t.shape)
+    view.copy_(t)
+    return view
+
+
+@pytest.mark.parametrize("K", [512, 1024, 2048])
+def test_product_scales_on_any_word(K):
+    """Scale rows of 16 and 32 bytes whose base is a multiple of 4 or 16 only."""
+    rng = np.random.default_rng(K)
+    ac, asc, c, s = blocks(rng.standard_normal((200, K)))
+    bc, bsc, wc, wsc = blocks(rng.standard_normal((300, K)))
+    want = moe.moe_mx4_product(ac, asc, bc, bsc, dtype=torch.float32)
+    a, w = M.values(c, s), M.values(wc, wsc)
+    assert (np.abs(np64(want) - a @ w.T) <= (K + 64) * 2.0 ** -23 * (np.abs(a) @ np.abs(w).T)).all()
+    for by in (4, 16):
+        got = moe.moe_mx4_product(shifted(ac, 16), shifted(asc, by), bc, shifted(bsc, by),
+                                  dtype=torch.float32)
+        assert torch.equal(got, want)
+
+
+def test_tokens_scales_on_any_word():
+    x, router, packed = layer(6, 8, 512, 1024, torch.bfloat16, 5)
+    args = [x.to(DEV), router.to(DEV)]
+    want = moe.moe_mx4_forward_tokens(*args, *[p[:2] for p in packed], top_k=3)
+    for by in (4, 16):
+        moved = [(shifted(p[0], 16), shifted(p[1], by)) for p in packed]
+        assert torch.equal(moe.moe_mx4_forward_tokens(*args, *moved, top_k=3), want)
+
+
+def test_outputs_on_any_element():
+    """out of 16-bit elements that starts on an odd element: no vector stores."""
+    x, router, packed = layer(5, 4, 256, 128, torch.float16, 6)
+    args = [x.to(DEV), router.to(DEV)] + [p[:2] for p in packed]
+    want = moe.moe_mx4_forward_tokens(*args, top_k=2)
+    out = torch.zeros(5 * 256 + 1, dtype=torch.float16, device=DEV)[1:].view(5, 256)
+    assert torch.equal(moe.moe_mx4_forward_tokens(*args, top_k=2, out=out), want)
+    c, s = moe.moe_mx4_quantize(x.to(DEV))
+    want = moe.moe_mx4_product(c, s, c, s, dtype=torch.float16)
+    out = torch.zeros(26, dtype=torch.float16, device=DEV)[1:].view(5, 5)
+    assert torch.equal(moe.moe_mx4_product(c, s, c, s, out=out), want)
+
+
+def test_quantize_past_32_bits():
+    """More than 2^31 values: the last rows land where they belong."""
+    rows, K = (1 << 18) + 9, 8192
+    x = torch.zeros(rows, K, dtype=torch.bfloat16, device=DEV)
+    tail = rows_of(9, K, torch.bfloat16, 77)
+    x[-9:] = tail.to(DEV)
+    codes, scales = moe.moe_mx4_quantize(x)
+    c, s = M.quantize(np64(tail))
+    assert (codes[-9:].cpu().numpy() == c).all() and (scales[-9:].cpu().numpy() == s).all()
+    assert not codes[:-9].any() and not scales[:-9].any()
+    v = moe.moe_mx4_dequantize(codes, scales, K, out=x)
+    assert torch.equal(v[-9:].cpu(), torch.from_numpy(M.values(c, s)).to(torch.bfloat16))
+
+
+def test_product_past_32_bits():
+    """An output of more than 2^31 values."""
+    rng = np.random.default_rng(12)
+    N, rows = 8192, (1 << 18) + 5
+    bc, bsc, wc, wsc = blocks(rng.standard_normal((N, 64)))
+    ac, asc, c, s = blocks(rng.standard_normal((261, 64)))
+    a_codes = torch.zeros(rows, 32, dtype=torch.uint8, device=DEV)
+    a_scales = torch.zeros(rows, 4, dtype=torch.uint8, device=DEV)
+    a_codes[-261:], a_scales[-261:] = ac, asc
+    out = moe.moe_mx4_product(a_codes, a_scales, bc, bsc)
+    ref = M.values(c, s) @ M.values(wc, wsc).T
+    mag = np.abs(M.values(c, s)) @ np.abs(M.values(wc, wsc)).T
+    got = np64(out[-261:])
+    assert (np.abs(got - ref) <= 128 * 2.0 ** -23 * mag + half_step(torch.bfloat16, ref)).all()
+    assert not out[:-261].any()
+
+
+def test_layer_example():
+    """The example's two paths against the 16-bit layer on the decoded weights.  Four-bit activations
+    leave each value off by up to an eighth of it, which a sum of many does not enlarge; 16-bit ones
+    leave the rounding of a and of the output."""
+    from examples import mx4_layer
+    prompt, single = mx4_layer.run(tokens=300, hidden=256, inter=384, experts=8, top_k=2, steps=4)
+    assert prompt < 0.3 and single < 4 * 2.0 ** -8
+
+
 # ----------------------------------------------------------------------------------- refusals
 def test_refusals():
     x = torch.zeros(4, 64, device=DEV)
