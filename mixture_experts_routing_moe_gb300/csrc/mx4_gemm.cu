@@ -15,12 +15,21 @@
 //   warps 4-6   scales of A and of the two halves of B: each lane holds 32 bytes (four slices) of
 //               four rows in registers, loads the next 32 ahead, and writes each slice's words to
 //               the chunk layout, 16 bytes at a time.  Groups start at any row, so no bulk copy of
-//               a fixed box would do; four bytes at a time per slice (the first form) kept the L1
-//               tag stage busy for 768 cycles a slice and held the product at 1.64 PFLOP/s.
+//               a fixed box would do.
 //   warps 8-15  epilogue: each warp takes 32 rows x 128 columns of the accumulator into registers
 //               at once and frees it, so the next tile's MMAs run while it converts and stores.
 //               (256 accumulator columns and the scales leave no room for a second accumulator.)
 // Waits are bounded; on expiry the status word records the timeout and every role leaves.
+//
+// What bounds it: at 8192^3 it runs in 161-163 us, 6.8 PFLOP/s; without the scales (skipped, to time
+// the rest) it takes 154, so the tensor pipe and its operands' way through shared memory are what
+// is left.  Deep K keeps that (K = 14336: 6.6); at K = 2048 a tile is 8 slices, and the 1400 cycles
+// in which the accumulator is emptied while no MMA can run are a fifth of it (3.4 with groups that
+// fill 78 % of their tiles).  On the way there, at 8192^3: scales four bytes at a time per slice,
+// 671 us (the L1 tag stage); pairs with a full release at cluster scope for each slice, 467 (it
+// waits for the warp's loads in flight), releasing shared memory only, 250; 16-byte chunk stores,
+// 238; whole-warp issue loops with an elected lane, 195; two slices behind one proxy fence, 184;
+// scale rows located once a tile and loaded 32 bytes at a time, 163.
 #include "launch.h"
 #include "mx4.cuh"
 #include "mx4_mma.cuh"
@@ -522,9 +531,11 @@ cudaError_t launch_cg(const CUtensorMap& a, const CUtensorMap& b, const CUtensor
   return cudaLaunchKernelEx(&cfg, kern, a, b, b2, p);
 }
 
-// Pairs when groups average at least 128 rows; below that a pair's taller tiles mostly multiply
-// padding.
-bool use_pairs(int64_t rows, int E) { return rows >= (int64_t)BM * E; }
+// Pairs when groups average at least 160 rows; below that a pair's taller tiles multiply mostly
+// padding, above it they read fewer bytes through L2.  Experts of 32 groups, H = 4096, I = 2048,
+// one CTA against a pair: 64 rows a group 91 / 96 us, 96 95 / 102, 128 105 / 107, 192 119 / 112,
+// 512 229 / 219.
+bool use_pairs(int64_t rows, int E) { return rows >= (int64_t)160 * E; }
 
 template <bool GATEUP, typename T>
 cudaError_t launch(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& b2,

@@ -82,6 +82,17 @@ struct TokensParams {
   int ncap_raw;      // ncap rounded up to 32
 };
 
+// The second launch may start once all CTAs of the first one run (start_next): it sets up its
+// barriers and tensor memory and waits for the first to end (wait_previous) before it reads what
+// that wrote (single token 24.3 -> 23.4 us of device time; between the launches of the experts the
+// same gave nothing).
+__device__ __forceinline__ void start_next() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 __device__ __forceinline__ unsigned ld_acquire_u32(const unsigned* p) {
   unsigned v;
   asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
@@ -218,6 +229,7 @@ constexpr int kEB = 4, kTB = 8, kFirstWarps = 8;
 template <typename T>
 __global__ void __launch_bounds__(kFirstWarps * 32)
     moe_mx4_tokens_first(const TokensParams p, int logit_ctas) {
+  start_next();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (blockIdx.x == 0)
     for (size_t i = threadIdx.x; i < p.zeroed; i += kFirstWarps * 32) p.status[i] = 0;
@@ -355,6 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_alloc(smem_u32(tmem_slot), kTmemCols);
   for (int e = threadIdx.x; e < p.E; e += kThreads) mask[e] = 0;
 
+  wait_previous();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -932,16 +945,18 @@ cudaError_t launch_t(const Mx4TokensArgs& a, cudaStream_t s) {
   moe_mx4_tokens_first<T><<<logit_ctas + split_ctas, kFirstWarps * 32, 0, s>>>(p, logit_ctas);
   err = cudaGetLastError();
   if (err != cudaSuccess) return err;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeCooperative;
   attr[0].val.cooperative = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(sms);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kern, mg, mu, md, mx, ma, p);
 }
 
