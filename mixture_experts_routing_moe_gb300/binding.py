@@ -411,14 +411,24 @@ def _mx4_pitch(K: int):
     return 16 * blocks, -(-blocks // 4) * 4
 
 
+@functools.lru_cache(maxsize=4096)
+def _mx4_scale_shape(shape, K: int):
+    """The shape of the scales that go with codes of a shape; None if those are not rows of K."""
+    pc, ps = _mx4_pitch(K)
+    return (*shape[:-1], ps) if len(shape) and shape[-1] == pc else None
+
+
+_u8 = torch.uint8
+
+
 def _mx4_rows(codes, scales, K: int, where: str):
     """Checks one operand in blocks, [..., rows] rows of K values; returns the shape of codes."""
     if not (codes.is_cuda and scales.is_cuda and codes.is_contiguous() and scales.is_contiguous()):
         raise ValueError("libmoe takes contiguous CUDA tensors")
-    if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
+    if codes.dtype is not _u8 or scales.dtype is not _u8:
         raise MoeError(3, f"{where}: codes and scales are uint8")
     shape = codes.shape
-    if (shape[-1], scales.shape[-1]) != _mx4_pitch(K) or scales.shape[:-1] != shape[:-1]:
+    if scales.shape != _mx4_scale_shape(shape, K):
         raise MoeError(2, f"{where}: rows of {K} values have {_mx4_pitch(K)} bytes of codes and "
                           "scales")
     return shape
@@ -441,8 +451,26 @@ def _mx4_dtype(t) -> int:
 
 def _mx4_ws(ws, need: int, device):
     if ws is None:
-        return torch.empty(need, dtype=torch.uint8, device=device)
+        return torch.empty(need, dtype=_u8, device=device)
     _cuda(ws)
+    return ws
+
+
+# The 256-byte workspaces (status words) of products whose caller gives none, one a stream: the calls
+# of a stream follow one another, as those that share a workspace have to.
+_mx4_status = {}
+
+
+def _mx4_status_ws(ws, stream: int, device):
+    if ws is not None:
+        _cuda(ws)
+        return ws
+    key = (device.index, stream)
+    ws = _mx4_status.get(key)
+    if ws is None:
+        if torch.cuda.is_current_stream_capturing():  # a graph's memory is not ours to keep
+            return torch.empty(256, dtype=_u8, device=device)
+        ws = _mx4_status[key] = torch.empty(256, dtype=_u8, device=device)
     return ws
 
 
@@ -457,9 +485,9 @@ def moe_mx4_quantize(x, codes=None, scales=None, stream=None):
     pc, ps = _mx4_pitch(K)
     lead = (shape[0],) if len(shape) == 2 else shape[:-1]
     if codes is None:
-        codes = torch.empty((*lead, pc), dtype=torch.uint8, device=x.device)
+        codes = torch.empty((*lead, pc), dtype=_u8, device=x.device)
     if scales is None:
-        scales = torch.empty((*lead, ps), dtype=torch.uint8, device=x.device)
+        scales = torch.empty((*lead, ps), dtype=_u8, device=x.device)
     if given and _mx4_rows(codes, scales, K, "moe_mx4_quantize")[:-1] != shape[:-1]:
         raise MoeError(2, "moe_mx4_quantize: codes have other rows than x")
     _check(lib().moe_mx4_quantize(x.data_ptr(), dt, x.numel() // K if K else 0, K, ld,
@@ -512,11 +540,12 @@ def moe_mx4_product(a_codes, a_scales, b_codes, b_scales, offsets=None, dtype=to
         raise MoeError(2, "moe_mx4_product: out has another shape")
     else:
         _cuda(out)
-    ws = _mx4_ws(ws, 256, a_codes.device)
+    s = _stream(stream)
+    ws = _mx4_status_ws(ws, s, out.device)
     _check(lib().moe_mx4_product(a_codes.data_ptr(), a_scales.data_ptr(), rows,
                                  b_codes.data_ptr(), b_scales.data_ptr(), off, E, N, K,
-                                 out.data_ptr(), _mx4_dtype(out), ws.data_ptr(), ws.numel(),
-                                 _stream(stream)), where)
+                                 out.data_ptr(), _mx4_dtype(out), ws.data_ptr(), ws.numel(), s),
+           where)
     return out
 
 
