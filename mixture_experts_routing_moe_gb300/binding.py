@@ -449,9 +449,12 @@ def _mx4_dtype(t) -> int:
     return _code(t) if code is None else code
 
 
-def _mx4_ws(ws, need: int, device):
+def _mx4_ws(ws, need: int, device, stream):
     if ws is None:
-        return torch.empty(need, dtype=_u8, device=device)
+        ws = torch.empty(need, dtype=_u8, device=device)
+        if stream is not None:  # its memory may not be handed out again before that stream is done
+            ws.record_stream(stream)
+        return ws
     _cuda(ws)
     return ws
 
@@ -580,7 +583,7 @@ def moe_mx4_experts_forward_dispatched(x_d, offsets, gate, up, down, y=None, ws=
         raise MoeError(2, f"{where}: y is not like x_d")
     else:
         _cuda(y)
-    ws = _mx4_ws(ws, mx4_experts_workspace_bytes(rows, H, I), x_d.device)
+    ws = _mx4_ws(ws, mx4_experts_workspace_bytes(rows, H, I), x_d.device, stream)
     _check(lib().moe_mx4_experts_forward_dispatched(
         x_d.data_ptr(), _mx4_dtype(x_d), off, rows, gate[0].data_ptr(), gate[1].data_ptr(),
         up[0].data_ptr(), up[1].data_ptr(), down[0].data_ptr(), down[1].data_ptr(), E, H, I,
@@ -613,7 +616,8 @@ def moe_mx4_forward_tokens(x, router, gate, up, down, top_k: int, renormalize: b
         raise MoeError(2, f"{where}: out is not like x")
     else:
         _cuda(out)
-    ws = _mx4_ws(ws, max(mx4_tokens_workspace_bytes(T, E, H, I, top_k, x.dtype), 256), x.device)
+    ws = _mx4_ws(ws, max(mx4_tokens_workspace_bytes(T, E, H, I, top_k, x.dtype), 256), x.device,
+                 stream)
     _check(lib().moe_mx4_forward_tokens(
         x.data_ptr(), router.data_ptr(), _mx4_dtype(x), gate[0].data_ptr(), gate[1].data_ptr(),
         up[0].data_ptr(), up[1].data_ptr(), down[0].data_ptr(), down[1].data_ptr(), T, E, H, I,

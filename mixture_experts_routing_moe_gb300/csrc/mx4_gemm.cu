@@ -488,6 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
 
+  settle_after_abort(abort_f);
   tc_fence_before();
   __syncwarp();
   if (CG == 2) cluster_sync_all();  // no CTA leaves while its pair may still signal it

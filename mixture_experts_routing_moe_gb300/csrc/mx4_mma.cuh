@@ -83,6 +83,14 @@ static __device__ __forceinline__ void wait_until(uint32_t bar, uint32_t parity,
   }
 }
 
+// After an abort, before the CTA's shared memory may go to another: copies that no wait saw land had
+// 2^24 cycles (8 ms) to do so.
+static __device__ __forceinline__ void settle_after_abort(volatile int* abort_f) {
+  if (!*abort_f) return;
+  const long long until = clock64() + (1 << 24);
+  while (clock64() < until) __nanosleep(1000);
+}
+
 // Register budget of the calling warpgroup (every warp of it executes this).
 template <int N>
 static __device__ __forceinline__ void set_max_regs_dec() {

@@ -27,8 +27,8 @@
 //   2  units of work: (expert, 64 columns of a) for gate/up, then (expert, 128 columns of the
 //      output, part of K) for down, dealt to the CTAs in turn.  Warp roles as in the grouped
 //      products: weight codes (TMA), token terms (TMA), raw scales, scales, MMA, epilogue, in slices
-//      of K = 256.  The gate/up epilogue writes a as terms (aq, as; rows in the order of
-//      the lists) and counts the unit on its expert; a down unit's weights are loaded ahead, its
+//      of K = 256.  The gate/up epilogue writes a as terms (aq, as; rows in the order of the lists)
+//      and another warp counts the unit on its expert; a down unit's weights are loaded ahead, its
 //      tokens once that count is full.  The weight loads never wait for anything but a free slot,
 //      from the first unit to the last.
 //   3  the down epilogue writes y (FP32, one row a slot and part); once every CTA has counted its
@@ -36,7 +36,6 @@
 //      finished an output tile's last unit add it up put several such sums, 20 to 70 us each, on
 //      the CTAs that were late already: 775 to 1045 us for the layer of 256 experts.)
 // Waits are bounded; on expiry the status word records the timeout and every role leaves.
-//
 #include "launch.h"
 #include "mx4.cuh"
 #include "mx4_mma.cuh"
@@ -61,7 +60,8 @@ constexpr int kRaw = 3;            // raw scale slots (four slices each) of weig
 // two accumulators, then the scales of two slices: 2 x 4 columns for A, 2 x 8 for B
 constexpr uint32_t kTmemCols = 512, kScaleCol = 2 * kMaxN;
 static_assert(kScaleCol + 2 * 24 <= kTmemCols, "tensor memory");
-constexpr int kExchange = 16 * 64 * 4;  // u of up to 16 tokens x 64 columns
+constexpr int kPer = 32 / P;              // tokens that the epilogue takes at a time
+constexpr int kExchange = kPer * 64 * 4;  // their gate or up columns on the way between warps
 
 struct TokensParams {
   const void* x;
@@ -687,9 +687,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             uint4 v = make_uint4(0, 0, 0, 0);
-            // (rows past the unit's columns hold old bytes: any finite or NaN scale of a column
-            // that is not read)
-            if (tokens ? 32 * j < r.cols : j < 4) v = ld_shared_v4(slot + raw_offset(32 * j + lane, h));
+            // (rows past the unit's columns hold old bytes: scales of columns that nobody reads)
+            if (tokens ? 32 * j < r.cols : j < 4)
+              v = ld_shared_v4(slot + raw_offset(32 * j + lane, h));
             now[j][4 * h] = v.x, now[j][4 * h + 1] = v.y;
             now[j][4 * h + 2] = v.z, now[j][4 * h + 3] = v.w;
           }
@@ -744,7 +744,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp >= 8) {
     // ---------------------------------------------------------------- epilogue
-    constexpr int PER = 32 / P;  // tokens at a time
+    constexpr int PER = kPer;
     const int q = warp & 3;
     int acc = 0, count = 0;
     uint32_t acc_phase = 0;
@@ -858,6 +858,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
 
+  settle_after_abort(abort_f);
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {

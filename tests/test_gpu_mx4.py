@@ -438,6 +438,26 @@ def test_tokens_ties_and_bad_rows():
     assert np.allclose(np64(w)[~bad], 1 / 3, atol=1e-6)
 
 
+def test_experts_on_another_stream_keep_their_workspace():
+    """A call on a side stream: the workspace it made for itself is not handed out again while that
+    stream still works (the current stream allocates and overwrites as much right after)."""
+    rng = np.random.default_rng(21)
+    E, H, I, rows = 4, 512, 768, 2048
+    x = torch.from_numpy(rng.standard_normal((rows, H))).to(torch.bfloat16).to(DEV)
+    packed = [blocks(rng.standard_normal(s))[:2] for s in ((E, I, H), (E, I, H), (E, H, I))]
+    off, _ = offsets_of([rows // E] * E)
+    want = moe.moe_mx4_experts_forward_dispatched(x, off, *packed)
+    side = torch.cuda.Stream()
+    for _ in range(5):
+        side.wait_stream(torch.cuda.current_stream())
+        got = moe.moe_mx4_experts_forward_dispatched(x, off, *packed, stream=side)
+        for _ in range(4):
+            torch.empty(moe.mx4_experts_workspace_bytes(rows, H, I), dtype=torch.uint8,
+                        device=DEV).fill_(255)
+        side.synchronize()
+        assert torch.equal(got, want)
+
+
 def test_tokens_none():
     _, router, packed = layer(1, 4, 128, 128, torch.bfloat16, 2)
     out = moe.moe_mx4_forward_tokens(torch.empty(0, 128, dtype=torch.bfloat16, device=DEV),
