@@ -418,7 +418,7 @@ def _mx4_scale_shape(shape, K: int):
     return (*shape[:-1], ps) if len(shape) and shape[-1] == pc else None
 
 
-_u8 = torch.uint8
+_u8, _empty = torch.uint8, torch.empty
 
 
 def _mx4_rows(codes, scales, K: int, where: str):
@@ -449,31 +449,28 @@ def _mx4_dtype(t) -> int:
     return _code(t) if code is None else code
 
 
-def _mx4_ws(ws, need: int, device, stream):
-    if ws is None:
-        ws = torch.empty(need, dtype=_u8, device=device)
-        if stream is not None:  # its memory may not be handed out again before that stream is done
-            ws.record_stream(stream)
-        return ws
-    _cuda(ws)
-    return ws
+# Workspaces of calls that were given none, one for each stream, kept from call to call up to a size:
+# the calls of a stream follow one another, as those that share a workspace have to.
+_mx4_kept = {}
+_MX4_KEPT_BYTES = 64 << 20
 
 
-# The 256-byte workspaces (status words) of products whose caller gives none, one a stream: the calls
-# of a stream follow one another, as those that share a workspace have to.
-_mx4_status = {}
-
-
-def _mx4_status_ws(ws, stream: int, device):
+def _mx4_ws(ws, need: int, device, stream, handle: int):
+    """The caller's workspace, or one of at least `need` bytes for a call on stream `handle`
+    (`stream`, or the current one if that is None)."""
     if ws is not None:
         _cuda(ws)
         return ws
-    key = (device.index, stream)
-    ws = _mx4_status.get(key)
-    if ws is None:
-        if torch.cuda.is_current_stream_capturing():  # a graph's memory is not ours to keep
-            return torch.empty(256, dtype=_u8, device=device)
-        ws = _mx4_status[key] = torch.empty(256, dtype=_u8, device=device)
+    # A captured call gets its own: the graph may run beside later calls.
+    if stream is None and need <= _MX4_KEPT_BYTES and not torch.cuda.is_current_stream_capturing():
+        key = (device.index, handle)
+        ws = _mx4_kept.get(key)
+        if ws is None or ws.numel() < need:
+            ws = _mx4_kept[key] = _empty(need, dtype=_u8, device=device)
+        return ws
+    ws = _empty(need, dtype=_u8, device=device)
+    if stream is not None:  # its memory may not be handed out again before that stream is done
+        ws.record_stream(stream)
     return ws
 
 
@@ -482,20 +479,24 @@ def moe_mx4_quantize(x, codes=None, scales=None, stream=None):
     [..., 4 ceil(K/128)]).  x is contiguous, or two-dimensional with rows a stride apart."""
     shape = x.shape
     K = shape[-1]
-    ld = _mx4_leading(x, K, "moe_mx4_quantize")
-    dt = _mx4_dtype(x)
+    ld = K if x.is_cuda and x.is_contiguous() else _mx4_leading(x, K, "moe_mx4_quantize")
+    dt = DTYPE_CODE.get(x.dtype)
+    if dt is None:
+        dt = _code(x)  # raises
     given = codes is not None or scales is not None
-    pc, ps = _mx4_pitch(K)
-    lead = (shape[0],) if len(shape) == 2 else shape[:-1]
-    if codes is None:
-        codes = torch.empty((*lead, pc), dtype=_u8, device=x.device)
-    if scales is None:
-        scales = torch.empty((*lead, ps), dtype=_u8, device=x.device)
+    if codes is None or scales is None:
+        pc, ps = _mx4_pitch(K)
+        lead = (shape[0],) if len(shape) == 2 else shape[:-1]
+        dev = x.device
+        codes = _empty((*lead, pc), dtype=_u8, device=dev) if codes is None else codes
+        scales = _empty((*lead, ps), dtype=_u8, device=dev) if scales is None else scales
     if given and _mx4_rows(codes, scales, K, "moe_mx4_quantize")[:-1] != shape[:-1]:
         raise MoeError(2, "moe_mx4_quantize: codes have other rows than x")
-    _check(lib().moe_mx4_quantize(x.data_ptr(), dt, x.numel() // K if K else 0, K, ld,
-                                  codes.data_ptr(), scales.data_ptr(), _stream(stream)),
-           "moe_mx4_quantize")
+    st = (_lib or lib()).moe_mx4_quantize(
+        x.data_ptr(), dt, shape[0] if len(shape) == 2 else x.numel() // max(K, 1), K, ld,
+        codes.data_ptr(), scales.data_ptr(), _stream(stream))
+    if st:
+        raise MoeError(st, "moe_mx4_quantize")
     return codes, scales
 
 
@@ -504,15 +505,21 @@ def moe_mx4_dequantize(codes, scales, K: int, dtype=torch.bfloat16, out=None, st
     shape = _mx4_rows(codes, scales, K, "moe_mx4_dequantize")
     if out is None:
         lead = (shape[0],) if len(shape) == 2 else shape[:-1]
-        out = torch.empty((*lead, K), dtype=dtype, device=codes.device)
+        out = _empty((*lead, K), dtype=dtype, device=codes.device)
         ld = K
     else:
         if out.shape != (*shape[:-1], K):
             raise MoeError(2, "moe_mx4_dequantize: out has another shape")
         ld = _mx4_leading(out, K, "moe_mx4_dequantize")
-    _check(lib().moe_mx4_dequantize(codes.data_ptr(), scales.data_ptr(),
-                                    out.numel() // K if K else 0, K, out.data_ptr(),
-                                    _mx4_dtype(out), ld, _stream(stream)), "moe_mx4_dequantize")
+    dt = DTYPE_CODE.get(out.dtype)
+    if dt is None:
+        dt = _code(out)  # raises
+    st = (_lib or lib()).moe_mx4_dequantize(
+        codes.data_ptr(), scales.data_ptr(),
+        shape[0] if len(shape) == 2 else out.numel() // max(K, 1), K, out.data_ptr(), dt, ld,
+        _stream(stream))
+    if st:
+        raise MoeError(st, "moe_mx4_dequantize")
     return out
 
 
@@ -544,7 +551,7 @@ def moe_mx4_product(a_codes, a_scales, b_codes, b_scales, offsets=None, dtype=to
     else:
         _cuda(out)
     s = _stream(stream)
-    ws = _mx4_status_ws(ws, s, out.device)
+    ws = _mx4_ws(ws, 256, out.device, stream, s)
     _check(lib().moe_mx4_product(a_codes.data_ptr(), a_scales.data_ptr(), rows,
                                  b_codes.data_ptr(), b_scales.data_ptr(), off, E, N, K,
                                  out.data_ptr(), _mx4_dtype(out), ws.data_ptr(), ws.numel(), s),
@@ -583,11 +590,12 @@ def moe_mx4_experts_forward_dispatched(x_d, offsets, gate, up, down, y=None, ws=
         raise MoeError(2, f"{where}: y is not like x_d")
     else:
         _cuda(y)
-    ws = _mx4_ws(ws, mx4_experts_workspace_bytes(rows, H, I), x_d.device, stream)
+    s = _stream(stream)
+    ws = _mx4_ws(ws, max(mx4_experts_workspace_bytes(rows, H, I), 256), x_d.device, stream, s)
     _check(lib().moe_mx4_experts_forward_dispatched(
         x_d.data_ptr(), _mx4_dtype(x_d), off, rows, gate[0].data_ptr(), gate[1].data_ptr(),
         up[0].data_ptr(), up[1].data_ptr(), down[0].data_ptr(), down[1].data_ptr(), E, H, I,
-        y.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream)), where)
+        y.data_ptr(), ws.data_ptr(), ws.numel(), s), where)
     return y
 
 
@@ -616,11 +624,12 @@ def moe_mx4_forward_tokens(x, router, gate, up, down, top_k: int, renormalize: b
         raise MoeError(2, f"{where}: out is not like x")
     else:
         _cuda(out)
+    s = _stream(stream)
     ws = _mx4_ws(ws, max(mx4_tokens_workspace_bytes(T, E, H, I, top_k, x.dtype), 256), x.device,
-                 stream)
+                 stream, s)
     _check(lib().moe_mx4_forward_tokens(
         x.data_ptr(), router.data_ptr(), _mx4_dtype(x), gate[0].data_ptr(), gate[1].data_ptr(),
         up[0].data_ptr(), up[1].data_ptr(), down[0].data_ptr(), down[1].data_ptr(), T, E, H, I,
         top_k, int(bool(renormalize)), out.data_ptr(), _ptr(idx), _ptr(w), ws.data_ptr(),
-        ws.numel(), _stream(stream)), where)
+        ws.numel(), s), where)
     return out

@@ -458,6 +458,26 @@ def test_experts_on_another_stream_keep_their_workspace():
         assert torch.equal(got, want)
 
 
+def test_graph_and_eager_calls_do_not_share_a_workspace():
+    """A captured call has a workspace of its own: its replays leave the one that the stream's eager
+    calls keep as it is."""
+    x, router, packed = layer(8, 16, 512, 384, torch.bfloat16, 31)
+    args = [x.to(DEV), router.to(DEV)] + [p[:2] for p in packed]
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        want = moe.moe_mx4_forward_tokens(*args, top_k=4)
+        kept = B._mx4_kept[(torch.cuda.current_device(), s.cuda_stream)]
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            out = moe.moe_mx4_forward_tokens(*args, top_k=4)
+        kept.fill_(0xAA)
+        g.replay()
+        s.synchronize()
+    assert torch.equal(out, want) and (kept == 0xAA).all()
+    with torch.cuda.stream(s):
+        assert torch.equal(moe.moe_mx4_forward_tokens(*args, top_k=4), want)
+
+
 def test_tokens_none():
     _, router, packed = layer(1, 4, 128, 128, torch.bfloat16, 2)
     out = moe.moe_mx4_forward_tokens(torch.empty(0, 128, dtype=torch.bfloat16, device=DEV),
