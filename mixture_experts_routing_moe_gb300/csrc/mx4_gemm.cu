@@ -48,6 +48,7 @@ constexpr int kThreads = 512;
 constexpr int kRegsIssue = 72, kRegsScales = 104, kRegsEpilogue = 168;
 constexpr int kMaxExperts = 1024;
 constexpr int kBarBytes = 256;
+constexpr int kTurnBytes = 1024;  // an epilogue warp's: 32 rows x 32 bytes
 constexpr uint32_t kTmemCols = 512, kScaleCol = 256;
 
 // CG: CTAs of a tile
@@ -57,7 +58,7 @@ struct Shape {
   static constexpr int A_BYTES = BM * 128, B_BYTES = BN / CG * 128;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
   static constexpr size_t SMEM = 1024 + (size_t)STAGES * (STAGE_BYTES + SF_BYTES) + kBarBytes +
-                                 2 * (kMaxExperts + 4) * sizeof(int);
+                                 (kMaxExperts + 4) * sizeof(int) + 8 * kTurnBytes;
 };
 static_assert(Shape<1>::SMEM <= 232448 && Shape<2>::SMEM <= 232448, "shared memory of a CTA");
 
@@ -71,6 +72,7 @@ struct Params {
   int scales_align;          // see load_scales()
   int E, N, KB, NT;          // N: rows of one expert's B (gate/up: I); KB: 256-deep slices
   void* out;
+  int store;                 // bytes of a store: 32 or 16 where they divide the pitch and the base
   uint8_t* codes;            // gate/up: rows of N values in blocks
   uint8_t* scales;
   unsigned* status;
@@ -110,23 +112,61 @@ __device__ __forceinline__ void st_v8(void* p, const uint4& a, const uint4& b) {
                "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
                : "memory");
 }
-// 32 accumulator columns of a row.  vec: the row pitch and the base are multiples of 32 bytes, so
-// that a store fills a whole 32-byte sector (16-byte stores cost twice the requests).
+// 32 accumulator columns of a row, 32 bytes (a whole sector; 16 cost twice the requests) or 16 at a
+// time; the last columns of a row of a ragged N one by one.
 template <typename T>
-__device__ __forceinline__ void store_row(T* row, const float* v, int col0, int N, bool vec) {
+__device__ __forceinline__ void store_row(T* row, const float* v, int col0, int N, int store) {
   constexpr int W = 16 / sizeof(T);
-  if (vec && col0 + 32 <= N) {
+  if (col0 + 32 <= N) {
 #pragma unroll
     for (int i = 0; i < 32 / W; i += 2) {
       Vec16<T> q, r;
       q.from_float(v + i * W);
       r.from_float(v + (i + 1) * W);
-      st_v8(row + col0 + i * W, q.u, r.u);
+      if (store == 32) {
+        st_v8(row + col0 + i * W, q.u, r.u);
+      } else {
+        st_v4(row + col0 + i * W, q.u);
+        st_v4(row + col0 + (i + 1) * W, r.u);
+      }
     }
   } else {
 #pragma unroll
     for (int i = 0; i < 32; ++i)
       if (col0 + i < N) row[col0 + i] = Dt<T>::from_f(v[i]);
+  }
+}
+// A warp's 32 rows x 128 columns of an output whose rows are not 16-byte aligned (out: row 0, the
+// warp's first column; rows, cols: how many of them exist): 32 bytes of each row at a time go through
+// shared memory, so that a store's lanes write neighbouring elements of two (f32: four) rows.  With
+// each lane writing its own row, element by element, 5467 x 6895 f16 with K = 512 took 342 us.
+template <typename T>
+__device__ __forceinline__ void store_turned(T* out, int64_t pitch, const uint32_t (&acc)[4][32],
+                                             int rows, int cols, uint8_t* turn, int lane) {
+  constexpr int CW = 32 / sizeof(T), RW = 32 / CW;  // columns of a piece, rows of a store
+  const int rsub = lane / CW, col = lane % CW;
+#pragma unroll
+  for (int c0 = 0; c0 < 128; c0 += CW) {
+    if (c0 < cols) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        Vec16<T> q;
+#pragma unroll
+        for (int i = 0; i < Vec16<T>::N; ++i) {
+          const int e = c0 + h * Vec16<T>::N + i;
+          q.e[i] = Dt<T>::from_f(__uint_as_float(acc[e / 32][e % 32]));
+        }
+        *reinterpret_cast<uint4*>(turn + raw_offset(lane, h)) = q.u;
+      }
+      __syncwarp();
+#pragma unroll 4
+      for (int r = 0; r < 32; r += RW) {
+        const int rr = r + rsub, at = col * (int)sizeof(T);
+        const T v = *reinterpret_cast<const T*>(turn + raw_offset(rr, at >> 4) + (at & 15));
+        if (rr < rows && c0 + col < cols) out[rr * pitch + c0 + col] = v;
+      }
+      __syncwarp();
+    }
   }
 }
 
@@ -149,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 3);
   volatile int* abort_f = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* pref = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + kBarBytes);
-  int* offs = pref + (kMaxExperts + 4);
+  uint8_t* turn = reinterpret_cast<uint8_t*>(pref + (kMaxExperts + 4));  // 16-byte aligned
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = CG == 2 ? (int)cluster_rank() : 0;
@@ -172,11 +212,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (CG == 2) tmem_alloc2(smem_u32(tmem_slot), kTmemCols);
     else tmem_alloc(smem_u32(tmem_slot), kTmemCols);
   }
-  // a copy of the offsets, kept inside [0, rows] whatever the caller's array holds
-  for (int i = threadIdx.x; i <= p.E; i += kThreads) {
-    const int64_t v = p.offsets ? (int64_t)__ldg(p.offsets + i) : (i ? p.rows : 0);
-    offs[i] = (int)min(max(v, (int64_t)0), p.rows);
-  }
+  // first row of group e, kept inside [0, rows] whatever the caller's array holds
+  auto offset_of = [&](int e) {
+    const int64_t v = p.offsets ? (int64_t)__ldg(p.offsets + e) : (e ? p.rows : 0);
+    return (int)min(max(v, (int64_t)0), p.rows);
+  };
+  int* offs = reinterpret_cast<int*>(turn);  // until the prefix is built
+  static_assert((kMaxExperts + 1) * sizeof(int) <= 8 * kTurnBytes, "offsets fit");
+  for (int i = threadIdx.x; i <= p.E; i += kThreads) offs[i] = offset_of(i);
   __syncthreads();
   if (warp == 2)
     build_expert_prefix(
@@ -208,8 +251,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // eight m-tiles beside one n-tile, then the next n-tile
     const int g0 = local / (8 * p.NT) * 8, gm = min(8, mt - g0), q = local - g0 * p.NT;
     x.n = q / gm;
-    x.r0 = offs[x.e] + (g0 + q % gm) * (BM * CG) + rank * BM;
-    x.r1 = offs[x.e + 1];
+    x.r0 = offset_of(x.e) + (g0 + q % gm) * (BM * CG) + rank * BM;
+    x.r1 = offset_of(x.e + 1);
     return x;
   };
 
@@ -448,7 +491,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) arrive_leader(tempty);
       const int row = x.r0 + q * 32 + lane;
-      if (row < x.r1) {
+      if (!GATEUP && p.store < 16) {
+        const int col0 = x.n * BN + h * 128;
+        store_turned((T*)p.out + (int64_t)(x.r0 + q * 32) * p.N + col0, p.N, acc,
+                     x.r1 - x.r0 - q * 32, p.N - col0, turn + (warp - 8) * kTurnBytes, lane);
+      } else if (row < x.r1) {
         if (GATEUP) {
           // columns 0-63 gate, 64-127 up of a's columns n * 128 + h * 64 ..: two blocks
           const int64_t cp = code_pitch(p.N), sp = scale_pitch(p.N);
@@ -478,11 +525,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         } else {
           T* orow = (T*)p.out + (int64_t)row * p.N;
-          const bool vec = ((uintptr_t)p.out & 31u) == 0 && (p.N * sizeof(T)) % 32 == 0;
 #pragma unroll
           for (int c = 0; c < 4; ++c)
             store_row(orow, reinterpret_cast<const float*>(acc[c]), x.n * BN + h * 128 + c * 32,
-                      p.N, vec);
+                      p.N, p.store);
         }
       }
     }
@@ -583,6 +629,8 @@ cudaError_t launch_mx4_product(Mx4Rows a, int64_t rows, Mx4Rows b, const int32_t
   p.b_scales = b.scales;
   p.scales_align = scales_align(p.scale_pitch, a.scales, b.scales, b.scales);
   p.out = out;
+  const uintptr_t both = (uintptr_t)out | (uintptr_t)N * (odt == MOE_F32 ? 4 : 2);
+  p.store = both % 32 == 0 ? 32 : both % 16 == 0 ? 16 : 1;
   p.zero_status = zero_status;
   switch (odt) {
     case MOE_F32: return launch<false, float>(ma, mb, mb, p, s);
