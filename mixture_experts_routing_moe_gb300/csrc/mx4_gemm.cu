@@ -170,10 +170,14 @@ __device__ __forceinline__ void store_turned(T* out, int64_t pitch, const uint32
   }
 }
 
-template <int CG, bool GATEUP, typename T>
+// What the epilogue writes: the blocks of a; rows that are 16-byte aligned; other rows.
+enum Kind { kGateUp, kRows, kTurned };
+
+template <int CG, int KIND, typename T>
 __global__ void __launch_bounds__(kThreads, 1)
     moe_mx4_gemm(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
                  const __grid_constant__ CUtensorMap mapB2, const Params p) {
+  constexpr bool GATEUP = KIND == kGateUp;
   using S = Shape<CG>;
   constexpr int STAGES = S::STAGES, STAGE_BYTES = S::STAGE_BYTES;
   extern __shared__ uint8_t mx4_smem_raw[];
@@ -491,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) arrive_leader(tempty);
       const int row = x.r0 + q * 32 + lane;
-      if (!GATEUP && p.store < 16) {
+      if (KIND == kTurned) {
         const int col0 = x.n * BN + h * 128;
         store_turned((T*)p.out + (int64_t)(x.r0 + q * 32) * p.N + col0, p.N, acc,
                      x.r1 - x.r0 - q * 32, p.N - col0, turn + (warp - 8) * kTurnBytes, lane);
@@ -553,10 +557,10 @@ int sm_count(cudaError_t* err) {
   return sms;
 }
 
-template <int CG, bool GATEUP, typename T>
+template <int CG, int KIND, typename T>
 cudaError_t launch_cg(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& b2,
                       const Params& p, int sms, cudaStream_t s) {
-  auto kern = moe_mx4_gemm<CG, GATEUP, T>;
+  auto kern = moe_mx4_gemm<CG, KIND, T>;
   cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)Shape<CG>::SMEM);
   if (err != cudaSuccess) return err;
@@ -584,14 +588,14 @@ cudaError_t launch_cg(const CUtensorMap& a, const CUtensorMap& b, const CUtensor
 // 512 229 / 219.
 bool use_pairs(int64_t rows, int E) { return rows >= (int64_t)160 * E; }
 
-template <bool GATEUP, typename T>
+template <int KIND, typename T>
 cudaError_t launch(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& b2,
                    const Params& p, cudaStream_t s) {
   cudaError_t err;
   const int sms = sm_count(&err);
   if (err != cudaSuccess) return err;
-  return use_pairs(p.rows, p.E) ? launch_cg<2, GATEUP, T>(a, b, b2, p, sms, s)
-                                : launch_cg<1, GATEUP, T>(a, b, b2, p, sms, s);
+  return use_pairs(p.rows, p.E) ? launch_cg<2, KIND, T>(a, b, b2, p, sms, s)
+                                : launch_cg<1, KIND, T>(a, b, b2, p, sms, s);
 }
 
 // Of 32, 16 and 4, the largest that divides the pitch and the three bases.
@@ -632,10 +636,16 @@ cudaError_t launch_mx4_product(Mx4Rows a, int64_t rows, Mx4Rows b, const int32_t
   const uintptr_t both = (uintptr_t)out | (uintptr_t)N * (odt == MOE_F32 ? 4 : 2);
   p.store = both % 32 == 0 ? 32 : both % 16 == 0 ? 16 : 1;
   p.zero_status = zero_status;
+  const bool turned = p.store < 16;
   switch (odt) {
-    case MOE_F32: return launch<false, float>(ma, mb, mb, p, s);
-    case MOE_F16: return launch<false, __half>(ma, mb, mb, p, s);
-    case MOE_BF16: return launch<false, __nv_bfloat16>(ma, mb, mb, p, s);
+    case MOE_F32:
+      return turned ? launch<kTurned, float>(ma, mb, mb, p, s) : launch<kRows, float>(ma, mb, mb, p, s);
+    case MOE_F16:
+      return turned ? launch<kTurned, __half>(ma, mb, mb, p, s)
+                    : launch<kRows, __half>(ma, mb, mb, p, s);
+    case MOE_BF16:
+      return turned ? launch<kTurned, __nv_bfloat16>(ma, mb, mb, p, s)
+                    : launch<kRows, __nv_bfloat16>(ma, mb, mb, p, s);
   }
   return cudaErrorInvalidValue;
 }
@@ -655,7 +665,7 @@ cudaError_t launch_mx4_gate_up(Mx4Rows a, int64_t rows, Mx4Rows gate, Mx4Rows up
   p.scales_align = scales_align(p.scale_pitch, a.scales, gate.scales, up.scales);
   p.codes = codes;
   p.scales = scales;
-  return launch<true, float>(ma, mg, mu, p, s);
+  return launch<kGateUp, float>(ma, mg, mu, p, s);
 }
 
 }  // namespace moe
