@@ -11,6 +11,7 @@ import ctypes
 import functools
 import os
 import re
+import threading
 
 import torch
 
@@ -449,10 +450,27 @@ def _mx4_dtype(t) -> int:
     return _code(t) if code is None else code
 
 
-# Workspaces of calls that were given none, one for each stream, kept from call to call up to a size:
-# the calls of a stream follow one another, as those that share a workspace have to.
-_mx4_kept = {}
-_MX4_KEPT_BYTES = 64 << 20
+# Workspaces of calls that were given none, kept from call to call up to a size.  A call makes several
+# launches and the GIL is released while it makes them, so two threads' launches may interleave on the
+# stream that they share (all threads start on the default one): each thread has buffers of its own,
+# one a stream, and the calls of one thread on one stream follow one another.  A buffer that is
+# outgrown, or belongs to a thread that ended, goes back to torch, which hands it out again behind the
+# work of the stream it was made on (as with any tensor, a stream from outside torch has to stay
+# alive until then).
+class _Mx4Kept(threading.local):
+    """(device, stream handle) -> the calling thread's workspace there."""
+
+    def __init__(self):
+        self.of = {}
+
+    def __getitem__(self, key):
+        return self.of[key]
+
+
+_mx4_kept = _Mx4Kept()
+# Calls that need more take longer on the device than an allocation takes on the host.
+_MX4_KEPT_BYTES = 8 << 20
+_MX4_KEPT_STREAMS = 4  # of a thread; the oldest buffer makes room
 
 
 def _mx4_ws(ws, need: int, device, stream, handle: int):
@@ -463,10 +481,12 @@ def _mx4_ws(ws, need: int, device, stream, handle: int):
         return ws
     # A captured call gets its own: the graph may run beside later calls.
     if stream is None and need <= _MX4_KEPT_BYTES and not torch.cuda.is_current_stream_capturing():
-        key = (device.index, handle)
-        ws = _mx4_kept.get(key)
+        key, of = (device.index, handle), _mx4_kept.of
+        ws = of.get(key)
         if ws is None or ws.numel() < need:
-            ws = _mx4_kept[key] = _empty(need, dtype=_u8, device=device)
+            if ws is None and len(of) >= _MX4_KEPT_STREAMS:
+                del of[next(iter(of))]
+            ws = of[key] = _empty(need, dtype=_u8, device=device)
         return ws
     ws = _empty(need, dtype=_u8, device=device)
     if stream is not None:  # its memory may not be handed out again before that stream is done

@@ -1,0 +1,48 @@
+"""What the binding does on the host around a microscaled 4-bit call, without a GPU."""
+import threading
+
+import pytest
+import torch
+
+from mixture_experts_routing_moe_gb300 import binding as B
+
+
+@pytest.fixture
+def on_cpu(monkeypatch):
+    """Workspaces come from the CPU; no stream is capturing."""
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    return torch.device("cpu")
+
+
+def test_threads_of_one_stream_have_workspaces_of_their_own(on_cpu):
+    """A call's launches may interleave with another thread's on the default stream."""
+    got, both = [], threading.Barrier(2)
+
+    def ask():
+        ws = [B._mx4_ws(None, n, on_cpu, None, 0) for n in (256, 4096, 1024)]
+        both.wait()
+        got.append([(w.data_ptr(), w.numel()) for w in ws])
+        both.wait()
+
+    threads = [threading.Thread(target=ask) for _ in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for (pa, na), (pb, nb) in zip(*got):
+        assert pa + na <= pb or pb + nb <= pa
+    assert all(n >= need for one in got for (_, n), need in zip(one, (256, 4096, 1024)))
+
+
+def test_kept_workspaces_are_few(on_cpu):
+    """A thread that moves over many streams does not keep a buffer for each of them."""
+    def run():
+        for handle in range(1, 100):
+            assert B._mx4_ws(None, 512, on_cpu, None, handle).numel() >= 512
+        kept.append(len(B._mx4_kept.of))
+
+    kept = []
+    t = threading.Thread(target=run)
+    t.start()
+    t.join()
+    assert kept and kept[0] <= 8
