@@ -127,6 +127,18 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+def _new(shape, dtype, device, stream):
+    """Memory for what a call on `stream` (None: the current one) writes.  It is that stream's: torch
+    may hand out a block of another stream whose queued work still uses it.  The current stream
+    counts as a user too, for a result that is freed while it is still read there."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(t.device))
+    return t
+
+
 def _cuda(*ts):
     for t in ts:
         if t is not None and (not t.is_cuda or not t.is_contiguous()):
@@ -488,10 +500,7 @@ def _mx4_ws(ws, need: int, device, stream, handle: int):
                 del of[next(iter(of))]
             ws = of[key] = _empty(need, dtype=_u8, device=device)
         return ws
-    ws = _empty(need, dtype=_u8, device=device)
-    if stream is not None:  # its memory may not be handed out again before that stream is done
-        ws.record_stream(stream)
-    return ws
+    return _new(need, _u8, device, stream)
 
 
 def moe_mx4_quantize(x, codes=None, scales=None, stream=None):
@@ -508,8 +517,8 @@ def moe_mx4_quantize(x, codes=None, scales=None, stream=None):
         pc, ps = _mx4_pitch(K)
         lead = (shape[0],) if len(shape) == 2 else shape[:-1]
         dev = x.device
-        codes = _empty((*lead, pc), dtype=_u8, device=dev) if codes is None else codes
-        scales = _empty((*lead, ps), dtype=_u8, device=dev) if scales is None else scales
+        codes = _new((*lead, pc), _u8, dev, stream) if codes is None else codes
+        scales = _new((*lead, ps), _u8, dev, stream) if scales is None else scales
     if given and _mx4_rows(codes, scales, K, "moe_mx4_quantize")[:-1] != shape[:-1]:
         raise MoeError(2, "moe_mx4_quantize: codes have other rows than x")
     st = (_lib or lib()).moe_mx4_quantize(
@@ -525,7 +534,7 @@ def moe_mx4_dequantize(codes, scales, K: int, dtype=torch.bfloat16, out=None, st
     shape = _mx4_rows(codes, scales, K, "moe_mx4_dequantize")
     if out is None:
         lead = (shape[0],) if len(shape) == 2 else shape[:-1]
-        out = _empty((*lead, K), dtype=dtype, device=codes.device)
+        out = _new((*lead, K), dtype, codes.device, stream)
         ld = K
     else:
         if out.shape != (*shape[:-1], K):
@@ -565,7 +574,7 @@ def moe_mx4_product(a_codes, a_scales, b_codes, b_scales, offsets=None, dtype=to
     E = sb[0] if len(sb) == 3 else 1
     off = None if offsets is None else _mx4_offsets(offsets, E, where)
     if out is None:
-        out = torch.empty((rows, N), dtype=dtype, device=a_codes.device)
+        out = _new((rows, N), dtype, a_codes.device, stream)
     elif out.shape != (rows, N):
         raise MoeError(2, "moe_mx4_product: out has another shape")
     else:
@@ -605,7 +614,7 @@ def moe_mx4_experts_forward_dispatched(x_d, offsets, gate, up, down, y=None, ws=
     E, I = _mx4_expert_weights(gate, up, down, H, where)
     off = _mx4_offsets(offsets, E, where)
     if y is None:
-        y = torch.empty_like(x_d)
+        y = _new(x_d.shape, x_d.dtype, x_d.device, stream)
     elif y.shape != x_d.shape or y.dtype != x_d.dtype:
         raise MoeError(2, f"{where}: y is not like x_d")
     else:
@@ -639,7 +648,7 @@ def moe_mx4_forward_tokens(x, router, gate, up, down, top_k: int, renormalize: b
             w is not None and (w.dtype != torch.float32 or w.shape != (T, top_k))):
         raise MoeError(2, f"{where}: idx is uint32 [T, top_k], w float32 [T, top_k]")
     if out is None:
-        out = torch.empty_like(x)
+        out = _new(x.shape, x.dtype, x.device, stream)
     elif out.shape != x.shape or out.dtype != x.dtype:
         raise MoeError(2, f"{where}: out is not like x")
     else:

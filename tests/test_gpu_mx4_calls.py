@@ -51,3 +51,47 @@ def test_two_threads_on_one_stream():
         t.join()
     torch.cuda.synchronize()
     assert not wrong
+
+
+def block_users(make, given):
+    """Calls make() with the side stream while the current one still has work queued on memory that it
+    has already given back, as much as each buffer of the call; the result, once all of it is done."""
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    torch.cuda._sleep(20_000_000)
+    for n in given:
+        torch.empty(n, dtype=torch.uint8, device=DEV).fill_(255)
+    got = make(side)
+    torch.cuda.synchronize()
+    return got
+
+
+def test_a_given_streams_memory_is_its_own():
+    """Results and workspace of a call on a given stream do not lie in memory that the current stream's
+    queued work still writes."""
+    E, H, I = 4, 256, 384
+    w = weights(E, H, I, 5)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(6)
+    x = torch.randn(8, H, generator=g, device=DEV).bfloat16()
+    router = (torch.randn(E, H, generator=g, device=DEV) * H ** -0.5).bfloat16()
+    rows = torch.randn(E * 300, H, generator=g, device=DEV).bfloat16()
+    off = torch.arange(E + 1, device=DEV, dtype=torch.int32) * 300
+    codes, scales = moe.moe_mx4_quantize(rows)
+    ws_rows = moe.mx4_experts_workspace_bytes(E * 300, H, I)
+    ws_x = moe.mx4_tokens_workspace_bytes(8, E, H, I, 2, x.dtype)
+    jobs = [
+        (lambda s: moe.moe_mx4_forward_tokens(x, router, *w, top_k=2, stream=s), (ws_x, 8 * H * 2)),
+        (lambda s: moe.moe_mx4_experts_forward_dispatched(rows, off, *w, stream=s),
+         (ws_rows, rows.numel() * 2)),
+        (lambda s: moe.moe_mx4_product(codes, scales, codes, scales, stream=s),
+         (256, rows.shape[0] ** 2 * 2)),
+        (lambda s: moe.moe_mx4_dequantize(codes, scales, H, stream=s), (rows.numel() * 2,)),
+        (lambda s: torch.cat([t.view(-1) for t in moe.moe_mx4_quantize(rows, stream=s)]),
+         (codes.numel(), scales.numel())),
+    ]
+    for make, given in jobs:
+        want = make(None)
+        torch.cuda.synchronize()
+        got = block_users(make, given)
+        assert torch.equal(got, want)

@@ -1,4 +1,5 @@
 """What the binding does on the host around a microscaled 4-bit call, without a GPU."""
+import contextlib
 import threading
 
 import pytest
@@ -46,3 +47,32 @@ def test_kept_workspaces_are_few(on_cpu):
     t.start()
     t.join()
     assert kept and kept[0] <= 8
+
+
+def test_workspace_of_a_given_stream_is_that_streams(monkeypatch):
+    """Memory that a call on a given stream writes is allocated on that stream: a block of the current
+    one may still be in use there."""
+    current, made_on = ["current"], []
+
+    @contextlib.contextmanager
+    def on(stream):
+        current.append(stream)
+        yield
+        current.pop()
+
+    class Memory:
+        device = "cuda"
+
+        def __init__(self, *args, **kwargs):
+            made_on.append(current[-1])
+
+        def record_stream(self, stream):
+            pass
+
+    monkeypatch.setattr(B, "_empty", Memory)
+    monkeypatch.setattr(torch, "empty", Memory)
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: current[-1])
+    for need in (256, 1 << 28):
+        B._mx4_ws(None, need, "cuda", "side", 7)
+    assert made_on == ["side", "side"] and current == ["current"]
