@@ -128,15 +128,19 @@ def _stream(stream):
 
 
 def _new(shape, dtype, device, stream):
-    """Memory for what a call on `stream` (None: the current one) writes.  It is that stream's: torch
-    may hand out a block of another stream whose queued work still uses it.  The current stream
-    counts as a user too, for a result that is freed while it is still read there."""
+    """Memory for what a call on `stream` (None: the current one) writes.  It is that stream's own:
+    torch may hand out a block of another stream whose queued work still uses it.  The current
+    stream counts as a user too, for a result that is freed while it is still read there."""
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
         t = torch.empty(shape, dtype=dtype, device=device)
     t.record_stream(torch.cuda.current_stream(t.device))
     return t
+
+
+def _new_ws(need: int, device, stream):
+    return _new(max(need, 256), torch.uint8, device, stream)
 
 
 def _cuda(*ts):
@@ -158,9 +162,9 @@ def moe_route(logits, top_k: int, renormalize: bool = True, idx=None, w=None, st
     _cuda(logits)
     T, E = logits.shape
     if idx is None:
-        idx = torch.empty(T, top_k, dtype=torch.uint32, device=logits.device)
+        idx = _new((T, top_k), torch.uint32, logits.device, stream)
     if w is None:
-        w = torch.empty(T, top_k, dtype=logits.dtype, device=logits.device)
+        w = _new((T, top_k), logits.dtype, logits.device, stream)
     _cuda(idx, w)
     _check(lib().moe_route(_ptr(logits), _code(logits), T, E, top_k, int(bool(renormalize)),
                            _ptr(idx), _ptr(w), _stream(stream)), "moe_route")
@@ -176,9 +180,9 @@ def moe_route_sigmoid_grouped(logits, top_k: int, groups: int, selected_groups: 
         raise MoeError(3, "bias must be float32")
     T, E = logits.shape
     if idx is None:
-        idx = torch.empty(T, top_k, dtype=torch.uint32, device=logits.device)
+        idx = _new((T, top_k), torch.uint32, logits.device, stream)
     if w is None:
-        w = torch.empty(T, top_k, dtype=logits.dtype, device=logits.device)
+        w = _new((T, top_k), logits.dtype, logits.device, stream)
     _cuda(idx, w)
     _check(lib().moe_route_sigmoid_grouped(
         _ptr(logits), _code(logits), _ptr(bias), T, E, top_k, groups, selected_groups,
@@ -197,7 +201,7 @@ def moe_selected_router_weights(logits, idx, scoring: str = "softmax", renormali
     _cuda(logits, idx)
     T, E = logits.shape
     k = idx.shape[1]
-    w = torch.empty(T, k, dtype=torch.float32, device=logits.device) if w is None else w
+    w = _new((T, k), torch.float32, logits.device, stream) if w is None else w
     _cuda(w)
     _check(lib().moe_selected_router_weights(
         _ptr(logits), _code(logits), _ptr(idx), INDEX_CODE[idx.dtype], T, E, k, SCORING[scoring],
@@ -215,7 +219,7 @@ def moe_selected_router_backward(logits, idx, grad_w, scoring: str = "softmax",
         raise MoeError(3, "grad_weights must be float32")
     T, E = logits.shape
     k = idx.shape[1]
-    grad = torch.empty_like(logits) if grad is None else grad
+    grad = _new(logits.shape, logits.dtype, logits.device, stream) if grad is None else grad
     _cuda(grad)
     _check(lib().moe_selected_router_backward(
         _ptr(logits), _code(logits), _ptr(idx), INDEX_CODE[idx.dtype], _ptr(grad_w), T, E, k,
@@ -235,15 +239,12 @@ def moe_dispatch(x, idx, E: int, x_d=None, offsets=None, token_of_row=None, row_
     T, H = x.shape
     k = idx.shape[1]
     R, dev = T * k, x.device
-    x_d = torch.empty(R, H, dtype=x.dtype, device=dev) if x_d is None else x_d
-    offsets = torch.empty(E + 1, dtype=torch.int32, device=dev) if offsets is None else offsets
-    token_of_row = (torch.empty(R, dtype=torch.uint32, device=dev) if token_of_row is None
-                    else token_of_row)
-    row_of_slot = (torch.empty(R, dtype=torch.uint32, device=dev) if row_of_slot is None
-                   else row_of_slot)
+    x_d = _new((R, H), x.dtype, dev, stream) if x_d is None else x_d
+    offsets = _new(E + 1, torch.int32, dev, stream) if offsets is None else offsets
+    token_of_row = _new(R, torch.uint32, dev, stream) if token_of_row is None else token_of_row
+    row_of_slot = _new(R, torch.uint32, dev, stream) if row_of_slot is None else row_of_slot
     if ws is None:
-        ws = torch.empty(max(dispatch_workspace_bytes(T, E, k), 256), dtype=torch.uint8,
-                         device=dev)
+        ws = _new_ws(dispatch_workspace_bytes(T, E, k), dev, stream)
     _cuda(x_d, offsets, token_of_row, row_of_slot, ws)
     _check(lib().moe_dispatch(_ptr(x), _code(x), T, H, _ptr(idx), E, k, _ptr(x_d), _ptr(offsets),
                               _ptr(token_of_row), _ptr(row_of_slot), _ptr(ws), ws.numel(),
@@ -261,10 +262,9 @@ def moe_experts_forward_dispatched(x_d, offsets, gate, up, down, y=None, ws=None
     _cuda(x_d, offsets, gate, up, down)
     rows, H = x_d.shape
     E, I, _ = gate.shape
-    y = torch.empty(rows, H, dtype=x_d.dtype, device=x_d.device) if y is None else y
+    y = _new((rows, H), x_d.dtype, x_d.device, stream) if y is None else y
     if ws is None:
-        ws = torch.empty(max(experts_workspace_bytes(rows, E, H, I, gate.dtype), 256),
-                         dtype=torch.uint8, device=x_d.device)
+        ws = _new_ws(experts_workspace_bytes(rows, E, H, I, gate.dtype), x_d.device, stream)
     _cuda(y, ws)
     _check(lib().moe_experts_forward_dispatched(
         _ptr(x_d), _ptr(offsets), rows, _ptr(gate), _ptr(up), _ptr(down), _code(gate), E, H, I,
@@ -277,7 +277,7 @@ def moe_combine(y, row_of_slot, w, out=None, stream=None):
     _cuda(y, row_of_slot, w)
     T, k = w.shape
     H = y.shape[1]
-    out = torch.empty(T, H, dtype=y.dtype, device=y.device) if out is None else out
+    out = _new((T, H), y.dtype, y.device, stream) if out is None else out
     _cuda(out)
     _check(lib().moe_combine(_ptr(y), _code(y), _ptr(row_of_slot), _ptr(w), _code(w), T, H, k,
                              _ptr(out), _stream(stream)), "moe_combine")
@@ -295,10 +295,10 @@ def moe_forward(x, logits, gate, up, down, top_k: int, renormalize: bool = True,
     _cuda(x, logits, gate, up, down)
     T, H = x.shape
     E, I, _ = gate.shape
-    out = torch.empty_like(x) if out is None else out
+    out = _new(x.shape, x.dtype, x.device, stream) if out is None else out
     if ws is None:
-        ws = torch.empty(max(forward_workspace_bytes(T, E, H, I, top_k, logits.dtype, x.dtype), 256),
-                         dtype=torch.uint8, device=x.device)
+        ws = _new_ws(forward_workspace_bytes(T, E, H, I, top_k, logits.dtype, x.dtype), x.device,
+                     stream)
     _cuda(out, ws)
     _check(lib().moe_forward(_ptr(x), _ptr(logits), _code(logits), _ptr(gate), _ptr(up),
                              _ptr(down), _code(gate), T, E, H, I, top_k, int(bool(renormalize)),
@@ -314,10 +314,10 @@ def moe_forward_sigmoid_grouped(x, logits, gate, up, down, top_k: int, groups: i
     _cuda(x, logits, gate, up, down, bias)
     T, H = x.shape
     E, I, _ = gate.shape
-    out = torch.empty_like(x) if out is None else out
+    out = _new(x.shape, x.dtype, x.device, stream) if out is None else out
     if ws is None:
-        ws = torch.empty(max(forward_workspace_bytes(T, E, H, I, top_k, logits.dtype, x.dtype), 256),
-                         dtype=torch.uint8, device=x.device)
+        ws = _new_ws(forward_workspace_bytes(T, E, H, I, top_k, logits.dtype, x.dtype), x.device,
+                     stream)
     _cuda(out, ws)
     _check(lib().moe_forward_sigmoid_grouped(
         _ptr(x), _ptr(logits), _code(logits), _ptr(bias), _ptr(gate), _ptr(up), _ptr(down),
@@ -340,10 +340,10 @@ def moe_forward_with_events(x, logits, gate, up, down, top_k: int, renormalize: 
     _cuda(x, logits, gate, up, down)
     T, H = x.shape
     E, I, _ = gate.shape
-    out = torch.empty_like(x) if out is None else out
+    out = _new(x.shape, x.dtype, x.device, stream) if out is None else out
     if ws is None:
-        ws = torch.empty(max(forward_workspace_bytes(T, E, H, I, top_k, logits.dtype, x.dtype), 256),
-                         dtype=torch.uint8, device=x.device)
+        ws = _new_ws(forward_workspace_bytes(T, E, H, I, top_k, logits.dtype, x.dtype), x.device,
+                     stream)
     _cuda(out, ws)
     arr = None
     if events is not None:
@@ -365,8 +365,8 @@ def moe_combine_backward(y, row_of_slot, w, dout, stream=None):
     _cuda(y, row_of_slot, w, dout)
     T, k = w.shape
     H = y.shape[1]
-    dexpert = torch.empty_like(y)
-    dweights = torch.empty(T, k, dtype=torch.float32, device=y.device)
+    dexpert = _new(y.shape, y.dtype, y.device, stream)
+    dweights = _new((T, k), torch.float32, y.device, stream)
     _check(lib().moe_combine_backward(_ptr(y), _code(y), _ptr(row_of_slot), _ptr(w), _code(w),
                                       _ptr(dout), T, H, k, _ptr(dexpert), _ptr(dweights),
                                       _stream(stream)), "moe_combine_backward")
@@ -379,13 +379,12 @@ def moe_experts_backward(x_d, offsets, gate, up, down, dy, ws=None, stream=None)
     rows, H = x_d.shape
     E, I, _ = gate.shape
     dev = x_d.device
-    dinput = torch.empty_like(x_d)
-    dgate = torch.empty(E, I, H, dtype=torch.float32, device=dev)
-    dup = torch.empty(E, I, H, dtype=torch.float32, device=dev)
-    ddown = torch.empty(E, H, I, dtype=torch.float32, device=dev)
+    dinput = _new(x_d.shape, x_d.dtype, x_d.device, stream)
+    dgate = _new((E, I, H), torch.float32, dev, stream)
+    dup = _new((E, I, H), torch.float32, dev, stream)
+    ddown = _new((E, H, I), torch.float32, dev, stream)
     if ws is None:
-        ws = torch.empty(max(lib().moe_experts_backward_workspace_bytes(rows, I), 256),
-                         dtype=torch.uint8, device=dev)
+        ws = _new_ws(lib().moe_experts_backward_workspace_bytes(rows, I), dev, stream)
     _check(lib().moe_experts_backward(
         _ptr(x_d), _ptr(offsets), rows, _ptr(gate), _ptr(up), _ptr(down), _code(gate), E, H, I,
         _ptr(dy), _ptr(dinput), _ptr(dgate), _ptr(dup), _ptr(ddown), _ptr(ws), ws.numel(),
@@ -397,7 +396,7 @@ def moe_dispatch_backward(dinput, row_of_slot, T: int, top_k: int, stream=None):
     """DispatchedTokens::dispatch_backward -> dx [T, H] (slot rows summed, no weights)."""
     _cuda(dinput, row_of_slot)
     H = dinput.shape[1]
-    dx = torch.empty(T, H, dtype=dinput.dtype, device=dinput.device)
+    dx = _new((T, H), dinput.dtype, dinput.device, stream)
     _check(lib().moe_dispatch_backward(_ptr(dinput), _code(dinput), _ptr(row_of_slot), T, H, top_k,
                                        _ptr(dx), _stream(stream)), "moe_dispatch_backward")
     return dx
