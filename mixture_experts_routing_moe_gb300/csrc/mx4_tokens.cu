@@ -726,21 +726,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The fence before a count reaches other SMs takes a thousand cycles or more, which the
     // epilogue does not have to spare (wide experts: 160 us with it there).
     int seen = 0;
-    bool stop = false;
-    for (int u = blockIdx.x; u < n1 && !stop; u += gridDim.x) {
+    for (int u = blockIdx.x; u < n1; u += gridDim.x) {
       const long long t0 = clock64();
+      bool ok = true;
       while (*written <= seen) {
         if (*abort_f || clock64() - t0 > kWaitLimit) {
-          stop = true;  // (the epilogue's own wait has recorded a timeout, or will)
+          ok = false;  // (the epilogue's own wait has recorded a timeout, or will)
           break;
         }
         __nanosleep(20);
       }
+      // Lanes may see the abort and the last unit's word in different order: they leave together, as
+      // the election below waits for all of them.
+      if (!__all_sync(0xFFFFFFFFu, ok)) break;
       ++seen;
       __syncwarp();
       __threadfence();          // the epilogue's writes, which its barrier ordered before the word
       fence_proxy_async_all();  // aq is read by TMA
-      if (!stop && elect_one()) atomicAdd(p.ready + unit_of(u).ai, 1u);
+      if (elect_one()) atomicAdd(p.ready + unit_of(u).ai, 1u);
     }
   } else if (warp >= 8) {
     // ---------------------------------------------------------------- epilogue

@@ -1,5 +1,8 @@
 """What the binding does on the host around a microscaled 4-bit call, without a GPU."""
 import contextlib
+import glob
+import os
+import re
 import threading
 
 import pytest
@@ -76,3 +79,11 @@ def test_workspace_of_a_given_stream_is_that_streams(monkeypatch):
     for need in (256, 1 << 28):
         B._mx4_ws(None, need, "cuda", "side", 7)
     assert made_on == ["side", "side"] and current == ["current"]
+
+
+def test_elections_are_made_by_whole_warps():
+    """elect.sync waits for every lane that its mask names, so no lane may be kept from it by a
+    condition in front: a warp of which some lanes had given up would wait for good."""
+    for path in glob.glob(os.path.join(os.path.dirname(B.__file__), "csrc", "*.cu*")):
+        with open(path) as f:
+            assert not re.findall(r"(?:&&|\|\||\?)\s*elect_one\(\)", f.read()), path
