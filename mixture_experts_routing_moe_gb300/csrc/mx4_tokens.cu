@@ -453,6 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     if (lane == 0) ok = wait_count(p.ready + ai, NI, abort_f, p.status);
     ok = __all_sync(0xFFFFFFFFu, ok);
+    __syncwarp();  // orders lane 0's acquire before the other lanes' loads (a vote orders nothing)
     fence_proxy_async_all();
     return ok;
   };
