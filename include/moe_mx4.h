@@ -90,8 +90,10 @@ int moe_mx4_experts_forward_dispatched(const void* x_d, int xdt, const int32_t* 
  *   a = silu(x gate[e]^T) (x up[e]^T) in FP32, rounded once to dt,
  *   out[t] = sum_j w[t, j] (a_j down[e_j]^T), FP32 in the order j = 0 .. top_k-1, rounded once.
  * x [T, H], router [E, H] and out [T, H] of dtype dt (f16 / bf16), weights as for the experts
- * above.  The activations are not quantised: they enter the products to within 2^-14 of the
- * largest value of their block of 32.  A token holding an infinity or a NaN gets NaN.
+ * above.  The activations are not quantised: they enter the products to within 2^-23 of the
+ * largest value of their block of 32 (2^-128 where that is smaller), which is what one rounding of an
+ * FP32 sum that holds it costs; bf16 values down to 2^-15 of the largest are exact, f16 values down
+ * to 2^-12.  A token holding an infinity or a NaN gets NaN.
  * idx [T, top_k] uint32 and w [T, top_k] float receive the selection; either may be NULL.
  * Two launches, the second a cooperative one; if its CTAs cannot all be resident (another context
  * holds SMs) the call returns MOE_ERR_CUDA.

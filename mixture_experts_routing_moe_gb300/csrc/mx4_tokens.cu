@@ -7,13 +7,15 @@
 // The layer reads each active expert's weights once, 17/32 of a byte a weight, and that is its
 // floor, so nothing may be spent on the weights but the copy.  The tensor cores decode them:
 // tcgen05.mma kind::mxf4 multiplies the packed codes (M = 128 weight rows) by e2m1 tokens and
-// applies the block scales of both.  The tokens stay what they are: each block of 32 values is the
-// sum of five e2m1 terms, each with a scale 2^-3 of the one before (a value scaled to at most 4 is
-// within 1/2 of a code, so a term takes three bits off).  What five leave is at most 2^-14 of the
-// block's largest value, far under the 16-bit rounding of that value itself, and nothing where
-// the value's bits end above that.  The terms are separate columns (N) of the MMA, and the
-// epilogue adds them up.  N is small, so they cost no time: a 256-deep slice of 128 weight rows
-// keeps the tensor pipe about 300 cycles and the memory about 700.
+// applies the block scales of both.  Each block of 32 token values is the sum of eight e2m1 terms,
+// each with a scale 2^-3 of the one before (a value scaled to at most 4 is within 1/2 of a code, so a
+// term takes three bits off).  What eight leave is at most 2^-23 of the block's largest value, as
+// much as one rounding of an FP32 sum that holds that value, and nothing where the value's bits end
+// above that: bf16 values down to 2^-15 of the largest are exact, f16 values down to 2^-12.  (Five
+// terms, 2^-14, lost the 16 bits of values beside one a few hundred times as large, which activations
+// do have.)  The terms are separate columns (N) of the MMA, and the epilogue adds them up.  N is
+// small, so they cost no time: a 256-deep slice of 128 weight rows keeps the tensor pipe about 300
+// cycles and the memory about 700.
 // (Two e4m3 terms under kind::mxf8f6f4 are exact for bf16, but the weights then widen to a byte in
 // shared memory: the TMA unit handles rows of 64 packed bytes, and half as many bytes are in
 // flight.  The layer of 256 experts took 1.08 ms that way.)
@@ -48,8 +50,8 @@ using namespace tc;
 using namespace mx4;
 
 constexpr int kThreads = 416, kWarps = kThreads / 32;
-constexpr int P = 5;               // terms of a token value
-constexpr int kG = 38;             // tokens of a unit
+constexpr int P = 8;               // terms of a token value
+constexpr int kG = 24;             // tokens of a unit
 constexpr int kMaxN = 192;         // columns of a unit
 static_assert(kG * P <= kMaxN, "columns of a group");
 constexpr int kA = 128 * 128;      // bytes of a slice's weights (128 rows, 256 deep)
@@ -317,8 +319,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   int* start = reinterpret_cast<int*>(at);  // first entry of an expert's tokens in `list`
   at += (p.E + 1) * 4;
   int* act = reinterpret_cast<int*>(at);  // expert | group << 16 of each group of tokens
-  at += 2 * p.E * 4;
   const int R = p.T * p.k;
+  at += R * 4;  // a group has one slot at least
   float* sel_w = reinterpret_cast<float*>(at);
   at += R * 4;
   uint16_t* sel_id = reinterpret_cast<uint16_t*>(at);
@@ -395,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int carry = 0, n_act = 0;
     for (int e0 = 0; e0 < p.E; e0 += 32) {
       const int e = e0 + lane;
-      const int n = e < p.E ? __popcll(mask[e]) : 0, g = (n + kG - 1) / kG;  // g <= 2
+      const int n = e < p.E ? __popcll(mask[e]) : 0, g = (n + kG - 1) / kG;
       int s = n, sg = g;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -873,8 +875,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Bytes of shared memory beside the ring.
 size_t fixed_smem(int E, int R, int ncap_raw) {
-  return 1024 + kBarBytes + kRaw * (128 + (size_t)ncap_raw) * 32 + kExchange + (size_t)E * 20 + 4 +
-         (size_t)R * 8;
+  return 1024 + kBarBytes + kRaw * (128 + (size_t)ncap_raw) * 32 + kExchange + (size_t)E * 12 + 4 +
+         (size_t)R * 12;
 }
 
 // Parts of K that a down unit is cut into: enough units for four to a CTA (a CTA's last unit is
