@@ -67,3 +67,53 @@ def test_values_beside_a_large_one_keep_their_16_bits(dtype, T, ratio):
         # the bound above is that of 16 bits: no looser than two roundings and a little
         few = ~np.isin(down_at, wide)
         assert (tol[few] <= (2 * eps + 4e-3 * (ratio > 64)) * np.abs(ref[few])).all()
+
+
+@pytest.mark.parametrize("rows", [16, 200])
+def test_swiglu_of_the_experts_far_below_zero(rows):
+    """silu(g) down to g = -88, where 1 + exp(-g) is the largest that FP32 holds, times a large u."""
+    H, I = 64, 64
+    x = np.zeros((rows, H))
+    x[:, 0], x[:, 1] = -4.0 * (1 + np.arange(rows) % 16), -24.0   # one block: scale 16 or less
+    x[:, 32] = 2.0 ** 100                                          # the other
+    g_cols = {0: 1.0, 1: 1.0}
+    gate, up, down = np.zeros((I, H)), np.zeros((I, H)), np.zeros((H, I))
+    for c, v in g_cols.items():
+        gate[:, c] = v
+    up[:, 32], down[:, 5] = 1.0, 1.0
+    w = [tuple(torch.from_numpy(t)[None].to(DEV) for t in M.quantize(m)) for m in (gate, up, down)]
+    off = torch.tensor([0, rows], dtype=torch.int32, device=DEV)
+    y = moe.moe_mx4_experts_forward_dispatched(torch.from_numpy(x).float().to(DEV), off, *w)
+    xq = M.fake(x)
+    g, u = xq[:, 0] + xq[:, 1], xq[:, 32]
+    assert g.min() == -88 and g.max() > -32
+    a = M.silu_mul(g, u)
+    # no a is near a border between codes, so the products are exact
+    assert (M.quantize_slack(np.repeat(a[:, None], 64, 1), 1e-4) == 0).all()
+    ref = M.fake(np.repeat(a[:, None], 64, 1))[:, 5]
+    assert (y.double().cpu().numpy() == ref[:, None]).all()
+
+
+def test_swiglu_of_the_experts_to_a_few_units():
+    """Four million values of a from exact g and u, g from about -100 to 100: each takes its code, or
+    where it is within eight units of FP32 of a border, either code."""
+    rng = np.random.default_rng(17)
+    n = 2048
+    x = rng.standard_normal((n, n)) * np.exp2(rng.uniform(-3, 5, (n, 1)))
+    x = torch.from_numpy(np.clip(x, -80, 80)).float()
+    weights, sums = [], []
+    xq = M.fake(x.double().numpy())
+    for _ in range(2):      # three values of x with 2^0, 2^-3 and 2^-6, which FP32 adds up exactly
+        w, total = np.zeros((n, n)), 0.0
+        for part, shift in zip(np.split(np.arange(1536), 3), (0, 3, 6)):
+            at = rng.choice(part, n)
+            w[np.arange(n), at] = 2.0 ** -shift
+            total = total + xq[:, at] * 2.0 ** -shift
+        weights.append(tuple(torch.from_numpy(t)[None].to(DEV) for t in M.quantize(w)))
+        sums.append(total)
+    off = torch.tensor([0, n], dtype=torch.int32, device=DEV)
+    y = moe.moe_mx4_experts_forward_dispatched(x.to(DEV), off, *weights, picks(n, np.arange(n)))
+    a = M.silu_mul(*sums)
+    err = np.abs(y.double().cpu().numpy() - M.fake(a))
+    wrong = err > M.quantize_slack(a, 8 * U)
+    assert not wrong.any(), (wrong.sum(), sums[0][wrong][:4])
