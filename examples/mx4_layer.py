@@ -2,11 +2,12 @@
 
     python examples/mx4_layer.py [--tokens 2048] [--hidden 2048] [--inter 768] [--experts 64]
 
-The weights are quantised once (moe_mx4_quantize).  The prompt's tokens get their router logits from
-a product in blocks (moe_mx4_product) and go through moe_route, moe_dispatch, the experts in blocks
-and moe_combine; the tokens that follow, a few at a time, take moe_mx4_forward_tokens, which routes
-them itself.  Both are compared with the 16-bit layer on the weights that the blocks stand for
-(moe_mx4_dequantize).
+The weights are quantised once (moe_mx4_quantize), all but the router's: which experts a token takes
+is decided by logits of its 16 bits and the router's, in a prompt as in single tokens.  The prompt's
+tokens go through moe_route, moe_dispatch, the experts in blocks and moe_combine; the tokens that
+follow, a few at a time, take moe_mx4_forward_tokens, which routes them itself.  Both are compared with
+the 16-bit layer on the weights that the blocks stand for (moe_mx4_dequantize), routed in FP32.  A
+dense projection in blocks (moe_mx4_product) takes the prompt's result on to a vocabulary.
 """
 import argparse
 import os
@@ -22,23 +23,26 @@ import mixture_experts_routing_moe_gb300 as moe  # noqa: E402
 
 
 class Mx4Layer:
-    """Router weights in 16 bits and in blocks, expert weights in blocks."""
+    """Router weights in 16 bits, expert weights and a head [V, H] in blocks."""
 
-    def __init__(self, router, gate, up, down, top_k):
+    def __init__(self, router, gate, up, down, head, top_k):
         self.router, self.top_k = router, top_k
-        self.router_mx4 = moe.moe_mx4_quantize(router)
         self.gate, self.up, self.down = (moe.moe_mx4_quantize(w) for w in (gate, up, down))
+        self.head_mx4 = moe.moe_mx4_quantize(head)
         self.ws = None
 
     def prompt(self, x):
-        """x [T, H], any T: weights and activations in blocks."""
+        """x [T, H], any T: expert weights and activations in blocks, routing in FP32."""
         E = self.router.shape[0]
-        logits = moe.moe_mx4_product(*moe.moe_mx4_quantize(x), *self.router_mx4, dtype=x.dtype)
-        idx, w = moe.moe_route(logits, self.top_k)
+        idx, w = moe.moe_route(x.float() @ self.router.float().T, self.top_k)
         d = moe.moe_dispatch(x, idx, E)
         y = moe.moe_mx4_experts_forward_dispatched(d["x_d"], d["offsets"], self.gate, self.up,
                                                    self.down)
-        return moe.moe_combine(y, d["row_of_slot"], w), logits
+        return moe.moe_combine(y, d["row_of_slot"], w)
+
+    def head(self, out):
+        """out [T, H] -> [T, V] in FP32, weights and activations in blocks."""
+        return moe.moe_mx4_product(*moe.moe_mx4_quantize(out), *self.head_mx4, dtype=torch.float32)
 
     def step(self, x):
         """x [T, H] with T <= 64: activations stay in 16 bits, one workspace serves every step."""
@@ -51,7 +55,8 @@ class Mx4Layer:
 
 
 def run(tokens=2048, hidden=2048, inter=768, experts=64, top_k=4, steps=8, seed=0):
-    """Relative errors (prompt, single tokens) against the 16-bit layer on the same weights."""
+    """Relative errors against the 16-bit layer on the same weights, each routing its own tokens: of a
+    prompt (or of the head on it, if that is larger), and of single tokens."""
     g = torch.Generator(device="cuda")
     g.manual_seed(seed)
 
@@ -61,22 +66,25 @@ def run(tokens=2048, hidden=2048, inter=768, experts=64, top_k=4, steps=8, seed=
     router = normal(experts, hidden, std=hidden ** -0.5)
     layer = Mx4Layer(router, normal(experts, inter, hidden, std=hidden ** -0.5),
                      normal(experts, inter, hidden, std=hidden ** -0.5),
-                     normal(experts, hidden, inter, std=inter ** -0.5), top_k)
+                     normal(experts, hidden, inter, std=inter ** -0.5),
+                     normal(4 * hidden, hidden, std=hidden ** -0.5), top_k)
     gate, up = (moe.moe_mx4_dequantize(*m, hidden) for m in (layer.gate, layer.up))
     down = moe.moe_mx4_dequantize(*layer.down, inter)
 
     def error(a, b):
         return float((a.float() - b.float()).norm() / b.float().norm())
 
+    def reference(x):
+        return moe.moe_forward(x, x.float() @ router.float().T, gate, up, down, top_k)
+
     x = normal(tokens, hidden)
-    out, logits = layer.prompt(x)
-    prompt = error(out, moe.moe_forward(x, logits, gate, up, down, top_k))
+    out = layer.prompt(x)
+    head = moe.moe_mx4_dequantize(*layer.head_mx4, hidden, torch.float32)
+    prompt = max(error(out, reference(x)), error(layer.head(out), out.float() @ head.T))
     single = 0.0
     for n in range(1, steps + 1):
         x = normal(n, hidden)
-        # the same selection for both: logits in FP32, as the layer computes them
-        ref = moe.moe_forward(x, x.float() @ router.float().T, gate, up, down, top_k)
-        single = max(single, error(layer.step(x), ref))
+        single = max(single, error(layer.step(x), reference(x)))
     return prompt, single
 
 

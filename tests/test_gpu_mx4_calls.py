@@ -95,3 +95,23 @@ def test_a_given_streams_memory_is_its_own():
         torch.cuda.synchronize()
         got = block_users(make, given)
         assert torch.equal(got, want)
+
+
+def test_the_examples_prompt_and_steps_choose_the_same_experts():
+    """Tokens of a prompt and the same tokens a few at a time: routed alike, so apart by no more than the
+    four bits of the prompt's activations."""
+    from examples import mx4_layer
+    E, H, I, k, T = 16, 256, 384, 2, 64
+    g = torch.Generator(device=DEV)
+    g.manual_seed(9)
+
+    def normal(*s):
+        return (torch.randn(*s, generator=g, device=DEV) * s[-1] ** -0.5).bfloat16()
+
+    layer = mx4_layer.Mx4Layer(normal(E, H), normal(E, I, H), normal(E, I, H), normal(E, H, I),
+                               normal(64, H), k)
+    x = normal(T, H) * 16
+    a, b = layer.prompt(x).float(), layer.step(x).float()
+    # a token of other experts would be off by as much as it is large
+    off = (a - b).norm(dim=1) / b.norm(dim=1)
+    assert off.max() < 0.5
