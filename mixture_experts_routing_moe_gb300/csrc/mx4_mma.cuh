@@ -112,15 +112,11 @@ static __device__ __forceinline__ void st_shared_u32(uint32_t addr, uint32_t v) 
 static __device__ __forceinline__ uint32_t raw_offset(int row, int half) {
   return (uint32_t)(row * 32 + ((half ^ (row >> 2 & 1)) * 16));
 }
-// Sixteen (past L1) or four bytes; zeros where `in` is false (nothing is read then).
+// Sixteen bytes past L1; zeros where `in` is false (nothing is read then).  (Four bytes can only be
+// copied through L1, which may hold a line from before it was written elsewhere.)
 static __device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool in) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
                "r"(in ? 16 : 0)
-               : "memory");
-}
-static __device__ __forceinline__ void cp_async4_or_zero(uint32_t dst, const void* src, bool in) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
-               "r"(in ? 4 : 0)
                : "memory");
 }
 // One arrival on `bar` once this thread's copies so far have landed.
