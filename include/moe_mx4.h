@@ -17,7 +17,9 @@
  * codes  [rows, 16 ceil(K / 32)] uint8, 16-byte aligned; a last short block is filled with
  *        zero codes.
  * scales [rows, 4 ceil(K / 128)] uint8, 4-byte aligned; the bytes past the last block are 0.
- * Limits: K, N, H, I >= 1 and below 2^24; rows below 2^31; 1 <= E <= 1024.
+ * Limits (MOE_ERR_SHAPE past them): K, N, H, I >= 1 and below 2^24; 1 <= E <= 1024; row strides
+ * below 2^31 elements; rows, and the weight rows E N, E H, E I, below 2^31 - 1024; for the products,
+ * (ceil(rows / 128) + E) ceil(N / 128) below 2^31 - 1024 (N: H and I for the experts).
  */
 #ifndef MOE_MX4_H_
 #define MOE_MX4_H_

@@ -9,6 +9,7 @@ import pytest
 import torch
 
 from mixture_experts_routing_moe_gb300 import binding as B
+from mixture_experts_routing_moe_gb300 import build as build_mod
 
 
 @pytest.fixture
@@ -87,3 +88,26 @@ def test_elections_are_made_by_whole_warps():
     for path in glob.glob(os.path.join(os.path.dirname(B.__file__), "csrc", "*.cu*")):
         with open(path) as f:
             assert not re.findall(r"(?:&&|\|\||\?)\s*elect_one\(\)", f.read()), path
+
+
+def test_largest_sizes_are_the_documented_ones():
+    """One below each limit of moe_mx4.h the call is refused for its missing workspace, at it for its
+    shape."""
+    build_mod.build()
+    fake, top = 0x10000, (1 << 31) - 1024
+
+    def product(rows=1, E=1, N=64, K=64):
+        return B.lib().moe_mx4_product(fake, fake, rows, fake, fake, fake, E, N, K, fake, B.MOE_F32,
+                                       None, 0, None)
+    workspace, shape = 5, 2
+    assert product(rows=top - 1) == workspace and product(rows=top) == shape
+    assert product(K=(1 << 24) - 1) == workspace and product(K=1 << 24) == shape
+    assert product(E=1023, N=top // 1023) == workspace and product(E=1023, N=top // 1023 + 1) == shape
+    tiles = lambda rows, N: (-(-rows // 128) + 1) * -(-N // 128)  # noqa: E731
+    N = (1 << 24) - 1
+    rows = ((top - 1) // -(-N // 128) - 1) * 128
+    assert tiles(rows, N) < top and product(rows=rows, N=N) == workspace
+    assert tiles(rows + 1, N) >= top and product(rows=rows + 1, N=N) == shape
+    wide = (1 << 31) - 1
+    assert B.lib().moe_mx4_quantize(fake, B.MOE_F32, 1, 64, wide, fake + 8, fake, None) == 4
+    assert B.lib().moe_mx4_quantize(fake, B.MOE_F32, 1, 64, wide + 1, fake, fake, None) == shape
