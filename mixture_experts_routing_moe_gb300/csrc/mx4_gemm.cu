@@ -7,11 +7,12 @@
 // A persistent kernel walks tiles (expert, m-tile, n-tile) of 256 columns and 128 rows (a CTA) or
 // 256 rows (a cluster of two CTAs, cta_group::2: each CTA holds 128 of the rows and half of the B
 // rows, so a tile pulls a third fewer bytes through L2).  Roles in each CTA:
-//   warp 0      one lane loads, for each 256-deep K slice, the codes of its A and B rows (128
-//               bytes a row) by TMA into a ring.  For gate/up the B tile holds gate rows 0-63, up
-//               rows 0-63, gate rows 64-127, up rows 64-127 of 128 columns of a.
-//   warp 1      one lane (of CTA 0) copies each slice's scales to tensor memory and issues its
-//               four K = 64 MMAs (N = 256); tcgen05.commit frees the slot.
+//   warp 0      loads, for each 256-deep K slice, the codes of its A and B rows (128 bytes a row) by
+//               TMA into a ring.  For gate/up the B tile holds gate rows 0-63, up rows 0-63, gate
+//               rows 64-127, up rows 64-127 of 128 columns of a.  (Warps 0 and 1 run their loops with
+//               all lanes; an elected one issues.)
+//   warp 1      (of CTA 0) copies each slice's scales to tensor memory and issues its four K = 64
+//               MMAs (N = 256); tcgen05.commit frees the slot.
 //   warps 4-6   scales of A and of the two halves of B: each lane holds 32 bytes (four slices) of
 //               four rows in registers, loads the next 32 ahead, and writes each slice's words to
 //               the chunk layout, 16 bytes at a time.  Groups start at any row, so no bulk copy of
