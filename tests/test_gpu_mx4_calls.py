@@ -53,6 +53,46 @@ def test_two_threads_on_one_stream():
     assert not wrong
 
 
+def together(*jobs):
+    """Each job in a thread of its own, all started at once; what they raised."""
+    start, raised = threading.Barrier(len(jobs)), []
+
+    def work(job):
+        start.wait()
+        try:
+            job()
+        except Exception as e:  # noqa: BLE001
+            raised.append(e)
+
+    threads = [threading.Thread(target=work, args=(job,)) for job in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    return raised
+
+
+def test_first_call_of_a_thread():
+    """A thread that has not used CUDA yet, and is given all the memory: the call makes the context
+    current by itself."""
+    E, H, I = 4, 256, 256
+    w = weights(E, H, I, 3)
+    x = torch.randn(5, H, device=DEV).bfloat16()
+    router = torch.randn(E, H, device=DEV).bfloat16()
+    codes, scales = moe.moe_mx4_quantize(x)
+    ws = torch.empty(moe.mx4_tokens_workspace_bytes(5, E, H, I, 2, x.dtype), dtype=torch.uint8,
+                     device=DEV)
+    for call, out in (
+            (lambda o: moe.moe_mx4_product(codes, scales, codes, scales, out=o, ws=ws),
+             torch.empty(5, 5, dtype=torch.bfloat16, device=DEV)),
+            (lambda o: moe.moe_mx4_forward_tokens(x, router, *w, top_k=2, out=o, ws=ws),
+             torch.empty_like(x))):
+        want = call(torch.empty_like(out))
+        assert not together(lambda: call(out))
+        assert torch.equal(out, want)
+
+
 def block_users(make, given):
     """Calls make() with the side stream while the current one still has work queued on memory that it
     has already given back, as much as each buffer of the call; the result, once all of it is done."""
