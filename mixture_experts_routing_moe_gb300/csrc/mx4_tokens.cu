@@ -944,7 +944,8 @@ cudaError_t launch_t(const Mx4TokensArgs& a, cudaStream_t s) {
       !make_map_bytes(&ma, p.aq, a.I / 2, (int64_t)R * P, kBox))
     return cudaErrorInvalidValue;
   auto kern = moe_mx4_tokens<T>;
-  err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // the same limit in every call: another thread's, of another size, may come before the launch
+  err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
   if (err != cudaSuccess) return err;
   const int logit_ctas = (a.E + kEB - 1) / kEB * ((a.T + kTB - 1) / kTB);
   const int64_t blocks = (int64_t)a.T * (a.H / 32);

@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import mixture_experts_routing_moe_gb300 as moe
+from mixture_experts_routing_moe_gb300 import binding as B
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -71,6 +72,31 @@ def together(*jobs):
         t.join()
     torch.cuda.synchronize()
     return raised
+
+
+def test_threads_with_layers_of_other_sizes():
+    """The kernel's limit of shared memory is the process's: a call of one size does not take it from a
+    larger call of another thread, between that one's look and its launch."""
+    E, H, I = 8, 256, 256
+    w = weights(E, H, I, 3)
+    router = torch.randn(E, H, device=DEV).bfloat16()
+
+    def many(T, k):
+        x = torch.randn(T, H, device=DEV).bfloat16()
+        out = torch.empty_like(x)
+        ws = torch.empty(moe.mx4_tokens_workspace_bytes(T, E, H, I, k, x.dtype), dtype=torch.uint8,
+                         device=DEV)
+        args = [x.data_ptr(), router.data_ptr(), B.MOE_BF16, *(t.data_ptr() for p in w for t in p), T,
+                E, H, I, k, 1, out.data_ptr(), None, None, ws.data_ptr(), ws.numel(), None]
+        call = B.lib().moe_mx4_forward_tokens
+
+        def job(kept=(x, out, ws)):
+            for _ in range(4000):
+                status = call(*args)
+                assert status == 0, B.STATUS[status]
+        return job
+
+    assert not together(many(1, 1), many(9, 2), many(40, 4))
 
 
 def test_first_call_of_a_thread():
