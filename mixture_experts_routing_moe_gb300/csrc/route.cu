@@ -440,15 +440,17 @@ cudaError_t launch_route_lc(const void* logits, int64_t T_, int E, int k, int re
                             uint32_t* idx, void* w, cudaStream_t s) {
   constexpr int RPB = kRouteWarps * (32 / L);
   const size_t smem = (size_t)RPB * k * 8;
+  constexpr size_t kMostSmem = (size_t)RPB * L * C * 8;  // k <= E <= L * C
   const int64_t blocks = (T_ + RPB - 1) / RPB;
   const bool vec = (((uintptr_t)logits) % 16 == 0) && ((E * sizeof(T)) % 16 == 0);
   if (smem > 48 * 1024) {
+    // the same limit in every call: another thread's, of another size, may come before the launch
     cudaError_t err;
     err = cudaFuncSetAttribute(moe_route_kernel<T, L, C, true>,
-                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMostSmem);
     if (err != cudaSuccess) return err;
     err = cudaFuncSetAttribute(moe_route_kernel<T, L, C, false>,
-                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMostSmem);
     if (err != cudaSuccess) return err;
   }
   if (vec)

@@ -692,8 +692,11 @@ cudaError_t launch_sig_c(const void* logits, const float* bias, int64_t T_, int 
                          int SG, int top_two, int renorm, float scale, uint32_t* idx, void* w,
                          cudaStream_t s) {
   const size_t smem = (size_t)kSigWarps * (E + 128 + 64 + 32) * sizeof(double);
-  cudaError_t err = cudaFuncSetAttribute(moe_route_sigmoid_kernel<T, C>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // the same limit in every call: another thread's, of another size, may come before the launch
+  constexpr size_t kMostSmem = (size_t)kSigWarps * (32 * C + 128 + 64 + 32) * sizeof(double);
+  cudaError_t err =
+      cudaFuncSetAttribute(moe_route_sigmoid_kernel<T, C>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMostSmem);
   if (err != cudaSuccess) return err;
   const unsigned blocks = (unsigned)((T_ + kSigWarps - 1) / kSigWarps);
   moe_route_sigmoid_kernel<T, C><<<blocks, kSigWarps * 32, smem, s>>>(
