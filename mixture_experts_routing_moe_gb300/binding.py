@@ -2,8 +2,9 @@
 
 Every function here takes torch CUDA tensors, checks that they are contiguous CUDA tensors,
 allocates missing outputs / workspace with torch (device memory is the one thing torch is used
-for), and passes raw pointers, sizes and the current stream to the C ABI.  All computation runs
-in libmoe's kernels; there is no CPU path.  A missing or unbuilt library raises at first use.
+for) on the stream that the call is given (the current one by default), and passes raw pointers,
+sizes and that stream to the C ABI.  All computation runs in libmoe's kernels; there is no CPU path.
+A missing or unbuilt library raises at first use.
 """
 from __future__ import annotations
 
@@ -461,13 +462,13 @@ def _mx4_dtype(t) -> int:
     return _code(t) if code is None else code
 
 
-# Workspaces of calls that were given none, kept from call to call up to a size.  A call makes several
-# launches and the GIL is released while it makes them, so two threads' launches may interleave on the
-# stream that they share (all threads start on the default one): each thread has buffers of its own,
-# one a stream, and the calls of one thread on one stream follow one another.  A buffer that is
-# outgrown, or belongs to a thread that ended, goes back to torch, which hands it out again behind the
-# work of the stream it was made on (as with any tensor, a stream from outside torch has to stay
-# alive until then).
+# Workspaces of calls that were given none, kept from call to call up to a size.  A call makes
+# several launches and the GIL is released while it makes them, so two threads' launches may
+# interleave on the stream that they share (all threads start on the default one): each thread has
+# buffers of its own, one a stream, and the calls of one thread on one stream follow one another.
+# A buffer that is outgrown, or belongs to a thread that ended, goes back to torch, which hands it
+# out again behind the work of the stream it was made on (as with any tensor, a stream from outside
+# torch has to stay alive until then).
 class _Mx4Kept(threading.local):
     """(device, stream handle) -> the calling thread's workspace there."""
 

@@ -22,15 +22,16 @@
 //               (256 accumulator columns and the scales leave no room for a second accumulator.)
 // Waits are bounded; on expiry the status word records the timeout and every role leaves.
 //
-// What bounds it: at 8192^3 it runs in 161-163 us, 6.8 PFLOP/s; without the scales (skipped, to time
-// the rest) it takes 154, so the tensor pipe and its operands' way through shared memory are what
-// is left.  Deep K keeps that (K = 14336: 6.6); at K = 2048 a tile is 8 slices, and the 1400 cycles
-// in which the accumulator is emptied while no MMA can run are a fifth of it (3.4 with groups that
-// fill 78 % of their tiles).  On the way there, at 8192^3: scales four bytes at a time per slice,
-// 671 us (the L1 tag stage); pairs with a full release at cluster scope for each slice, 467 (it
-// waits for the warp's loads in flight), releasing shared memory only, 250; 16-byte chunk stores,
-// 238; whole-warp issue loops with an elected lane, 195; two slices behind one proxy fence, 184;
-// scale rows located once a tile and loaded 32 bytes at a time, 163.
+// What bounds it: at 8192^3 it runs in 159-161 us, 6.9 PFLOP/s, the tensor pipe 80 % active (in K =
+// 64 steps); without the scales (skipped, to time the rest) it takes 154, so the tensor pipe and
+// its operands' way through shared memory are what is left.  Deep K keeps that (K = 14336: 6.6); at
+// K = 2048 a tile is 8 slices, and the 1400 cycles in which the accumulator is emptied while no MMA
+// can run are a fifth of it (3.4 with groups that fill 78 % of their tiles).  On the way there, at
+// 8192^3: scales four bytes at a time per slice, 671 us (the L1 tag stage); pairs with a full
+// release at cluster scope for each slice, 467 (it waits for the warp's loads in flight), releasing
+// shared memory only, 250; 16-byte chunk stores, 238; whole-warp issue loops with an elected lane,
+// 195; two slices behind one proxy fence, 184; scale rows located once a tile and loaded 32 bytes
+// at a time, 163.
 #include "launch.h"
 #include "mx4.cuh"
 #include "mx4_mma.cuh"
@@ -140,7 +141,8 @@ __device__ __forceinline__ void store_row(T* row, const float* v, int col0, int 
 // A warp's 32 rows x 128 columns of an output whose rows are not 16-byte aligned (out: row 0, the
 // warp's first column; rows, cols: how many of them exist): 32 bytes of each row at a time go through
 // shared memory, so that a store's lanes write neighbouring elements of two (f32: four) rows.  With
-// each lane writing its own row, element by element, 5467 x 6895 f16 with K = 512 took 342 us.
+// each lane writing its own row, element by element, 5467 x 6895 f16 with K = 512 took 342 us; this
+// way, 74.  (The pair kernel spills nine registers for it.)
 template <typename T>
 __device__ __forceinline__ void store_turned(T* out, int64_t pitch, const uint32_t (&acc)[4][32],
                                              int rows, int cols, uint8_t* turn, int lane) {
