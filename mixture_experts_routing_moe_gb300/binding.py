@@ -20,6 +20,8 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmoe.so")
 HEADER = os.path.join(os.path.dirname(_HERE), "include", "moe.h")
 MX4_HEADER = os.path.join(os.path.dirname(_HERE), "include", "moe_mx4.h")
+MX8_HEADER = os.path.join(os.path.dirname(_HERE), "include", "moe_mx8.h")
+FRONT_HEADER = os.path.join(os.path.dirname(_HERE), "include", "moe_front.h")
 
 MOE_F32, MOE_F16, MOE_BF16 = 0, 1, 2
 DTYPE_CODE = {torch.float32: MOE_F32, torch.float16: MOE_F16, torch.bfloat16: MOE_BF16}
@@ -78,6 +80,31 @@ _SIGS = {
     "moe_mx4_tokens_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64, _int, _int]),
     "moe_mx4_forward_tokens": (_int, [_vp, _vp, _int, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64,
                                       _i64, _i64, _int, _int, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "moe_mx8_code_bytes": (_sz, [_i64]),
+    "moe_mx8_scale_bytes": (_sz, [_i64]),
+    "moe_mx8_quantize": (_int, [_vp, _int, _i64, _i64, _i64, _vp, _vp, _vp]),
+    "moe_mx8_dequantize": (_int, [_vp, _vp, _i64, _i64, _vp, _int, _i64, _vp]),
+    "moe_mx8_dispatch": (_int, [_vp, _vp, _i64, _i64, _vp, _i64, _int, _vp, _vp, _vp, _vp, _vp, _vp,
+                                _sz, _vp]),
+    "moe_mx8_product_workspace_bytes": (_sz, []),
+    "moe_mx8_product": (_int, [_vp, _vp, _i64, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _int, _vp,
+                               _sz, _vp]),
+    "moe_mx8_experts_workspace_bytes": (_sz, [_i64, _i64]),
+    "moe_mx8_experts_forward_dispatched": (_int, [_vp, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp,
+                                                  _i64, _i64, _i64, _vp, _int, _vp, _sz, _vp]),
+    "moe_mx8_forward_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64, _int, _int]),
+    "moe_mx8_forward": (_int, [_vp, _vp, _vp, _vp, _int, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64,
+                               _i64, _i64, _int, _vp, _int, _vp, _sz, _vp]),
+    "moe_rms_norm": (_int, [_vp, _i64, _vp, _i64, _vp, _int, _int, _i64, _i64, _f32, _vp, _i64, _vp,
+                            _i64, _vp, _vp, _vp, _vp]),
+    "moe_rms_norm_backward_workspace_bytes": (_sz, [_i64, _i64, _int]),
+    "moe_rms_norm_backward": (_int, [_vp, _i64, _vp, _i64, _vp, _int, _vp, _vp, _i64, _int, _i64,
+                                     _i64, _vp, _i64, _vp, _vp, _sz, _vp]),
+    "moe_route_softmax_grouped": (_int, [_vp, _int, _vp, _i64, _i64, _int, _int, _int, _int, _int,
+                                         _f32, _vp, _vp, _vp]),
+    "moe_forward_softmax_grouped": (_int, [_vp, _vp, _int, _vp, _vp, _vp, _vp, _int, _i64, _i64,
+                                           _i64, _i64, _int, _int, _int, _int, _int, _f32, _vp,
+                                           _vp, _sz, _vp]),
 }
 
 _lib = None

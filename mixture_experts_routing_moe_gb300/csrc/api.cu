@@ -5,6 +5,7 @@
 #include <math.h>
 #include <string.h>
 
+#include "../../include/moe_front.h"
 #include "common.cuh"
 #include "launch.h"
 
@@ -87,7 +88,7 @@ int run_experts(const void* x_d, const int32_t* offsets, int64_t rows, const voi
                                        (int)I, y, a, status, s, between));
 }
 
-int check_sigmoid_args(int64_t T, int64_t E, int top_k, int G, int SG, int top_two, float scale) {
+int check_grouped_args(int64_t T, int64_t E, int top_k, int G, int SG, int top_two, float scale) {
   if (T < 0 || E < 1 || E > kMaxE || G < 1 || G > 128 || E % G != 0) return MOE_ERR_SHAPE;
   if (SG < 1 || SG > G || top_k < 1 || top_k > 64) return MOE_ERR_SHAPE;
   if ((int64_t)top_k > (int64_t)SG * (E / G)) return MOE_ERR_SHAPE;
@@ -97,9 +98,11 @@ int check_sigmoid_args(int64_t T, int64_t E, int top_k, int G, int SG, int top_t
   return MOE_OK;
 }
 
-// How a forward routes its tokens: the softmax router of §4 or the sigmoid router of §10.
+// How a forward routes its tokens: the softmax router of §4, the sigmoid router of §10, or softmax
+// with groups.
+enum Router { kSoftmax, kSigmoidGrouped, kSoftmaxGrouped };
 struct RouteSpec {
-  bool sigmoid;
+  Router router;
   int renormalize;
   const float* bias;
   int groups, selected_groups, top_two;
@@ -180,7 +183,7 @@ int run_forward(const void* x, const void* logits, int ldt, const void* gate, co
     f.I = (int)I;
     f.k = top_k;
     f.renorm = rs.renormalize != 0;
-    f.sigmoid = rs.sigmoid ? 1 : 0;
+    f.sigmoid = rs.router == kSigmoidGrouped;
     f.bias = rs.bias;
     f.G = rs.groups;
     f.SG = rs.selected_groups;
@@ -204,12 +207,12 @@ int run_forward(const void* x, const void* logits, int ldt, const void* gate, co
   }
   if (cudaMemsetAsync(status, 0, sizeof(unsigned), s) != cudaSuccess) return MOE_ERR_CUDA;
   if (!record(events, 0, s)) return MOE_ERR_CUDA;
+  const auto grouped = rs.router == kSigmoidGrouped ? launch_route_sigmoid : launch_route_softmax_grouped;
   cudaError_t err =
-      rs.sigmoid
-          ? launch_route_sigmoid(logits, ldt, rs.bias, T, (int)E, top_k, rs.groups,
-                                 rs.selected_groups, rs.top_two != 0, rs.renormalize != 0,
-                                 rs.scale, idx, w, s)
-          : launch_route(logits, ldt, T, (int)E, top_k, rs.renormalize != 0, idx, w, s);
+      rs.router == kSoftmax
+          ? launch_route(logits, ldt, T, (int)E, top_k, rs.renormalize != 0, idx, w, s)
+          : grouped(logits, ldt, rs.bias, T, (int)E, top_k, rs.groups, rs.selected_groups,
+                    rs.top_two != 0, rs.renormalize != 0, rs.scale, idx, w, s);
   if (err != cudaSuccess || !record(events, 1, s)) return MOE_ERR_CUDA;
   err = launch_dispatch(x, wdt, T, H, idx, (int)E, top_k, xd, offsets, tor, ros, hist, status, s);
   if (err != cudaSuccess || !record(events, 2, s)) return MOE_ERR_CUDA;
@@ -259,13 +262,30 @@ int moe_route_sigmoid_grouped(const void* logits, int ldt, const float* bias, in
                               int group_top_two, int renormalize, float scale, uint32_t* idx,
                               void* w, moe_stream_t stream) {
   if (!valid_dtype(ldt)) return MOE_ERR_DTYPE;
-  const int st = check_sigmoid_args(T, E, top_k, groups, selected_groups, group_top_two, scale);
+  const int st = check_grouped_args(T, E, top_k, groups, selected_groups, group_top_two, scale);
   if (st != MOE_OK) return st;
   if (T == 0) return MOE_OK;
   if (!logits || !idx || !w) return MOE_ERR_NULL;
   return cuda_status(launch_route_sigmoid(logits, ldt, bias, T, (int)E, top_k, groups,
                                           selected_groups, group_top_two != 0, renormalize != 0,
                                           scale, idx, w, (cudaStream_t)stream));
+}
+
+int moe_route_softmax_grouped(const void* logits, int ldt, const float* bias, int64_t T, int64_t E,
+                              int top_k, int groups, int selected_groups, int group_top_two,
+                              int renormalize, float scale, uint32_t* idx, void* w,
+                              moe_stream_t stream) {
+  if (!valid_dtype(ldt)) return MOE_ERR_DTYPE;
+  const int st = check_grouped_args(T, E, top_k, groups, selected_groups, group_top_two, scale);
+  if (st != MOE_OK) return st;
+  if (T == 0) return MOE_OK;
+  if (!logits || !idx || !w) return MOE_ERR_NULL;
+  const uintptr_t es = dtype_size(ldt) - 1;
+  if (((uintptr_t)logits | (uintptr_t)w) & es || ((uintptr_t)idx | (uintptr_t)bias) & 3u)
+    return MOE_ERR_ALIGN;
+  return cuda_status(launch_route_softmax_grouped(
+      logits, ldt, bias, T, (int)E, top_k, groups, selected_groups, group_top_two != 0,
+      renormalize != 0, scale, idx, w, (cudaStream_t)stream));
 }
 
 static int check_router_train(int ldt, int idt, int64_t T, int64_t E, int top_k, int scoring,
@@ -406,7 +426,7 @@ int moe_forward(const void* x, const void* logits, int ldt, const void* gate, co
                 int renormalize, void* out, void* ws, size_t ws_bytes, moe_stream_t stream) {
   const int st = check_route_shape(T, E, top_k);
   if (st != MOE_OK) return st;
-  const RouteSpec r{false, renormalize, nullptr, 1, 1, 0, 1.f};
+  const RouteSpec r{kSoftmax, renormalize, nullptr, 1, 1, 0, 1.f};
   return run_forward(x, logits, ldt, gate, up, down, wdt, T, E, H, I, top_k, r, out, ws, ws_bytes,
                      (cudaStream_t)stream, nullptr, /*allow_fused=*/true);
 }
@@ -420,7 +440,7 @@ int moe_wait_selftest(void* ws, size_t ws_bytes, moe_stream_t stream) {
 int moe_forward_fused(int64_t T, int64_t E, int64_t H, int64_t I, int top_k, int ldt, int wdt) {
   if (check_route_shape(T, E, top_k) != MOE_OK || check_experts_shape(T * top_k, E, H, I) != MOE_OK)
     return 0;
-  const RouteSpec r{false, 1, nullptr, 1, 1, 0, 1.f};
+  const RouteSpec r{kSoftmax, 1, nullptr, 1, 1, 0, 1.f};
   return takes_fused(r, T, E, H, I, top_k, ldt, wdt) ? 1 : 0;
 }
 
@@ -430,7 +450,7 @@ int moe_forward_with_events(const void* x, const void* logits, int ldt, const vo
                             size_t ws_bytes, moe_stream_t stream, void* const* events) {
   const int st = check_route_shape(T, E, top_k);
   if (st != MOE_OK) return st;
-  const RouteSpec r{false, renormalize, nullptr, 1, 1, 0, 1.f};
+  const RouteSpec r{kSoftmax, renormalize, nullptr, 1, 1, 0, 1.f};
   return run_forward(x, logits, ldt, gate, up, down, wdt, T, E, H, I, top_k, r, out, ws, ws_bytes,
                      (cudaStream_t)stream, events, /*allow_fused=*/false);
 }
@@ -442,11 +462,25 @@ int moe_forward_sigmoid_grouped(const void* x, const void* logits, int ldt, cons
                                 float scale, void* out, void* ws, size_t ws_bytes,
                                 moe_stream_t stream) {
   if (!valid_dtype(ldt)) return MOE_ERR_DTYPE;
-  const int st = check_sigmoid_args(T, E, top_k, groups, selected_groups, group_top_two, scale);
+  const int st = check_grouped_args(T, E, top_k, groups, selected_groups, group_top_two, scale);
   if (st != MOE_OK) return st;
-  const RouteSpec r{true, renormalize, bias, groups, selected_groups, group_top_two, scale};
+  const RouteSpec r{kSigmoidGrouped, renormalize, bias, groups, selected_groups, group_top_two, scale};
   return run_forward(x, logits, ldt, gate, up, down, wdt, T, E, H, I, top_k, r, out, ws, ws_bytes,
                      (cudaStream_t)stream, nullptr, /*allow_fused=*/true);
+}
+
+int moe_forward_softmax_grouped(const void* x, const void* logits, int ldt, const float* bias,
+                                const void* gate, const void* up, const void* down, int wdt,
+                                int64_t T, int64_t E, int64_t H, int64_t I, int top_k, int groups,
+                                int selected_groups, int group_top_two, int renormalize,
+                                float scale, void* out, void* ws, size_t ws_bytes,
+                                moe_stream_t stream) {
+  if (!valid_dtype(ldt)) return MOE_ERR_DTYPE;
+  const int st = check_grouped_args(T, E, top_k, groups, selected_groups, group_top_two, scale);
+  if (st != MOE_OK) return st;
+  const RouteSpec r{kSoftmaxGrouped, renormalize, bias, groups, selected_groups, group_top_two, scale};
+  return run_forward(x, logits, ldt, gate, up, down, wdt, T, E, H, I, top_k, r, out, ws, ws_bytes,
+                     (cudaStream_t)stream, nullptr, /*allow_fused=*/false);
 }
 
 int moe_combine_backward(const void* y, int ydt, const uint32_t* row_of_slot, const void* w,

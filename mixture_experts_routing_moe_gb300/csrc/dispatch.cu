@@ -195,7 +195,42 @@ __global__ void __launch_bounds__(THREADS)
   }
 }
 
+// The same for rows in blocks: `vecs` 16-byte vectors of codes and `words` words of scales a row.
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS)
+    moe_dispatch_block_rows(const uint4* __restrict__ codes, const uint32_t* __restrict__ scales,
+                            int64_t T, int64_t vecs, int64_t words, int k,
+                            const uint32_t* __restrict__ row_of_slot, uint4* __restrict__ codes_d,
+                            uint32_t* __restrict__ scales_d) {
+  extern __shared__ uint32_t rows_smem[];
+  for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
+    for (int j = threadIdx.x; j < k; j += THREADS) rows_smem[j] = row_of_slot[t * k + j];
+    __syncthreads();
+    for (int64_t c = threadIdx.x; c < vecs; c += THREADS) {
+      const uint4 v = ld_nc_v4(codes + t * vecs + c);
+      for (int j = 0; j < k; ++j)
+        if (rows_smem[j] != kInvalidRow) st_v4(codes_d + (int64_t)rows_smem[j] * vecs + c, v);
+    }
+    for (int64_t c = threadIdx.x; c < words; c += THREADS) {
+      const uint32_t v = __ldg(scales + t * words + c);
+      for (int j = 0; j < k; ++j)
+        if (rows_smem[j] != kInvalidRow) scales_d[(int64_t)rows_smem[j] * words + c] = v;
+    }
+    __syncthreads();
+  }
+}
+
 }  // namespace
+
+cudaError_t launch_dispatch_block_rows(const uint8_t* codes, const uint8_t* scales, int64_t T,
+                                       int64_t code_bytes, int64_t scale_bytes, int k,
+                                       const uint32_t* row_of_slot, uint8_t* codes_d,
+                                       uint8_t* scales_d, cudaStream_t s) {
+  moe_dispatch_block_rows<128><<<(unsigned)(T < 65536 ? T : 65536), 128, (size_t)k * 4, s>>>(
+      (const uint4*)codes, (const uint32_t*)scales, T, code_bytes / 16, scale_bytes / 4, k,
+      row_of_slot, (uint4*)codes_d, (uint32_t*)scales_d);
+  return cudaGetLastError();
+}
 
 DispatchPlan dispatch_plan(int64_t R) {
   DispatchPlan p;
@@ -266,10 +301,9 @@ size_t dispatch_scratch_bytes(int64_t R, int E) {  // per-chunk histograms + per
   return ((size_t)dispatch_plan(R).W + 1) * (size_t)E * sizeof(int32_t);
 }
 
-cudaError_t launch_dispatch(const void* x, int xdt, int64_t T, int64_t H, const uint32_t* idx,
-                            int E, int k, void* x_d, int32_t* offsets, uint32_t* token_of_row,
-                            uint32_t* row_of_slot, int32_t* hist, unsigned* status,
-                            cudaStream_t s) {
+cudaError_t launch_dispatch_map(int64_t T, const uint32_t* idx, int E, int k, int32_t* offsets,
+                                uint32_t* token_of_row, uint32_t* row_of_slot, int32_t* hist,
+                                unsigned* status, cudaStream_t s) {
   const int64_t R = T * k;
   if (R <= kSmallR) {
     const int CH = (int)(((R + kSmallWarps - 1) / kSmallWarps + 31) / 32 * 32);
@@ -286,6 +320,16 @@ cudaError_t launch_dispatch(const void* x, int xdt, int64_t T, int64_t H, const 
     moe_dispatch_scatter<<<blocks, kDispWarps * 32, smem, s>>>(
         idx, R, E, k, p.W, p.CH, hist, totals, offsets, token_of_row, row_of_slot);
   }
+  return cudaGetLastError();
+}
+
+cudaError_t launch_dispatch(const void* x, int xdt, int64_t T, int64_t H, const uint32_t* idx,
+                            int E, int k, void* x_d, int32_t* offsets, uint32_t* token_of_row,
+                            uint32_t* row_of_slot, int32_t* hist, unsigned* status,
+                            cudaStream_t s) {
+  const cudaError_t err = launch_dispatch_map(T, idx, E, k, offsets, token_of_row, row_of_slot, hist,
+                                              status, s);
+  if (err != cudaSuccess) return err;
   const size_t esz = xdt == MOE_F32 ? 4 : 2;
   const int64_t vecs = H * (int64_t)esz / 16;
   int64_t grid = T < 65536 ? T : 65536;

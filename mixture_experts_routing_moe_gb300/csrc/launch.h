@@ -22,6 +22,11 @@ cudaError_t launch_route_sigmoid(const void* logits, int ldt, const float* bias,
                                  int k, int G, int SG, int top_two, int renorm, float scale,
                                  uint32_t* idx, void* w, cudaStream_t s);
 
+// Group-limited softmax routing (float64 selection); bias may be null.
+cudaError_t launch_route_softmax_grouped(const void* logits, int ldt, const float* bias, int64_t T,
+                                         int E, int k, int G, int SG, int top_two, int renorm,
+                                         float scale, uint32_t* idx, void* w, cudaStream_t s);
+
 // Fixed-selection router weights (grad_w == nullptr) or their logits gradient.
 cudaError_t launch_router_train(const void* logits, int ldt, const void* idx, int idt,
                                 const float* grad_w, int64_t T, int E, int k, int scoring,
@@ -59,6 +64,16 @@ cudaError_t launch_dispatch(const void* x, int xdt, int64_t T, int64_t H, const 
                             int E, int k, void* x_d, int32_t* offsets, uint32_t* token_of_row,
                             uint32_t* row_of_slot, int32_t* hist, unsigned* status,
                             cudaStream_t s);
+
+// The map alone, without the rows.
+cudaError_t launch_dispatch_map(int64_t T, const uint32_t* idx, int E, int k, int32_t* offsets,
+                                uint32_t* token_of_row, uint32_t* row_of_slot, int32_t* hist,
+                                unsigned* status, cudaStream_t s);
+// Rows in blocks (code_bytes a multiple of 16, scale_bytes of 4) copied to their slots' rows.
+cudaError_t launch_dispatch_block_rows(const uint8_t* codes, const uint8_t* scales, int64_t T,
+                                       int64_t code_bytes, int64_t scale_bytes, int k,
+                                       const uint32_t* row_of_slot, uint8_t* codes_d,
+                                       uint8_t* scales_d, cudaStream_t s);
 
 // One bounded mbarrier wait that nothing completes: sets kStatusTimeout in *status after ~1 s.
 cudaError_t launch_wait_selftest(unsigned* status, cudaStream_t s);

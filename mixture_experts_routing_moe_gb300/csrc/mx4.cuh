@@ -72,16 +72,16 @@ cudaError_t launch_mx4_quantize(const void* x, int xdt, int64_t rows, int64_t K,
 cudaError_t launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows,
                                   int64_t K, void* out, int odt, int64_t ldo, cudaStream_t s);
 // One row operand of a product.
-struct Mx4Rows {
+struct MxRows {
   const uint8_t* codes;
   const uint8_t* scales;
 };
 // out = A B^T by groups; zero_status: this launch zeroes *status (it is the first of the call).
-cudaError_t launch_mx4_product(Mx4Rows a, int64_t rows, Mx4Rows b, const int32_t* offsets, int E,
+cudaError_t launch_mx4_product(MxRows a, int64_t rows, MxRows b, const int32_t* offsets, int E,
                                int N, int K, void* out, int odt, unsigned* status,
                                bool zero_status, cudaStream_t s);
 // codes / scales of silu(A gate^T) * (A up^T), rows of I values.
-cudaError_t launch_mx4_gate_up(Mx4Rows a, int64_t rows, Mx4Rows gate, Mx4Rows up,
+cudaError_t launch_mx4_gate_up(MxRows a, int64_t rows, MxRows gate, MxRows up,
                                const int32_t* offsets, int E, int I, int H, uint8_t* codes,
                                uint8_t* scales, unsigned* status, cudaStream_t s);
 
@@ -97,7 +97,7 @@ struct Mx4TokensArgs {
   const void* x;
   const void* router;
   int dt, T, E, H, I, k, renorm;
-  Mx4Rows gate, up, down;
+  MxRows gate, up, down;
   void* out;
   uint32_t* idx;  // may be null
   float* w;       // may be null

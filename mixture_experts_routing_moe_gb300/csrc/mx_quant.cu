@@ -1,9 +1,10 @@
-// moe_mx4_quantize / moe_mx4_dequantize: rows to microscaled 4-bit blocks and back.
+// moe_mx4_quantize / moe_mx4_dequantize and moe_mx8_quantize / moe_mx8_dequantize: rows to
+// microscaled blocks (of 4 or 8 bits a value) and back.
 //
 // A block's scale is a power of two taken from the exponent field of its largest magnitude, so
-// scaling is exact and the only rounding is the conversion to e2m1.  Both kernels are bound by
-// memory: 2 or 4 bytes a value against 17/32 of a byte.  A lane owns units of eight consecutive
-// values (16 or 32 bytes in, four bytes of codes out), four lanes a block; the block's maximum is
+// scaling is exact and the only rounding is the conversion to e2m1 or e4m3.  Both kernels are bound
+// by memory: 2 or 4 bytes a value against 17/32 or 33/32 of a byte.  A lane owns units of eight
+// consecutive values (16 or 32 bytes in, four or eight bytes of codes out), four lanes a block; the block's maximum is
 // two shuffles.  A group of L lanes (32, or a smaller power of two for narrow rows) takes U * L
 // units of one row, U of them in flight; values wait in their storage type (16 registers for four
 // units of 16 bits), which leaves room for 2048 threads an SM: with them widened on arrival,
@@ -12,10 +13,11 @@
 // consecutive elements, and turned around in shared memory.
 #include "launch.h"
 #include "mx4.cuh"
+#include "mx8.cuh"
 
 namespace moe {
 namespace {
-using namespace mx4;
+using mx4::blocks_of;
 
 constexpr int kThreads = 256, U = 4;
 
@@ -46,6 +48,34 @@ __device__ __forceinline__ uint32_t top_bits(const Unit<__half>& q) {
   return __float_as_uint(__half2float(__ushort_as_half((unsigned short)top_bits16(q.u[0]))));
 }
 
+// The codes of a unit in the two formats.
+struct Unit4 {
+  typedef uint32_t Code;
+  static __device__ uint32_t scale_byte(uint32_t top) { return mx4::scale_byte(top); }
+  static __device__ Code codes(const float* v, uint32_t b) {
+    return b == 255u ? 0u : mx4::codes8(v, mx4::inv_scale(b));
+  }
+  static __device__ void values(Code c, uint32_t b, float* v) {
+    mx4::values8(c, mx4::scale_value(b), v);
+  }
+  static __device__ Code none() { return 0u; }
+};
+struct Unit8 {
+  typedef uint2 Code;
+  static __device__ uint32_t scale_byte(uint32_t top) { return mx8::scale_byte(top); }
+  static __device__ Code codes(const float* v, uint32_t b) {
+    if (b == 255u) return none();
+    const float inv = mx8::inv_scale(b);
+    return make_uint2(mx8::codes4(v, inv), mx8::codes4(v + 4, inv));
+  }
+  static __device__ void values(Code c, uint32_t b, float* v) {
+    const float s = mx8::scale_value(b);
+    mx8::values4(c.x, s, v);
+    mx8::values4(c.y, s, v + 4);
+  }
+  static __device__ Code none() { return make_uint2(0u, 0u); }
+};
+
 // Group g of L lanes: row g of the grid's x extent, piece blockIdx.y of the row.
 struct Place {
   int64_t row;
@@ -61,9 +91,9 @@ __device__ __forceinline__ Place place(int64_t rows, int L) {
   return p;
 }
 
-template <typename T, bool VEC>
+template <typename F, typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads)
-    moe_mx4_quantize_kernel(const T* __restrict__ x, int64_t rows, int K, int64_t ldx,
+    moe_mx_quantize_kernel(const T* __restrict__ x, int64_t rows, int K, int64_t ldx,
                             uint8_t* __restrict__ codes, uint8_t* __restrict__ scales, int L,
                             int units, unsigned* status) {
   __shared__ __align__(16) T turn[VEC ? 1 : kThreads / 32][VEC ? 8 : 256];
@@ -94,7 +124,8 @@ __global__ void __launch_bounds__(kThreads)
       }
     }
   }
-  uint8_t* crow = codes + p.row * (int64_t)(units * 4);
+  typedef typename F::Code Code;
+  Code* crow = reinterpret_cast<Code*>(codes) + p.row * (int64_t)units;
   uint8_t* srow = scales + p.row * (int64_t)((units / 4 + 3) / 4 * 4);
 #pragma unroll
   for (int j = 0; j < U; ++j) {
@@ -112,13 +143,13 @@ __global__ void __launch_bounds__(kThreads)
     uint32_t top = top_bits(q[j]);
     top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
     top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-    const uint32_t b = scale_byte(top);
+    const uint32_t b = F::scale_byte(top);
     float v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = Dt<T>::to_f(q[j].e[i]);
-    const uint32_t c = b == 255u ? 0u : codes8(v, inv_scale(b));
+    const Code c = F::codes(v, b);
     if (p.ok && unit < units) {
-      *reinterpret_cast<uint32_t*>(crow + unit * 4) = c;
+      crow[unit] = c;
       if ((unit & 3) == 0) srow[unit >> 2] = (uint8_t)b;
       // the bytes past the last block of the row
       if (unit == units - 1)
@@ -127,29 +158,31 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-template <typename T, bool VEC>
+template <typename F, typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads)
-    moe_mx4_dequantize_kernel(const uint8_t* __restrict__ codes,
+    moe_mx_dequantize_kernel(const uint8_t* __restrict__ codes,
                               const uint8_t* __restrict__ scales, int64_t rows, int K,
                               T* __restrict__ out, int64_t ldo, int L, int units) {
   __shared__ __align__(16) T turn[VEC ? 1 : kThreads / 32][VEC ? 8 : 256];
   const Place p = place(rows, L);
   T* row = out + p.row * ldo;
-  const uint8_t* crow = codes + p.row * (int64_t)(units * 4);
+  typedef typename F::Code Code;
+  const Code* crow = reinterpret_cast<const Code*>(codes) + p.row * (int64_t)units;
   const uint8_t* srow = scales + p.row * (int64_t)((units / 4 + 3) / 4 * 4);
-  uint32_t c[U], b[U];
+  Code c[U];
+  uint32_t b[U];
 #pragma unroll
   for (int j = 0; j < U; ++j) {
     const int unit = p.unit0 + j * L + p.gl;
     const bool in = p.ok && unit < units;
-    c[j] = in ? __ldg(reinterpret_cast<const uint32_t*>(crow + unit * 4)) : 0u;
+    c[j] = in ? __ldg(crow + unit) : F::none();
     b[j] = in ? __ldg(srow + (unit >> 2)) : 0u;
   }
 #pragma unroll
   for (int j = 0; j < U; ++j) {
     const int u0 = p.unit0 + j * L, c0 = (u0 + p.gl) * 8;
     float v[8];
-    values8(c[j], scale_value(b[j]), v);
+    F::values(c[j], b[j], v);
     Unit<T> q;
 #pragma unroll
     for (int i = 0; i < 8; ++i) q.e[i] = Dt<T>::from_f(v[i]);
@@ -196,24 +229,47 @@ bool vec_rows(const void* p, int64_t ld, int size) {
   return ((uintptr_t)p & 15u) == 0 && (ld * size) % 16 == 0;
 }
 
-template <typename T>
+template <typename F, typename T>
 cudaError_t quantize_t(const T* x, int64_t rows, int64_t K, int64_t ldx, uint8_t* codes,
                        uint8_t* scales, unsigned* status, cudaStream_t s) {
   const RowPlan p = plan_rows(rows, K);
-  const auto kern = vec_rows(x, ldx, sizeof(T)) ? moe_mx4_quantize_kernel<T, true>
-                                                : moe_mx4_quantize_kernel<T, false>;
+  const auto kern = vec_rows(x, ldx, sizeof(T)) ? moe_mx_quantize_kernel<F, T, true>
+                                                : moe_mx_quantize_kernel<F, T, false>;
   kern<<<p.grid, kThreads, 0, s>>>(x, rows, (int)K, ldx, codes, scales, p.L, p.units, status);
   return cudaGetLastError();
 }
 
-template <typename T>
+template <typename F, typename T>
 cudaError_t dequantize_t(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t K,
                          T* out, int64_t ldo, cudaStream_t s) {
   const RowPlan p = plan_rows(rows, K);
-  const auto kern = vec_rows(out, ldo, sizeof(T)) ? moe_mx4_dequantize_kernel<T, true>
-                                                  : moe_mx4_dequantize_kernel<T, false>;
+  const auto kern = vec_rows(out, ldo, sizeof(T)) ? moe_mx_dequantize_kernel<F, T, true>
+                                                  : moe_mx_dequantize_kernel<F, T, false>;
   kern<<<p.grid, kThreads, 0, s>>>(codes, scales, rows, (int)K, out, ldo, p.L, p.units);
   return cudaGetLastError();
+}
+
+template <typename F>
+cudaError_t quantize(const void* x, int xdt, int64_t rows, int64_t K, int64_t ldx, uint8_t* codes,
+                     uint8_t* scales, unsigned* status, cudaStream_t s) {
+  switch (xdt) {
+    case MOE_F32: return quantize_t<F>((const float*)x, rows, K, ldx, codes, scales, status, s);
+    case MOE_F16: return quantize_t<F>((const __half*)x, rows, K, ldx, codes, scales, status, s);
+    case MOE_BF16:
+      return quantize_t<F>((const __nv_bfloat16*)x, rows, K, ldx, codes, scales, status, s);
+  }
+  return cudaErrorInvalidValue;
+}
+
+template <typename F>
+cudaError_t dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t K,
+                       void* out, int odt, int64_t ldo, cudaStream_t s) {
+  switch (odt) {
+    case MOE_F32: return dequantize_t<F>(codes, scales, rows, K, (float*)out, ldo, s);
+    case MOE_F16: return dequantize_t<F>(codes, scales, rows, K, (__half*)out, ldo, s);
+    case MOE_BF16: return dequantize_t<F>(codes, scales, rows, K, (__nv_bfloat16*)out, ldo, s);
+  }
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace
@@ -221,23 +277,22 @@ cudaError_t dequantize_t(const uint8_t* codes, const uint8_t* scales, int64_t ro
 cudaError_t launch_mx4_quantize(const void* x, int xdt, int64_t rows, int64_t K, int64_t ldx,
                                 uint8_t* codes, uint8_t* scales, unsigned* status,
                                 cudaStream_t s) {
-  switch (xdt) {
-    case MOE_F32: return quantize_t((const float*)x, rows, K, ldx, codes, scales, status, s);
-    case MOE_F16: return quantize_t((const __half*)x, rows, K, ldx, codes, scales, status, s);
-    case MOE_BF16:
-      return quantize_t((const __nv_bfloat16*)x, rows, K, ldx, codes, scales, status, s);
-  }
-  return cudaErrorInvalidValue;
+  return quantize<Unit4>(x, xdt, rows, K, ldx, codes, scales, status, s);
 }
 
 cudaError_t launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows,
                                   int64_t K, void* out, int odt, int64_t ldo, cudaStream_t s) {
-  switch (odt) {
-    case MOE_F32: return dequantize_t(codes, scales, rows, K, (float*)out, ldo, s);
-    case MOE_F16: return dequantize_t(codes, scales, rows, K, (__half*)out, ldo, s);
-    case MOE_BF16: return dequantize_t(codes, scales, rows, K, (__nv_bfloat16*)out, ldo, s);
-  }
-  return cudaErrorInvalidValue;
+  return dequantize<Unit4>(codes, scales, rows, K, out, odt, ldo, s);
+}
+
+cudaError_t launch_mx8_quantize(const void* x, int xdt, int64_t rows, int64_t K, int64_t ldx,
+                                uint8_t* codes, uint8_t* scales, cudaStream_t s) {
+  return quantize<Unit8>(x, xdt, rows, K, ldx, codes, scales, nullptr, s);
+}
+
+cudaError_t launch_mx8_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows,
+                                  int64_t K, void* out, int odt, int64_t ldo, cudaStream_t s) {
+  return dequantize<Unit8>(codes, scales, rows, K, out, odt, ldo, s);
 }
 
 }  // namespace moe
