@@ -34,6 +34,21 @@ __device__ __forceinline__ uint32_t codes4(const float* v, float inv) {
       : "f"(v[0] * inv), "f"(v[1] * inv), "f"(v[2] * inv), "f"(v[3] * inv));
   return r;
 }
+// The same of two register pairs, scaled with the packed multiplication.
+__device__ __forceinline__ uint32_t codes4(const unsigned long long* v, unsigned long long inv) {
+  uint32_t r;
+  asm("{\n\t.reg .b64 a, b;\n\t.reg .f32 f0, f1, f2, f3;\n\t.reg .b16 h0, h1;\n\t"
+      "mul.rn.f32x2 a, %1, %3;\n\t"
+      "mul.rn.f32x2 b, %2, %3;\n\t"
+      "mov.b64 {f0, f1}, a;\n\t"
+      "mov.b64 {f2, f3}, b;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 h0, f1, f0;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 h1, f3, f2;\n\t"
+      "mov.b32 %0, {h0, h1};\n\t}"
+      : "=r"(r)
+      : "l"(v[0]), "l"(v[1]), "l"(inv));
+  return r;
+}
 // Four codes to four values.
 __device__ __forceinline__ void values4(uint32_t c, float s, float* v) {
   uint32_t h[2];

@@ -22,17 +22,36 @@ namespace {
 template <typename T>
 constexpr int kUnits = sizeof(T) == 4 ? 2 : 4;
 
+// Eight values, as words: a union with elements of 16 bits is taken apart into them where a full and a
+// partial unit's paths meet, and every word put together again (1400 instructions a warp and row of
+// 7168, of which 700 were that).
 template <typename T>
-union Unit {
-  static constexpr int V = sizeof(T) / 2;
-  uint4 u[V];
-  T e[8];
+struct Unit {
+  static constexpr int V = sizeof(T) / 2, WORDS = 4 * V;  // 16-byte vectors, 32-bit words
+  uint32_t w[WORDS];
 };
+template <typename T>
+__device__ __forceinline__ void put_vec(Unit<T>& q, int i, const uint4& v) {
+  q.w[4 * i] = v.x, q.w[4 * i + 1] = v.y, q.w[4 * i + 2] = v.z, q.w[4 * i + 3] = v.w;
+}
+// One element of a row (0 past it), as bits; READ_ONLY: no one writes the row.
+template <typename T, bool READ_ONLY>
+__device__ __forceinline__ uint32_t element(const T* row, int c, int H) {
+  if (c >= H) return 0u;
+  if constexpr (sizeof(T) == 4) {
+    const uint32_t* p = reinterpret_cast<const uint32_t*>(row) + c;
+    return READ_ONLY ? __ldg(p) : *p;
+  } else {
+    const unsigned short* p = reinterpret_cast<const unsigned short*>(row) + c;
+    return READ_ONLY ? __ldg(p) : *p;
+  }
+}
 
-// Plain loads: outputs may be the inputs themselves.
+// Rows are read once and leave L1 to the weights; not through the read-only path, as outputs may be
+// the inputs themselves.
 __device__ __forceinline__ uint4 ld_v4(const void* p) {
   uint4 r;
-  asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];"
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
                : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
                : "l"(p)
                : "memory");
@@ -44,6 +63,16 @@ template <bool VEC>
 __device__ __forceinline__ int column(int u0, int lane, int i) {
   return VEC ? (u0 + lane) * 8 + i : u0 * 8 + i * 32 + lane;
 }
+template <typename T, bool VEC, bool READ_ONLY>
+__device__ __forceinline__ void load_elements(const T* row, int u0, int lane, int H, Unit<T>& q) {
+  constexpr int PER = 8 / Unit<T>::WORDS;  // elements of a word
+#pragma unroll
+  for (int i = 0; i < Unit<T>::WORDS; ++i) {
+    q.w[i] = element<T, READ_ONLY>(row, column<VEC>(u0, lane, PER * i), H);
+    if (PER == 2)
+      q.w[i] |= element<T, READ_ONLY>(row, column<VEC>(u0, lane, PER * i + 1), H) << 16;
+  }
+}
 // A lane's unit of a row of H values (zeros past it).
 template <typename T, bool VEC>
 __device__ __forceinline__ Unit<T> load_unit(const T* row, int u0, int lane, int H) {
@@ -51,13 +80,9 @@ __device__ __forceinline__ Unit<T> load_unit(const T* row, int u0, int lane, int
   if (VEC && column<VEC>(u0, lane, 8) <= H) {
 #pragma unroll
     for (int i = 0; i < Unit<T>::V; ++i)
-      q.u[i] = ld_v4(row + column<VEC>(u0, lane, 0) + i * (16 / sizeof(T)));
+      put_vec(q, i, ld_v4(row + column<VEC>(u0, lane, 0) + i * (16 / sizeof(T))));
   } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int c = column<VEC>(u0, lane, i);
-      q.e[i] = c < H ? row[c] : Dt<T>::from_f(0.f);
-    }
+    load_elements<T, VEC, false>(row, u0, lane, H, q);
   }
   return q;
 }
@@ -66,33 +91,112 @@ __device__ __forceinline__ void store_unit(T* row, const Unit<T>& q, int u0, int
   if (VEC && column<VEC>(u0, lane, 8) <= H) {
 #pragma unroll
     for (int i = 0; i < Unit<T>::V; ++i)
-      st_v4(row + column<VEC>(u0, lane, 0) + i * (16 / sizeof(T)), q.u[i]);
+      st_v4(row + column<VEC>(u0, lane, 0) + i * (16 / sizeof(T)),
+            make_uint4(q.w[4 * i], q.w[4 * i + 1], q.w[4 * i + 2], q.w[4 * i + 3]));
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int c = column<VEC>(u0, lane, i);
-      if (c < H) row[c] = q.e[i];
+      if (c >= H) continue;
+      if constexpr (sizeof(T) == 4) reinterpret_cast<uint32_t*>(row)[c] = q.w[i];
+      else reinterpret_cast<unsigned short*>(row)[c] = (unsigned short)(q.w[i / 2] >> (i % 2 * 16));
     }
   }
 }
-template <typename T>
-__device__ __forceinline__ void widen(const Unit<T>& q, float* v) {
+// Two FP32 values in a register pair, for the packed instructions: the kernels are as much bound by the
+// issue of instructions as by memory (44 a value without these, 205 us for 16384 x 7168 bf16).
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 pack(float lo, float hi) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpack(f2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ float sum2(f2 v) {
+  const float2 f = unpack(v);
+  return f.x + f.y;
+}
+
+// The values of a unit in FP32, and back (rounded once).
+__device__ __forceinline__ void widen(const Unit<float>& q, f2* v) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = Dt<T>::to_f(q.e[i]);
+  for (int i = 0; i < 4; ++i)
+    v[i] = pack(__uint_as_float(q.w[2 * i]), __uint_as_float(q.w[2 * i + 1]));
+}
+__device__ __forceinline__ void widen(const Unit<__half>& q, f2* v) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float lo, hi;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
+        : "=f"(lo), "=f"(hi)
+        : "r"(q.w[i]));
+    v[i] = pack(lo, hi);
+  }
+}
+__device__ __forceinline__ void widen(const Unit<__nv_bfloat16>& q, f2* v) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    v[i] = pack(__uint_as_float(q.w[i] << 16), __uint_as_float(q.w[i] & 0xFFFF0000u));
 }
 template <typename T>
-__device__ __forceinline__ Unit<T> narrow(const float* v) {
+__device__ __forceinline__ Unit<T> narrow(const f2* v) {
   Unit<T> q;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) q.e[i] = Dt<T>::from_f(v[i]);
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = unpack(v[i]);
+    if constexpr (sizeof(T) == 4) {
+      q.w[2 * i] = __float_as_uint(f.x);
+      q.w[2 * i + 1] = __float_as_uint(f.y);
+    } else if constexpr (Dt<T>::code == MOE_F16) {
+      asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(q.w[i]) : "f"(f.y), "f"(f.x));
+    } else {
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(q.w[i]) : "f"(f.y), "f"(f.x));
+    }
+  }
   return q;
 }
-// Eight weights, held in T or in FP32.
-template <typename T, bool VEC>
-__device__ __forceinline__ void load_weight(const void* w, bool w32, int u0, int lane, int H,
-                                            float* v) {
-  if (w32) widen(load_unit<float, VEC>((const float*)w, u0, lane, H), v);
-  else widen(load_unit<T, VEC>((const T*)w, u0, lane, H), v);
+// s = round(x + residual)
+template <typename T>
+__device__ __forceinline__ Unit<T> add_units(const Unit<T>& x, const Unit<T>& res) {
+  f2 a[4], b[4];
+  widen(x, a);
+  widen(res, b);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) a[i] = add2(a[i], b[i]);
+  return narrow<T>(a);
+}
+// A lane's unit of the weight (zeros past it).
+template <typename TW, bool VEC>
+__device__ __forceinline__ Unit<TW> load_weight(const void* weight, int u0, int lane, int H) {
+  const TW* w = (const TW*)weight;
+  Unit<TW> q;
+  if (VEC && column<VEC>(u0, lane, 8) <= H) {
+#pragma unroll
+    for (int i = 0; i < Unit<TW>::V; ++i)
+      put_vec(q, i, __ldg(reinterpret_cast<const uint4*>(w + column<VEC>(u0, lane, 0)) + i));
+  } else {
+    load_elements<TW, VEC, true>(w, u0, lane, H, q);
+  }
+  return q;
 }
 
 // Where a thread works: row `t` of the grid, its warp of the row, and the row's slot of the block.
@@ -112,12 +216,11 @@ __device__ __forceinline__ Place place(int W, int64_t T) {
   return p;
 }
 // The sum of v over a row's W warps, in a fixed order (every thread of the block calls it; `part` has
-// a float for each warp).
+// a float for each warp, whose last values every thread has read before another barrier).
 __device__ __forceinline__ float row_sum(float v, int W, const Place& p, float* part) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   if (W == 1) return v;
-  __syncthreads();  // the last sum's parts have been read
   if (p.lane == 0) part[threadIdx.x >> 5] = v;
   __syncthreads();
   v = 0.f;
@@ -125,16 +228,40 @@ __device__ __forceinline__ float row_sum(float v, int W, const Place& p, float* 
   return v;
 }
 
+// 1 / sqrt(m) to half a unit in FP32: one step of Newton's method from the approximation, its residual
+// 1 - m r^2 taken exactly (fused).  (1 / sqrtf(m) is off by up to one and a half.)
+__device__ __forceinline__ float rsqrt_exact(float m) {
+  const float r = rsqrtf(m), t = m * r;
+  const float e = fmaf(-t, r, 1.f) - fmaf(m, r, -t) * r;
+  return r > 0.f && r < INFINITY ? fmaf(0.5f * r, e, r) : r;
+}
+// The sum of a unit's squares, as a tree.
+__device__ __forceinline__ f2 squares(const f2* v) {
+  return add2(fma2(v[1], v[1], mul2(v[0], v[0])), fma2(v[3], v[3], mul2(v[2], v[2])));
+}
+// The larger of m and two magnitudes; a NaN stays one.
+__device__ __forceinline__ float max_abs(float m, f2 v) {
+  const float2 f = unpack(v);
+  asm("max.NaN.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(fabsf(f.x)), "f"(fabsf(f.y)));
+  return m;
+}
+
 // y, and its blocks, of a lane's unit of normalised values.  (Every lane of the warp calls it.)
-template <typename T, bool VEC>
-__device__ __forceinline__ void finish_unit(const NormArgs& a, int64_t t, bool ok, int u0, int lane,
-                                            int blocks, const float* h, float r) {
+template <typename T, typename TW, bool VEC>
+__device__ __forceinline__ void finish_unit(const NormArgs& a, int64_t t, int u0, int lane, int blocks,
+                                            const f2* h, const Unit<TW>& w, float r) {
   const int H = (int)a.H;
-  float w[8], v[8];
-  load_weight<T, VEC>(a.weight, a.w32, u0, lane, H, w);
+  f2 v[4];
+  widen(w, v);
+  const f2 r2 = pack(r, r), minus = pack(-r, -r);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = h[i] * r * w[i];
-  if (a.y && ok) store_unit<T, VEC>((T*)a.y + t * a.ldy, narrow<T>(v), u0, lane, H);
+  for (int i = 0; i < 4; ++i) {
+    // h r w with one rounding (h r and what its rounding left, both times w): a value next to a border
+    // between codes is moved by a step of the code
+    const f2 left = fma2(h[i], r2, mul2(h[i], minus));
+    v[i] = fma2(mul2(h[i], r2), v[i], mul2(left, v[i]));
+  }
+  if (a.y) store_unit<T, VEC>((T*)a.y + t * a.ldy, narrow<T>(v), u0, lane, H);
   if (!a.codes) return;
   uint8_t* crow = a.codes + t * ((int64_t)blocks * 32);
   uint8_t* srow = a.scales + t * (int64_t)((blocks + 3) / 4 * 4);
@@ -143,22 +270,25 @@ __device__ __forceinline__ void finish_unit(const NormArgs& a, int64_t t, bool o
     if (blk == blocks - 1)  // the bytes past the last block of the row
       for (int z = blocks; z & 3; ++z) srow[z] = 0;
   };
-  // (values past H are zero: their weights are)
   if (VEC) {
-    uint32_t top = 0;
+    if (column<VEC>(u0, lane, 8) > H) {  // values past H are zeros, whatever r is
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (column<VEC>(u0, lane, i) >= H) v[i] = 0.f;
-      top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = unpack(v[i]);
+        v[i] = pack(column<VEC>(u0, lane, 2 * i) < H ? f.x : 0.f,
+                    column<VEC>(u0, lane, 2 * i + 1) < H ? f.y : 0.f);
+      }
     }
+    float m = max_abs(max_abs(max_abs(max_abs(0.f, v[0]), v[1]), v[2]), v[3]);
+    uint32_t top = __float_as_uint(m);
     top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
     top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
     const uint32_t b = mx8::scale_byte(top);
     const float inv = mx8::inv_scale(b);
-    uint2 c = make_uint2(mx8::codes4(v, inv), mx8::codes4(v + 4, inv));
+    uint2 c = make_uint2(mx8::codes4(v, pack(inv, inv)), mx8::codes4(v + 2, pack(inv, inv)));
     if (b == 255u) c = make_uint2(0u, 0u);
     const int unit = u0 + lane;
-    if (ok && unit < blocks * 4) {
+    if (unit < blocks * 4) {
       *reinterpret_cast<uint2*>(crow + unit * 8) = c;
       if ((unit & 3) == 0) put_scale(unit >> 2, b);
     }
@@ -166,11 +296,12 @@ __device__ __forceinline__ void finish_unit(const NormArgs& a, int64_t t, bool o
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int c = column<VEC>(u0, lane, i), blk = u0 / 4 + i;
-      float x[4] = {c < H ? v[i] : 0.f, 0.f, 0.f, 0.f};
+      const float2 f = unpack(v[i / 2]);
+      float x[4] = {c < H ? (i & 1 ? f.y : f.x) : 0.f, 0.f, 0.f, 0.f};
       const uint32_t b = mx8::scale_byte(
           __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(x[0]) & 0x7FFFFFFFu));
       const uint32_t code = b == 255u ? 0u : mx8::codes4(x, mx8::inv_scale(b));
-      if (ok && blk < blocks) {
+      if (blk < blocks) {
         crow[c] = (uint8_t)code;
         if (lane == 0) put_scale(blk, b);
       }
@@ -178,55 +309,76 @@ __device__ __forceinline__ void finish_unit(const NormArgs& a, int64_t t, bool o
   }
 }
 
+// Blocks of 256 threads on an SM: two leave registers for two rows of 16 bits.
+template <typename T>
+constexpr int kNormBlocks = sizeof(T) == 4 ? 4 : 2;
+
+// A lane's units of a row of x and of the residual.
 template <typename T, bool VEC, int U>
-__global__ void __launch_bounds__(1024)
-    moe_rms_norm_kernel(const __grid_constant__ NormArgs a, int W, int blocks) {
-  __shared__ float part[32];
-  const Place p = place(W, a.T);
+__device__ __forceinline__ void load_rows(const NormArgs& a, int64_t t, int W, const Place& p,
+                                          Unit<T>* x, Unit<T>* res) {
   const int H = (int)a.H;
-  const int64_t t = p.ok ? p.t : 0;
-  const T* x = (const T*)a.x + t * a.ldx;
-  const T* res = a.residual ? (const T*)a.residual + t * a.ldr : nullptr;
-  Unit<T> q[U];
 #pragma unroll
-  for (int j = 0; j < U; ++j) q[j] = load_unit<T, VEC>(x, (j * W + p.w) * 32, p.lane, H);
-  if (res) {
-    Unit<T> q2[U];
+  for (int j = 0; j < U; ++j)
+    x[j] = load_unit<T, VEC>((const T*)a.x + t * a.ldx, (j * W + p.w) * 32, p.lane, H);
+  if (!a.residual) return;
 #pragma unroll
-    for (int j = 0; j < U; ++j) q2[j] = load_unit<T, VEC>(res, (j * W + p.w) * 32, p.lane, H);
+  for (int j = 0; j < U; ++j)
+    res[j] = load_unit<T, VEC>((const T*)a.residual + t * a.ldr, (j * W + p.w) * 32, p.lane, H);
+}
+
+// Row groups walk the rows g, g + groups, ..., a row ahead with their loads where registers allow it;
+// the weight stays in registers.  THREADS: the most that a block has; BLOCKS of them an SM.
+template <typename T, typename TW, bool VEC, int U, int THREADS, int BLOCKS>
+__global__ void __launch_bounds__(THREADS, BLOCKS)
+    moe_rms_norm_kernel(const __grid_constant__ NormArgs a, int W, int64_t groups, int blocks) {
+  __shared__ float part[2][32];
+  constexpr bool AHEAD = U > 1 && sizeof(T) == 2 && THREADS <= 512;
+  const int H = (int)a.H;
+  const Place p = place(W, groups);
+  Unit<TW> w[U];
+  Unit<T> q[U], q2[U], n[U], n2[U];
+  if (AHEAD && p.t < a.T) load_rows<T, VEC, U>(a, p.t, W, p, n, n2);
+#pragma unroll
+  for (int j = 0; j < U; ++j) w[j] = load_weight<TW, VEC>(a.weight, (j * W + p.w) * 32, p.lane, H);
+  int turn = 0;
+  // (the block's groups take their turns together; one without a row left only joins the sum)
+  for (int64_t t0 = p.t - p.g; t0 < a.T; t0 += groups, turn ^= 1) {
+    const int64_t t = t0 + p.g;
+    const bool ok = t < a.T;
+    if (AHEAD) {
+#pragma unroll
+      for (int j = 0; j < U; ++j) q[j] = n[j], q2[j] = n2[j];
+      if (t + groups < a.T) load_rows<T, VEC, U>(a, t + groups, W, p, n, n2);
+    } else if (ok) {
+      load_rows<T, VEC, U>(a, t, W, p, q, q2);
+    }
+    f2 parts = 0;
+    if (ok) {
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        if (a.residual) q[j] = add_units(q[j], q2[j]);
+        if (a.sum) store_unit<T, VEC>((T*)a.sum + t * a.lds, q[j], (j * W + p.w) * 32, p.lane, H);
+        f2 v[4];
+        widen(q[j], v);
+        parts = add2(parts, squares(v));
+      }
+    }
+    const float ss = row_sum(sum2(parts), W, p, part[turn]);
+    if (!ok) continue;
+    const float r = rsqrt_exact(ss / (float)H + a.eps);
+    if (a.rstd && p.w == 0 && p.lane == 0) a.rstd[t] = r;
 #pragma unroll
     for (int j = 0; j < U; ++j) {
-      float v[8], v2[8];
+      f2 v[4];
       widen(q[j], v);
-      widen(q2[j], v2);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] += v2[i];
-      q[j] = narrow<T>(v);
+      finish_unit<T, TW, VEC>(a, t, (j * W + p.w) * 32, p.lane, blocks, v, w[j], r);
     }
-  }
-  float ss = 0.f;
-#pragma unroll
-  for (int j = 0; j < U; ++j) {
-    float v[8];
-    widen(q[j], v);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fmaf(v[i], v[i], ss);
-  }
-  ss = row_sum(ss, W, p, part);
-  const float r = 1.f / sqrtf(ss / (float)H + a.eps);
-  if (a.rstd && p.ok && p.w == 0 && p.lane == 0) a.rstd[t] = r;
-#pragma unroll
-  for (int j = 0; j < U; ++j) {
-    const int u0 = (j * W + p.w) * 32;
-    if (a.sum && p.ok) store_unit<T, VEC>((T*)a.sum + t * a.lds, q[j], u0, p.lane, H);
-    float v[8];
-    widen(q[j], v);
-    finish_unit<T, VEC>(a, t, p.ok, u0, p.lane, blocks, v, r);
   }
 }
 
 // Rows that a block's registers do not hold: a block a row, which it reads twice.
-template <typename T, bool VEC>
+template <typename T, typename TW, bool VEC>
 __global__ void __launch_bounds__(1024)
     moe_rms_norm_long(const __grid_constant__ NormArgs a, int blocks) {
   __shared__ float part[32];
@@ -236,115 +388,151 @@ __global__ void __launch_bounds__(1024)
   const T* res = a.residual ? (const T*)a.residual + p.t * a.ldr : nullptr;
   T* sum = a.sum ? (T*)a.sum + p.t * a.lds : nullptr;
   auto value = [&](int u0) {
-    Unit<T> q = load_unit<T, VEC>(x, u0, p.lane, H);
-    if (!res) return q;
-    float v[8], v2[8];
-    widen(q, v);
-    widen(load_unit<T, VEC>(res, u0, p.lane, H), v2);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] += v2[i];
-    return narrow<T>(v);
+    const Unit<T> q = load_unit<T, VEC>(x, u0, p.lane, H);
+    return res ? add_units(q, load_unit<T, VEC>(res, u0, p.lane, H)) : q;
   };
-  float ss = 0.f;
+  f2 parts = 0;
   for (int j = 0; j < steps; ++j) {
     const int u0 = (j * 32 + p.w) * 32;
     const Unit<T> q = value(u0);
     if (sum) store_unit<T, VEC>(sum, q, u0, p.lane, H);
-    float v[8], s = 0.f;
+    f2 v[4];
     widen(q, v);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s = fmaf(v[i], v[i], s);
-    ss += s;
+    parts = add2(parts, squares(v));
   }
-  ss = row_sum(ss, 32, p, part);
-  const float r = 1.f / sqrtf(ss / (float)H + a.eps);
+  const float ss = row_sum(sum2(parts), 32, p, part);
+  const float r = rsqrt_exact(ss / (float)H + a.eps);
   if (a.rstd && threadIdx.x == 0) a.rstd[p.t] = r;
   for (int j = 0; j < steps; ++j) {
     const int u0 = (j * 32 + p.w) * 32;
     // a lane reads what it wrote itself (the sum may lie where x or the residual was)
     const Unit<T> q = sum ? load_unit<T, VEC>(sum, u0, p.lane, H) : value(u0);
-    float v[8];
+    f2 v[4];
     widen(q, v);
-    finish_unit<T, VEC>(a, p.t, true, u0, p.lane, blocks, v, r);
+    finish_unit<T, TW, VEC>(a, p.t, u0, p.lane, blocks, v,
+                            load_weight<TW, VEC>(a.weight, u0, p.lane, H), r);
   }
 }
 
 // -------------------------------------------------------------------------------- backward
-// Row groups walk the rows g, g + groups, ...; each keeps its columns' share of dw in registers and
-// leaves it in part_dw[group]; moe_column_sum adds the groups in order, so dw repeats bit for bit.
+constexpr int kGradBlocks = 2;  // of 256 threads, on an SM
+// One unit's terms: n = s r and dn = dy w; what they add to the mean's sum, and to dw.
+__device__ __forceinline__ f2 grad_terms(const f2* d, const f2* s, const f2* w, f2 r, f2 along, f2* dw) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const f2 n = mul2(s[i], r);
+    if (dw) dw[i] = fma2(d[i], n, dw[i]);
+    along = fma2(mul2(d[i], w[i]), n, along);
+  }
+  return along;
+}
+// r (dy w - n mean) + ds of a unit; back: -r times the mean.
+template <typename T>
+__device__ __forceinline__ Unit<T> grad_unit(const f2* d, const f2* s, const f2* w, f2 r, f2 back,
+                                             const f2* ds) {
+  f2 v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[i] = mul2(r, fma2(s[i], back, mul2(d[i], w[i])));
+    if (ds) v[i] = add2(v[i], ds[i]);
+  }
+  return narrow<T>(v);
+}
+
+// A lane's units of a row's dy, s and ds.
+template <typename T, int U>
+struct GradRow {
+  Unit<T> d[U], s[U], e[U];
+  float r;
+};
 template <typename T, bool VEC, int U>
-__global__ void __launch_bounds__(512)
+__device__ __forceinline__ void load_row(const NormGradArgs& a, int64_t t, int W, const Place& p,
+                                         GradRow<T, U>& q) {
+#pragma unroll
+  for (int j = 0; j < U; ++j) {
+    const int u0 = (j * W + p.w) * 32, H = (int)a.H;
+    q.d[j] = load_unit<T, VEC>((const T*)a.dy + t * a.lddy, u0, p.lane, H);
+    q.s[j] = load_unit<T, VEC>((const T*)a.s + t * a.lds, u0, p.lane, H);
+    if (a.dsum) q.e[j] = load_unit<T, VEC>((const T*)a.dsum + t * a.ldds, u0, p.lane, H);
+  }
+  q.r = __ldg(a.rstd + t);
+}
+
+// Row groups walk the rows g, g + groups, ..., a row ahead with their loads; each keeps its columns'
+// share of dw in registers and leaves it in part_dw[group]; moe_column_sum adds the groups in order,
+// so dw repeats bit for bit.
+template <typename T, typename TW, bool VEC, int U, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS == 256 ? kGradBlocks : 1)
     moe_rms_norm_backward_kernel(const __grid_constant__ NormGradArgs a, int W, int groups) {
-  __shared__ float part[16];
+  __shared__ float part[2][16];
   const int H = (int)a.H;
   const Place p = place(W, groups);
-  float dw[U][8];
+  f2 dw[U][4];
+  Unit<TW> qw[U];
 #pragma unroll
-  for (int j = 0; j < U; ++j)
+  for (int j = 0; j < U; ++j) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) dw[j][i] = 0.f;
-  // (the block's groups take their turns together; one without a row left works on row 0 for nothing)
-  const int64_t first = (int64_t)blockIdx.x * (blockDim.x / (32 * W));
-  for (int64_t t0 = first; t0 < a.T; t0 += groups) {
-    const bool ok = p.ok && t0 + p.g < a.T;
-    const int64_t t = ok ? t0 + p.g : 0;
-    Unit<T> qd[U], qs[U], qa[U];
-#pragma unroll
-    for (int j = 0; j < U; ++j) {
-      const int u0 = (j * W + p.w) * 32;
-      qd[j] = load_unit<T, VEC>((const T*)a.dy + t * a.lddy, u0, p.lane, H);
-      qs[j] = load_unit<T, VEC>((const T*)a.s + t * a.lds, u0, p.lane, H);
-      if (a.dsum) qa[j] = load_unit<T, VEC>((const T*)a.dsum + t * a.ldds, u0, p.lane, H);
+    for (int i = 0; i < 4; ++i) dw[j][i] = 0;
+    qw[j] = load_weight<TW, VEC>(a.weight, (j * W + p.w) * 32, p.lane, H);
+  }
+  // (the block's groups take their turns together; one without a row left only joins the sum)
+  constexpr bool AHEAD = sizeof(T) == 2;  // (two rows of FP32 would spill)
+  GradRow<T, U> q, next;
+  if (AHEAD && p.t < a.T) load_row<T, VEC, U>(a, p.t, W, p, next);
+  int turn = 0;
+  for (int64_t t0 = p.t - p.g; t0 < a.T; t0 += groups, turn ^= 1) {
+    const int64_t t = t0 + p.g;
+    if (AHEAD) {
+      q = next;
+      if (t + groups < a.T) load_row<T, VEC, U>(a, t + groups, W, p, next);
+    } else if (t < a.T) {
+      load_row<T, VEC, U>(a, t, W, p, q);
     }
-    const float r = a.rstd[t];
-    float along = 0.f;
+    const f2 r2 = pack(q.r, q.r);
+    f2 sum = 0;
+    if (t < a.T) {
 #pragma unroll
-    for (int j = 0; j < U; ++j) {
-      float d[8], s[8], w[8];
-      widen(qd[j], d);
-      widen(qs[j], s);
-      load_weight<T, VEC>(a.weight, a.w32, (j * W + p.w) * 32, p.lane, H, w);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float n = s[i] * r;
-        if (ok) dw[j][i] = fmaf(d[i], n, dw[j][i]);
-        along = fmaf(d[i] * w[i], n, along);
+      for (int j = 0; j < U; ++j) {
+        f2 d[4], s[4], w[4];
+        widen(q.d[j], d);
+        widen(q.s[j], s);
+        widen(qw[j], w);
+        sum = grad_terms(d, s, w, r2, sum, dw[j]);
       }
     }
     if (!a.dx) continue;
-    along = row_sum(along, W, p, part) / (float)H;
+    const float along = row_sum(sum2(sum), W, p, part[turn]) / (float)H;
+    if (t >= a.T) continue;
+    const f2 back = pack(-q.r * along, -q.r * along);
 #pragma unroll
     for (int j = 0; j < U; ++j) {
-      const int u0 = (j * W + p.w) * 32;
-      float d[8], s[8], w[8], v[8];
-      widen(qd[j], d);
-      widen(qs[j], s);
-      load_weight<T, VEC>(a.weight, a.w32, u0, p.lane, H, w);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = r * (d[i] * w[i] - s[i] * r * along);
-      if (a.dsum) {
-        float e[8];
-        widen(qa[j], e);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] += e[i];
-      }
-      if (ok) store_unit<T, VEC>((T*)a.dx + t * a.lddx, narrow<T>(v), u0, p.lane, H);
+      f2 d[4], s[4], w[4], e[4];
+      widen(q.d[j], d);
+      widen(q.s[j], s);
+      widen(qw[j], w);
+      if (a.dsum) widen(q.e[j], e);
+      store_unit<T, VEC>((T*)a.dx + t * a.lddx,
+                         grad_unit<T>(d, s, w, r2, back, a.dsum ? e : nullptr),
+                         (j * W + p.w) * 32, p.lane, H);
     }
   }
-  if (!a.dweight || !p.ok) return;
+  if (!a.dweight) return;
   float* mine = a.part_dw + p.t * (int64_t)a.H;
 #pragma unroll
   for (int j = 0; j < U; ++j)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int c = column<VEC>((j * W + p.w) * 32, p.lane, i);
-      if (c < H) mine[c] = dw[j][i];
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = unpack(dw[j][i]);
+      const int c = column<VEC>((j * W + p.w) * 32, p.lane, 2 * i);
+      const int c1 = column<VEC>((j * W + p.w) * 32, p.lane, 2 * i + 1);
+      if (c < H) mine[c] = f.x;
+      if (c1 < H) mine[c1] = f.y;
     }
 }
 
 // Longer rows: dx by a block a row that reads its row twice; dw's shares by blocks of 256 columns and
 // a run of rows.
-template <typename T, bool VEC>
+template <typename T, typename TW, bool VEC>
 __global__ void __launch_bounds__(1024)
     moe_rms_norm_backward_long(const __grid_constant__ NormGradArgs a) {
   __shared__ float part[32];
@@ -353,33 +541,26 @@ __global__ void __launch_bounds__(1024)
   const T* dy = (const T*)a.dy + p.t * a.lddy;
   const T* s = (const T*)a.s + p.t * a.lds;
   const float r = a.rstd[p.t];
-  float along = 0.f;
+  f2 sum = 0;
   for (int j = 0; j < steps; ++j) {
     const int u0 = (j * 32 + p.w) * 32;
-    float d[8], h[8], w[8], sum = 0.f;
+    f2 d[4], h[4], w[4];
     widen(load_unit<T, VEC>(dy, u0, p.lane, H), d);
     widen(load_unit<T, VEC>(s, u0, p.lane, H), h);
-    load_weight<T, VEC>(a.weight, a.w32, u0, p.lane, H, w);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) sum = fmaf(d[i] * w[i], h[i] * r, sum);
-    along += sum;
+    widen(load_weight<TW, VEC>(a.weight, u0, p.lane, H), w);
+    sum = add2(sum, grad_terms(d, h, w, pack(r, r), 0, nullptr));
   }
-  along = row_sum(along, 32, p, part) / (float)H;
+  const float along = row_sum(sum2(sum), 32, p, part) / (float)H;
+  const f2 back = pack(-r * along, -r * along);
   for (int j = 0; j < steps; ++j) {
     const int u0 = (j * 32 + p.w) * 32;
-    float d[8], h[8], w[8], v[8];
+    f2 d[4], h[4], w[4], e[4];
     widen(load_unit<T, VEC>(dy, u0, p.lane, H), d);
     widen(load_unit<T, VEC>(s, u0, p.lane, H), h);
-    load_weight<T, VEC>(a.weight, a.w32, u0, p.lane, H, w);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = r * (d[i] * w[i] - h[i] * r * along);
-    if (a.dsum) {
-      float e[8];
-      widen(load_unit<T, VEC>((const T*)a.dsum + p.t * a.ldds, u0, p.lane, H), e);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] += e[i];
-    }
-    store_unit<T, VEC>((T*)a.dx + p.t * a.lddx, narrow<T>(v), u0, p.lane, H);
+    widen(load_weight<TW, VEC>(a.weight, u0, p.lane, H), w);
+    if (a.dsum) widen(load_unit<T, VEC>((const T*)a.dsum + p.t * a.ldds, u0, p.lane, H), e);
+    store_unit<T, VEC>((T*)a.dx + p.t * a.lddx,
+                       grad_unit<T>(d, h, w, pack(r, r), back, a.dsum ? e : nullptr), u0, p.lane, H);
   }
 }
 template <typename T>
@@ -395,21 +576,22 @@ __global__ void __launch_bounds__(256)
 }
 
 // out[c] = sum over groups of part[group][c], in a fixed order: a block takes 32 columns, its warps
-// every eighth group each.
-__global__ void __launch_bounds__(256)
+// every 32nd group each.
+__global__ void __launch_bounds__(1024)
     moe_column_sum(const float* __restrict__ part, int groups, int64_t H, float* __restrict__ out) {
-  __shared__ float s[8][32];
+  __shared__ float s[32][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t c = (int64_t)blockIdx.x * 32 + lane;
   float v = 0.f;
   if (c < H) {
 #pragma unroll 8
-    for (int g = warp; g < groups; g += 8) v += part[g * H + c];
+    for (int g = warp; g < groups; g += 32) v += part[g * H + c];
   }
   s[warp][lane] = v;
   __syncthreads();
   if (warp == 0 && c < H) {
-    for (int i = 1; i < 8; ++i) v += s[i][lane];
+#pragma unroll 8
+    for (int i = 1; i < 32; ++i) v += s[i][lane];
     out[c] = v;
   }
 }
@@ -418,65 +600,66 @@ bool rows_aligned(const void* p, int64_t ld, size_t size) {
   return !p || (((uintptr_t)p & 15u) == 0 && (ld * (int64_t)size) % 16 == 0);
 }
 
-template <typename T, bool VEC, int U>
-cudaError_t norm_u(const NormArgs& a, int blocks, int W, cudaStream_t s) {
-  const int G = W >= 8 ? 1 : 8 / W;
-  moe_rms_norm_kernel<T, VEC, U>
-      <<<(unsigned)((a.T + G - 1) / G), 32 * W * G, 0, s>>>(a, W, blocks);
-  return cudaGetLastError();
-}
-template <typename T, bool VEC>
+template <typename T, typename TW, bool VEC>
 cudaError_t norm_v(const NormArgs& a, cudaStream_t s) {
-  const int64_t blocks = mx8::blocks_of(a.H), warps = (blocks + 7) / 8;  // warps at a unit a lane
   constexpr int U = kUnits<T>;
+  const int64_t blocks = mx8::blocks_of(a.H), warps = (blocks + 7) / 8;  // warps at a unit a lane
   if (warps > 32 * U) {
-    moe_rms_norm_long<T, VEC><<<(unsigned)a.T, 1024, 0, s>>>(a, (int)blocks);
+    moe_rms_norm_long<T, TW, VEC><<<(unsigned)a.T, 1024, 0, s>>>(a, (int)blocks);
     return cudaGetLastError();
   }
   // Few rows: a unit a lane, for latency.  Many: U, for bytes in flight with fewer threads.
-  if (warps <= 32 && a.T * warps <= 152 * 16) return norm_u<T, VEC, 1>(a, (int)blocks, (int)warps, s);
-  return norm_u<T, VEC, U>(a, (int)blocks, (int)((warps + U - 1) / U), s);
+  const bool few = warps <= 32 && a.T * warps <= 152 * 16;
+  const int W = few ? (int)warps : (int)((warps + U - 1) / U), G = W >= 8 ? 1 : 8 / W;
+  const auto kern = few       ? moe_rms_norm_kernel<T, TW, VEC, 1, 1024, 1>
+                    : W <= 8  ? moe_rms_norm_kernel<T, TW, VEC, U, 256, kNormBlocks<T>>
+                    : W <= 16 ? moe_rms_norm_kernel<T, TW, VEC, U, 512, 1>
+                              : moe_rms_norm_kernel<T, TW, VEC, U, 1024, 1>;
+  const int64_t all = (a.T + G - 1) / G, most = W <= 8 ? 152 * kNormBlocks<T> : 152;
+  const int64_t grid = few || all < most ? all : most;
+  kern<<<(unsigned)grid, 32 * W * G, 0, s>>>(a, W, grid * G, (int)blocks);
+  return cudaGetLastError();
 }
 template <typename T>
 cudaError_t norm_t(const NormArgs& a, cudaStream_t s) {
   const bool vec = rows_aligned(a.x, a.ldx, sizeof(T)) && rows_aligned(a.residual, a.ldr, sizeof(T)) &&
                    rows_aligned(a.sum, a.lds, sizeof(T)) && rows_aligned(a.y, a.ldy, sizeof(T)) &&
                    rows_aligned(a.weight, 0, 4);
-  return vec ? norm_v<T, true>(a, s) : norm_v<T, false>(a, s);
+  if (a.w32) return vec ? norm_v<T, float, true>(a, s) : norm_v<T, float, false>(a, s);
+  return vec ? norm_v<T, T, true>(a, s) : norm_v<T, T, false>(a, s);
 }
 
-// W warps a row and the number of row groups whose shares of dw the workspace holds.
+// U units a lane and W warps a row; the number of row groups whose shares of dw the workspace holds.
 struct GradPlan {
-  int W, G, groups;
-  bool stays;  // a row fits its warps' registers
+  int U, W, G, groups;  // U = 0: a row does not fit its warps' registers
 };
-GradPlan grad_plan(int64_t T, int64_t H, int U) {
+GradPlan grad_plan(int64_t T, int64_t H) {
   GradPlan p;
   const int64_t warps = (H + 255) / 256;  // at a unit a lane
-  p.stays = warps <= 16 * U;
-  p.W = p.stays ? (int)((warps + U - 1) / U) : 1;
+  p.U = warps <= 32 ? 2 : 0;  // two of them, and those of the next row, leave two blocks an SM
+  p.W = p.U ? (int)((warps + p.U - 1) / p.U) : 1;
   p.G = p.W >= 8 ? 1 : 8 / p.W;
-  // two blocks an SM of 256 threads (or one of up to 512)
-  const int64_t most = p.stays ? (int64_t)152 * (p.W > 8 ? 1 : 2) * p.G : 64;
+  const int64_t most = p.U ? (int64_t)152 * (p.W > 8 ? 1 : kGradBlocks) * p.G : 64;
   const int64_t even = (T + p.G - 1) / p.G * p.G;
   p.groups = (int)(even < most ? even : most);
   return p;
 }
 
-template <typename T, bool VEC>
+template <typename T, typename TW, bool VEC>
 cudaError_t grad_v(const NormGradArgs& a, cudaStream_t s) {
-  const GradPlan p = grad_plan(a.T, a.H, kUnits<T>);
-  if (p.stays) {
-    moe_rms_norm_backward_kernel<T, VEC, kUnits<T>>
-        <<<(unsigned)(p.groups / p.G), 32 * p.W * p.G, 0, s>>>(a, p.W, p.groups);
+  const GradPlan p = grad_plan(a.T, a.H);
+  if (p.U) {
+    auto kern = p.W <= 8 ? moe_rms_norm_backward_kernel<T, TW, VEC, 2, 256>
+                         : moe_rms_norm_backward_kernel<T, TW, VEC, 2, 512>;
+    kern<<<(unsigned)(p.groups / p.G), 32 * p.W * p.G, 0, s>>>(a, p.W, p.groups);
   } else {
     if (a.dweight)  // first: dx may lie where dy was
       moe_rms_norm_weight_long<T>
           <<<dim3((unsigned)((a.H + 255) / 256), (unsigned)p.groups), 256, 0, s>>>(a, p.groups);
-    if (a.dx) moe_rms_norm_backward_long<T, VEC><<<(unsigned)a.T, 1024, 0, s>>>(a);
+    if (a.dx) moe_rms_norm_backward_long<T, TW, VEC><<<(unsigned)a.T, 1024, 0, s>>>(a);
   }
   if (a.dweight)
-    moe_column_sum<<<(unsigned)((a.H + 31) / 32), 256, 0, s>>>(a.part_dw, p.groups, a.H, a.dweight);
+    moe_column_sum<<<(unsigned)((a.H + 31) / 32), 1024, 0, s>>>(a.part_dw, p.groups, a.H, a.dweight);
   return cudaGetLastError();
 }
 template <typename T>
@@ -484,7 +667,8 @@ cudaError_t grad_t(const NormGradArgs& a, cudaStream_t s) {
   const bool vec = rows_aligned(a.dy, a.lddy, sizeof(T)) && rows_aligned(a.s, a.lds, sizeof(T)) &&
                    rows_aligned(a.dsum, a.ldds, sizeof(T)) && rows_aligned(a.dx, a.lddx, sizeof(T)) &&
                    rows_aligned(a.weight, 0, 4);
-  return vec ? grad_v<T, true>(a, s) : grad_v<T, false>(a, s);
+  if (a.w32) return vec ? grad_v<T, float, true>(a, s) : grad_v<T, float, false>(a, s);
+  return vec ? grad_v<T, T, true>(a, s) : grad_v<T, T, false>(a, s);
 }
 
 }  // namespace
@@ -498,9 +682,8 @@ cudaError_t launch_rms_norm(const NormArgs& a, int dt, cudaStream_t s) {
   return cudaErrorInvalidValue;
 }
 
-size_t rms_norm_backward_scratch_bytes(int64_t T, int64_t H, int dt) {
-  return T < 1 ? 0 : (size_t)grad_plan(T, H, dt == MOE_F32 ? kUnits<float> : kUnits<__half>).groups *
-                         H * sizeof(float);
+size_t rms_norm_backward_scratch_bytes(int64_t T, int64_t H) {
+  return T < 1 ? 0 : (size_t)grad_plan(T, H).groups * H * sizeof(float);
 }
 
 cudaError_t launch_rms_norm_backward(const NormGradArgs& a, int dt, cudaStream_t s) {

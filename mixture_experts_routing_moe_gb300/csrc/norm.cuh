@@ -33,7 +33,7 @@ struct NormGradArgs {
   float* dweight;
   float* part_dw;        // rms_norm_backward_scratch_bytes() bytes, with dweight
 };
-size_t rms_norm_backward_scratch_bytes(int64_t T, int64_t H, int dt);
+size_t rms_norm_backward_scratch_bytes(int64_t T, int64_t H);
 cudaError_t launch_rms_norm_backward(const NormGradArgs& a, int dt, cudaStream_t s);
 
 }  // namespace moe

@@ -58,7 +58,7 @@ int moe_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t ldr, 
 
 size_t moe_rms_norm_backward_workspace_bytes(int64_t T, int64_t H, int dt) {
   if (check_rows(dt, dt, T, H) != MOE_OK) return 0;
-  return kWsHeader + align_up(rms_norm_backward_scratch_bytes(T, H, dt), 256);
+  return kWsHeader + align_up(rms_norm_backward_scratch_bytes(T, H), 256);
 }
 
 int moe_rms_norm_backward(const void* dy, int64_t lddy, const void* s, int64_t lds,

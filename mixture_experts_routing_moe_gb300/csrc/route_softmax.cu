@@ -14,15 +14,18 @@
 //   weighs at most 1.25e-6 in a sum of 1024 terms (sum p d <= ln E), and that sum by another
 //   (C + 5) 2^-24.
 // Where a margin that the choice rests on is within twice the bound (the last kept group against the
-// best other one, each chosen expert against the next, unless the two have the same logit and bias),
-// or a score is not finite, the warp decides the row again in float64.
+// best other one, each chosen expert against the next, unless the two have the same logit and bias,
+// and the last one against the first that is not tied with it so), or a score is not finite, the warp decides the row again in float64.
 //
-// What bounds it is the issue of instructions: some 600 a row of 256 experts.  Chosen experts come
-// from k rounds of a warp maximum over the lanes' best keys (redux), where the lane that gave the
-// maximum looks for its next best.
+// What bounds it is the issue of integer and FP32 instructions.  With k rounds of a warp maximum,
+// each of which sent the lane that gave it looking for its next best, a row of 256 experts took 1800
+// (16384 rows: 57 us, 25 of them the tail of 32 rows in float64).  So the choice is made among few:
+// the rounds run over the lanes' best alone, which bounds the last choice from below, the experts
+// above that bound (mostly a dozen) go to shared memory, one for each lane, and each counts those
+// before it.  The float64 form keeps a lane's scores in registers, so that its exponentials overlap,
+// and ranks them as 64-bit integers.
 #include "common.cuh"
 #include "launch.h"
-#include "route_sigmoid_core.cuh"
 
 namespace moe {
 namespace {
@@ -90,80 +93,173 @@ __device__ __forceinline__ float largest_chosen(const SoftmaxRoute& a, const T* 
   return value_of(__reduce_max_sync(kAll, key));
 }
 
-// The row's decision in float64.  cs: scratch of E + kMaxGroups doubles.
-template <typename T>
-__device__ __noinline__ void route_row_f64(const SoftmaxRoute& a, int64_t row, float m, double* cs) {
+// Order-preserving map of a double that is not NaN to 64 bits (-0 counts as +0), never 0.
+__device__ __forceinline__ unsigned long long key64_of(double v) {
+  const unsigned long long u = (unsigned long long)__double_as_longlong(v + 0.0);
+  return (u >> 63) ? ~u : (u | 0x8000000000000000ull);
+}
+__device__ __forceinline__ double value64_of(unsigned long long k) {
+  return __longlong_as_double((long long)((k >> 63) ? (k & 0x7FFFFFFFFFFFFFFFull) : ~k));
+}
+// The largest of the lanes' keys.
+__device__ __forceinline__ unsigned long long warp_max64(unsigned long long k) {
+  const uint32_t hi = __reduce_max_sync(kAll, (uint32_t)(k >> 32));
+  const uint32_t lo = __reduce_max_sync(kAll, (uint32_t)(k >> 32) == hi ? (uint32_t)k : 0u);
+  return (unsigned long long)hi << 32 | lo;
+}
+__device__ __forceinline__ uint32_t warp_max(uint32_t k) { return __reduce_max_sync(kAll, k); }
+__device__ __forceinline__ unsigned long long warp_max(unsigned long long k) { return warp_max64(k); }
+
+// b1, b2: the two largest of a lane's keys so far; takes another one.
+template <typename K>
+__device__ __forceinline__ void take_two(K& b1, K& b2, K k) {
+  b2 = max(b2, min(b1, k));
+  b1 = max(b1, k);
+}
+
+// Which of a lane's n experts (from e0 on) are in a kept group, as bits.  key: their scores' keys; F, to_
+// and of_key turn keys into scores and back.  scratch: E keys and kMaxGroups more.  in, out: the keys of
+// the scores of the last kept group and of the best other one.
+template <int C, typename K, typename ToValue, typename ToKey>
+__device__ __forceinline__ unsigned kept_experts(const SoftmaxRoute& a, const K* key, int e0, int n,
+                                                 K* scratch, ToValue value, ToKey key_of_value,
+                                                 K* in, K* out) {
   const int lane = threadIdx.x & 31, gs = a.E / a.G;
+  auto score_key = [&](K b1, K b2) { return key_of_value(group_score(value(b1), value(b2), a.two)); };
+  if (a.lanes) {  // a group is a.lanes whole lanes: each of them has its score
+    K b1 = 0, b2 = 0;
+#pragma unroll
+    for (int i = 0; i < C; ++i) take_two(b1, b2, i < n ? key[i] : (K)0);
+    for (int o = 1; o < a.lanes; o <<= 1) {
+      const K o1 = __shfl_xor_sync(kAll, b1, o), o2 = __shfl_xor_sync(kAll, b2, o);
+      b2 = max(max(b2, o2), min(b1, o1));
+      b1 = max(b1, o1);
+    }
+    const int mine = lane / a.lanes;
+    const K sc = n > 0 ? score_key(b1, b2) : (K)0;
+    int rank = 0;
+    for (int h = 0; h < a.G; ++h) {
+      const K v = __shfl_sync(kAll, sc, h * a.lanes);
+      rank += h < mine ? v >= sc : v > sc;
+    }
+    const bool kept = n > 0 && rank < a.SG;
+    *in = ~warp_max(n > 0 && kept ? ~sc : (K)0);
+    *out = warp_max(kept ? (K)0 : sc);
+    return kept ? (n < 32 ? (1u << n) - 1u : ~0u) : 0u;
+  }
+  K* score = scratch + a.E;
+#pragma unroll
+  for (int i = 0; i < C; ++i)
+    if (i < n) scratch[e0 + i] = key[i];
+  __syncwarp();
+  for (int g = lane; g < a.G; g += 32) {
+    K b1 = 0, b2 = 0;
+    for (int j = 0; j < gs; ++j) take_two(b1, b2, scratch[g * gs + j]);
+    score[g] = score_key(b1, b2);
+  }
+  __syncwarp();
+  unsigned kept[kMaxGroups / 32] = {};
+  K last = 0, best = 0;  // of this lane's: the complement of the least kept, the best other
+#pragma unroll
+  for (int q = 0; q < kMaxGroups / 32; ++q) {
+    const int g = q * 32 + lane;
+    if (q * 32 < a.G) {
+      const K sc = g < a.G ? score[g] : (K)0;
+      int rank = 0;
+      for (int h = 0; h < a.G; ++h) rank += h < g ? score[h] >= sc : score[h] > sc;
+      const bool keep = g < a.G && rank < a.SG;
+      kept[q] = __ballot_sync(kAll, keep);
+      if (keep) last = max(last, ~sc);
+      else best = max(best, sc);
+    }
+  }
+  *in = ~warp_max(last);
+  *out = warp_max(best);
+  unsigned bits = 0;
+  int g = e0 / gs, left = gs - (e0 - g * gs);  // the expert's group, and how many of it are left
+#pragma unroll
+  for (int i = 0; i < C; ++i)
+    if (i < n) {
+      unsigned word = 0;
+#pragma unroll
+      for (int q = 0; q < kMaxGroups / 32; ++q) word = g / 32 == q ? kept[q] : word;
+      bits |= ((word >> (g & 31)) & 1u) << i;
+      if (--left == 0) {
+        left = gs;
+        ++g;
+      }
+    }
+  return bits;
+}
+
+// The next best of the lanes' keys: its key, and its expert's id in every lane; its owner takes it out.
+template <int C, typename K>
+__device__ __forceinline__ int take_best(K* key, K& best, int e0, K* top) {
+  *top = warp_max(best);
+  const int from = __ffs(__ballot_sync(kAll, best == *top)) - 1;  // the lowest lane: the lowest id
+  int id = 0;
+  if ((int)(threadIdx.x & 31) == from) {
+    int at = 0;
+#pragma unroll
+    for (int i = C - 1; i >= 0; --i) at = key[i] == *top ? i : at;
+    best = 0;
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      key[i] = i == at ? (K)0 : key[i];
+      best = max(best, key[i]);
+    }
+    id = e0 + at;
+  }
+  return __shfl_sync(kAll, id, from);
+}
+
+// The row's decision in float64 (m: its largest logit, a number).
+template <typename T, int C>
+__device__ __noinline__ void route_row_f64(const SoftmaxRoute& a, int64_t row, float m,
+                                           unsigned long long* scratch) {
+  typedef unsigned long long K;
+  const int lane = threadIdx.x & 31, e0 = lane * a.per, n = max(0, min(a.per, a.E - e0));
   const T* src = reinterpret_cast<const T*>(a.logits) + row * a.E;
-  double* score = cs + a.E;
-  double z = 0.0;
-  for (int e = lane; e < a.E; e += 32) {
-    cs[e] = exp((double)Dt<T>::to_f(src[e]) - (double)m);
-    z += cs[e];
+  double c[C], z = 0.0;
+#pragma unroll
+  for (int i = 0; i < C; ++i) {
+    c[i] = i < n ? exp((double)Dt<T>::to_f(src[e0 + i]) - (double)m) : 0.0;
+    z += c[i];
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(kAll, z, o);
+  const double inv = 1.0 / z;
   bool nan = false;
-  if (a.bias)
-    for (int e = lane; e < a.E; e += 32) {
-      cs[e] = cs[e] / z + (double)a.bias[e];
-      nan |= cs[e] != cs[e];
-    }
-  // (without a bias the exponentials rank groups as the probabilities do)
+  K key[C];
+#pragma unroll
+  for (int i = 0; i < C; ++i) {
+    if (a.bias && i < n) c[i] = fma(c[i], inv, (double)a.bias[e0 + i]);
+    nan |= c[i] != c[i];
+    key[i] = i < n ? key64_of(c[i]) : 0ull;
+  }
   if (__any_sync(kAll, nan)) {
     for (int r = lane; r < a.k; r += 32) write_slot<T>(a, row, r, r, __int_as_float(0x7FC00000));
     return;
   }
-  __syncwarp();
-  for (int g = lane; g < a.G; g += 32) {
-    double b1 = -INFINITY, b2 = -INFINITY;
-    for (int j = 0; j < gs; ++j) {
-      const double v = cs[g * gs + j];
-      if (v > b1) {
-        b2 = b1;
-        b1 = v;
-      } else if (v > b2) {
-        b2 = v;
-      }
-    }
-    score[g] = group_score(b1, b2, a.two);
+  unsigned keep = n > 0 ? (n < 32 ? (1u << n) - 1u : ~0u) : 0u;
+  if (a.SG < a.G) {
+    K in, out;
+    keep = kept_experts<C>(a, key, e0, n, scratch, value64_of, key64_of, &in, &out);
   }
-  __syncwarp();
-  unsigned kept[kMaxGroups / 32] = {};
+  K best = 0;
 #pragma unroll
-  for (int q = 0; q < kMaxGroups / 32; ++q) {
-    const int g = q * 32 + lane;
-    int rank = 0;
-    if (g < a.G)
-      for (int h = 0; h < a.G; ++h)
-        rank += score[h] > score[g] || (score[h] == score[g] && h < g);
-    kept[q] = __ballot_sync(kAll, g < a.G && rank < a.SG);
-  }
-  // k rounds of a warp maximum over the experts that are kept and not taken yet
-  unsigned open = 0;  // of this lane's experts lane, lane + 32, ...
-  for (int i = 0; lane + 32 * i < a.E; ++i) {
-    const int g = (lane + 32 * i) / gs;
-    unsigned word = 0;
-#pragma unroll
-    for (int q = 0; q < kMaxGroups / 32; ++q) word = g / 32 == q ? kept[q] : word;
-    if ((word >> (g & 31)) & 1u) open |= 1u << i;
+  for (int i = 0; i < C; ++i) {
+    // (without a bias the logits rank the experts, the exponentials only pairs of them)
+    if (!a.bias && i < n) key[i] = key_of(Dt<T>::to_f(src[e0 + i]));
+    if (!((keep >> i) & 1u)) key[i] = 0;
+    best = max(best, key[i]);
   }
   int mine[2] = {0, 0};
   for (int r = 0; r < a.k; ++r) {
-    double bv = -INFINITY;
-    int bi = 0x7FFFFFFF;
-    for (int i = 0; lane + 32 * i < a.E; ++i) {
-      const int e = lane + 32 * i;
-      const double v = a.bias ? cs[e] : (double)Dt<T>::to_f(src[e]);
-      if (((open >> i) & 1u) && (bi == 0x7FFFFFFF || v > bv)) {
-        bv = v;
-        bi = e;
-      }
-    }
-    warp_argmax(bv, bi);
-    if ((bi & 31) == lane) open &= ~(1u << (bi >> 5));
-    if (r == lane) mine[0] = bi;
-    if (r == lane + 32) mine[1] = bi;
+    K top;
+    const int id = take_best<C>(key, best, e0, &top);
+    if (r == lane) mine[0] = id;
+    if (r == lane + 32) mine[1] = id;
   }
   // renormalised weights do not depend on m: the largest chosen logit keeps them from vanishing
   float l[2];
@@ -185,186 +281,192 @@ __device__ __noinline__ void route_row_f64(const SoftmaxRoute& a, int64_t row, f
                     (float)(w[h] / (a.renorm ? sel : z) * (double)a.scale));
 }
 
-// C: registers for a lane's experts, at least a.per
-template <typename T, int C>
+// N values from p on, which is 16-byte aligned.
+template <typename T, int N>
+__device__ __forceinline__ void load_vec(const T* p, float* v) {
+  constexpr int PER = 16 / (int)sizeof(T);
+#pragma unroll
+  for (int i = 0; i < N / PER; ++i) {
+    Vec16<T> q;
+    q.u = ld_nc_v4(p + i * PER);
+    q.to_float(v + i * PER);
+  }
+}
+
+// C: registers for a lane's experts, at least a.per; VEC: a.per == C, in 16-byte vectors
+template <typename T, int C, bool VEC>
 __global__ void __launch_bounds__(kWarps * 32)
-    moe_route_softmax_kernel(const __grid_constant__ SoftmaxRoute a, int vec) {
-  extern __shared__ double soft_smem[];
+    moe_route_softmax_kernel(const __grid_constant__ SoftmaxRoute a) {
+  extern __shared__ unsigned long long soft_smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t row = (int64_t)blockIdx.x * kWarps + warp;
   if (row >= a.T) return;  // whole warps leave
-  double* cs = soft_smem + (size_t)warp * (a.E + kMaxGroups);
+  unsigned long long* scratch = soft_smem + (size_t)warp * (a.E + kMaxGroups);
   const T* src = reinterpret_cast<const T*>(a.logits) + row * a.E;
   const int e0 = lane * a.per, n = max(0, min(a.per, a.E - e0));  // this lane's experts
-  float x[C];
-  if (vec) {  // per == C, whole 16-byte vectors
-    constexpr int PER = 16 / (int)sizeof(T);
+  float x[C], c[C];
 #pragma unroll
-    for (int v = 0; v < (C + PER - 1) / PER; ++v) {
-      Vec16<T> q;
-      q.u = make_uint4(0, 0, 0, 0);
-      if (n > 0) q.u = ld_nc_v4(src + e0 + v * PER);
-#pragma unroll
-      for (int i = 0; i < PER && v * PER + i < C; ++i)
-        x[v * PER + i] = n > 0 ? Dt<T>::to_f(q.e[i]) : -INFINITY;
-    }
+  for (int i = 0; i < C; ++i) x[i] = -INFINITY;
+  if (VEC) {
+    if (n > 0) load_vec<T, C>(src + e0, x);
   } else {
 #pragma unroll
-    for (int i = 0; i < C; ++i) x[i] = i < n ? Dt<T>::to_f(src[e0 + i]) : -INFINITY;
+    for (int i = 0; i < C; ++i)
+      if (i < n) x[i] = Dt<T>::to_f(src[e0 + i]);
   }
-  float m = -INFINITY;
-  bool bad = false;
+  float m = x[0];
 #pragma unroll
-  for (int i = 0; i < C; ++i) {
-    m = fmaxf(m, x[i]);
-    bad |= !(x[i] < INFINITY);  // NaN or +inf
-  }
-  const uint32_t mk = __reduce_max_sync(kAll, key_of(m));
-  m = value_of(mk);
-  if (__any_sync(kAll, bad) || m == -INFINITY) {
-    for (int r = lane; r < a.k; r += 32) write_slot<T>(a, row, r, r, __int_as_float(0x7FC00000));
-    return;
-  }
-  // c: what ranks the experts; -inf past them
-  float z = 0.f, c[C];
+  for (int i = 1; i < C; ++i) m = fmaxf(m, x[i]);
+  m = value_of(warp_max(key_of(m)));
+  float z = 0.f;
 #pragma unroll
   for (int i = 0; i < C; ++i) {
     c[i] = exp_below(x[i], m);
     z += c[i];
   }
   z = warp_sum(z);
+  if (!(z < INFINITY)) {  // a NaN, a +inf or only -inf: NaN
+    for (int r = lane; r < a.k; r += 32) write_slot<T>(a, row, r, r, __int_as_float(0x7FC00000));
+    return;
+  }
   float err = 0.f;
   bool sure = true;
+  uint32_t key[C];  // of what ranks the experts
   if (a.bias) {
     const float inv = 1.f / z;
-    float top = 0.f;
+    float b[C];
+    if (VEC) {
+#pragma unroll
+      for (int i = 0; i < C; ++i) b[i] = 0.f;
+      if (n > 0) load_vec<float, C>(a.bias + e0, b);
+    } else {
+#pragma unroll
+      for (int i = 0; i < C; ++i) b[i] = i < n ? __ldg(a.bias + e0 + i) : 0.f;
+    }
+    uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-      const float b = i < n ? __ldg(a.bias + e0 + i) : 0.f;
-      c[i] = fmaf(c[i], inv, b);
-      if (i < n) top = fmaxf(top, fabsf(c[i]));
-      sure &= fabsf(c[i]) < INFINITY;
+      c[i] = fmaf(c[i], inv, b[i]);
+      top = max(top, __float_as_uint(c[i]) & 0x7FFFFFFFu);
+      key[i] = key_of(c[i]);
     }
-    top = value_of(__reduce_max_sync(kAll, key_of(top)));
-    err = (2.5e-6f + 6.5e-8f * C) * inv + 1.2e-7f * top;
-    sure = __all_sync(kAll, sure);
-  }
-  // keep: whether this lane's experts are in a kept group (bit i: expert i)
-  unsigned keep = n > 0 ? (n < 32 ? (1u << n) - 1u : ~0u) : 0u;
-  const bool by_logit = !a.bias && !a.two;  // groups too
-  if (sure && a.SG < a.G) {
-    float* score = reinterpret_cast<float*>(cs);  // [G], the two scores at the border, then c [E]
-    const int gs = a.E / a.G;
-    if (a.lanes) {  // a group is a.lanes whole lanes
-      float b1 = -INFINITY, b2 = -INFINITY;
+    top = warp_max(top);
+    sure = top < 0x7F800000u;
+    err = (2.5e-6f + 6.5e-8f * C) * inv + 1.2e-7f * __uint_as_float(top);
+  } else {
 #pragma unroll
-      for (int i = 0; i < C; ++i) {
-        const float v = i < n ? (by_logit ? x[i] : c[i]) : -INFINITY;
-        b2 = fmaxf(b2, fminf(b1, v));
-        b1 = fmaxf(b1, v);
-      }
-      for (int o = 1; o < a.lanes; o <<= 1) {
-        const float o1 = __shfl_xor_sync(kAll, b1, o), o2 = __shfl_xor_sync(kAll, b2, o);
-        b2 = fmaxf(fmaxf(b2, o2), fminf(b1, o1));
-        b1 = fmaxf(b1, o1);
-      }
-      if (n > 0 && (lane & (a.lanes - 1)) == 0) score[lane / a.lanes] = group_score(b1, b2, a.two);
+    for (int i = 0; i < C; ++i) key[i] = key_of(x[i]);
+  }
+  unsigned keep = n > 0 ? (n < 32 ? (1u << n) - 1u : ~0u) : 0u;
+  if (sure && a.SG < a.G) {
+    uint32_t in, out;
+    uint32_t* floats = reinterpret_cast<uint32_t*>(scratch);
+    if (a.bias || !a.two) {
+      keep = kept_experts<C>(a, key, e0, n, floats, value_of, key_of, &in, &out);
     } else {
-      float* sc = score + kMaxGroups + 2;
+      uint32_t ekey[C];
+#pragma unroll
+      for (int i = 0; i < C; ++i) ekey[i] = __float_as_uint(c[i]) | 0x80000000u;  // (not negative)
+      keep = kept_experts<C>(a, ekey, e0, n, floats, value_of, key_of, &in, &out);
+    }
+    if (a.bias || a.two) {
+      // sums of two exponentials: 4e-7 of the sum and 2 * 0.37 * 1.8e-7 (d e^-d <= 0.37)
+      const float vi = value_of(in), vo = value_of(out);
+      const float bound = a.bias ? (a.two ? 2.f * err + 1.2e-7f * fabsf(vi) : err)
+                                 : 4e-7f * vi + 1.4e-7f;
+      sure = vi - vo > 2.f * bound;
+    }
+  }
+  uint32_t best = 0;
+#pragma unroll
+  for (int i = 0; i < C; ++i) {
+    key[i] = (keep >> i) & 1u ? key[i] : 0u;
+    best = max(best, key[i]);
+  }
+  // one expert more than is chosen, for the last one's margin
+  const bool more = a.bias && a.k < a.SG * (a.E / a.G);
+  const int rounds = a.k + (more ? 1 : 0);
+  auto tied = [&](int i, int j) {  // the same inputs: the lower id, which is first, is sure to be so
+    return Dt<T>::to_f(src[i]) == Dt<T>::to_f(src[j]) && a.bias[i] == a.bias[j];
+  };
+  int mine[2] = {0, 0}, count = 33;
+  uint32_t least = 1u;
+  if (sure && rounds <= 32) {
+    // `rounds` lanes have an expert at or above the bound, so the last choice is at or above it too
+    uint32_t b = best;
+    for (int r = 0; r < rounds; ++r) {
+      const uint32_t top = warp_max(b);
+      if (top == 0u) break;  // fewer lanes: every kept expert
+      least = r == rounds - 1 ? top : 1u;
+      b = b == top ? 0u : b;
+    }
+    unsigned above = 0;
+#pragma unroll
+    for (int i = 0; i < C; ++i) above |= key[i] >= least ? 1u << i : 0u;
+    const int have = __popc(above);
+    int before = have;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(kAll, before, o);
+      if (lane >= o) before += v;
+    }
+    count = __shfl_sync(kAll, before, 31);
+    if (count <= 32) {
+      // an expert a lane: (key, ~id), so that equal keys rank the lower id first
+      unsigned long long* list = scratch;
+      before -= have;
+      __syncwarp();
 #pragma unroll
       for (int i = 0; i < C; ++i)
-        if (i < n) sc[e0 + i] = by_logit ? x[i] : c[i];
+        if ((above >> i) & 1u)
+          list[before++] = (unsigned long long)key[i] << 32 | (uint32_t)~(e0 + i);
       __syncwarp();
-      for (int g = lane; g < a.G; g += 32) {
-        float b1 = -INFINITY, b2 = -INFINITY;
-        for (int j = 0; j < gs; ++j) {
-          const float v = sc[g * gs + j];
-          b2 = fmaxf(b2, fminf(b1, v));
-          b1 = fmaxf(b1, v);
-        }
-        score[g] = group_score(b1, b2, a.two);
-      }
-    }
-    __syncwarp();
-    unsigned kept[kMaxGroups / 32] = {};
-#pragma unroll
-    for (int q = 0; q < kMaxGroups / 32; ++q) {
-      if (q * 32 >= a.G) break;
-      const int g = q * 32 + lane;
-      const float mine = g < a.G ? score[g] : 0.f;
+      const unsigned long long own = lane < count ? list[lane] : 0ull;
       int rank = 0;
-      for (int h = 0; h < a.G; ++h) {
-        const float v = score[h];
-        rank += v > mine || (v == mine && h < g);
-      }
-      if (g < a.G && rank >= a.SG - 1 && rank <= a.SG) score[kMaxGroups + rank - a.SG + 1] = mine;
-      kept[q] = __ballot_sync(kAll, g < a.G && rank < a.SG);
-    }
-    __syncwarp();
-    if (!by_logit) {
-      const float in = score[kMaxGroups], out = score[kMaxGroups + 1];
-      // sums of two exponentials: 4e-7 of the sum and 2 * 0.37 * 1.8e-7 (d e^-d <= 0.37)
-      const float bound = a.bias ? (a.two ? 2.f * err + 1.2e-7f * fabsf(in) : err)
-                                 : 4e-7f * in + 1.4e-7f;
-      sure = in - out > 2.f * bound;
-    }
-    unsigned word = 0, of_kept = 0;
-    int was = -1;
-#pragma unroll
-    for (int i = 0; i < C; ++i) {
-      if (i < n) {
-        const int g = (e0 + i) / gs;
-        if (g != was) {
-          was = g;
-#pragma unroll
-          for (int q = 0; q < kMaxGroups / 32; ++q) word = g / 32 == q ? kept[q] : word;
+      for (int j = 0; j < count; ++j) rank += list[j] > own;
+      __syncwarp();
+      if (lane < count) list[rank] = own;
+      __syncwarp();
+      const unsigned long long at = lane < count ? list[lane] : 0ull;
+      mine[0] = lane < count ? (int)~(uint32_t)at : 0;
+      if (a.bias) {
+        const int next = __shfl_down_sync(kAll, mine[0], 1);
+        const float v = value_of((uint32_t)(at >> 32)), vn = __shfl_down_sync(kAll, v, 1);
+        const bool clear = lane < count - 1 && v - vn > 2.f * err;
+        const unsigned clears = __ballot_sync(kAll, clear);
+        const unsigned ties = __ballot_sync(kAll, lane < count - 1 && !clear && tied(mine[0], next));
+        const unsigned chosen = (1u << (a.k - 1)) - 1u;  // pairs among the chosen
+        sure = ((clears | ties) & chosen) == chosen;
+        if (more) {
+          // the last one against the rest: those tied with it, and then a clear margin
+          const int end = __ffs(~(ties >> (a.k - 1))) - 1 + a.k - 1;
+          sure = sure && ((clears >> end) & 1u || (end == count - 1 && least == 1u));
         }
-        of_kept |= ((word >> (g & 31)) & 1u) << i;
       }
     }
-    keep = of_kept;
   }
-  // k rounds (and one more for the margin): the lanes' best keys, their maximum, the lowest lane
-  uint32_t key[C];
-#pragma unroll
-  for (int i = 0; i < C; ++i) key[i] = (keep >> i) & 1u ? key_of(a.bias ? c[i] : x[i]) : 0u;
-  auto best_of = [&]() {
-    uint32_t b = 0;
-#pragma unroll
-    for (int i = 0; i < C; ++i) b = max(b, key[i]);
-    return b;
-  };
-  uint32_t best = best_of();
-  const int rounds = a.k + (a.bias && a.k < a.SG * (a.E / a.G) ? 1 : 0);
-  int mine[2] = {0, 0}, last = 0;
-  float before = 0.f;
-  for (int r = 0; r < rounds && sure; ++r) {
-    const uint32_t top = __reduce_max_sync(kAll, best);
-    const int from = __ffs(__ballot_sync(kAll, best == top)) - 1;
-    int id = 0;
-    if (lane == from) {
-      int at = 0;
-#pragma unroll
-      for (int i = C - 1; i >= 0; --i) at = key[i] == top ? i : at;
-#pragma unroll
-      for (int i = 0; i < C; ++i) key[i] = i == at ? 0u : key[i];
-      best = best_of();
-      id = e0 + at;
+  if (sure && count > 32) {  // many slots, or many alike: a round each
+    float last_v = 0.f;
+    int last = 0;
+    const int all = a.SG * (a.E / a.G), end = more ? all : a.k;
+    for (int r = 0; r < end && sure; ++r) {
+      uint32_t top;
+      const int id = take_best<C>(key, best, e0, &top);
+      if (a.bias) {
+        const float v = value_of(top);
+        const bool clear = r > 0 && last_v - v > 2.f * err;
+        if (clear && r >= a.k) break;  // (those tied with the last chosen one have been passed)
+        sure = r == 0 || clear || tied(id, last);
+        last_v = v;
+        last = id;
+      }
+      if (r == lane && r < a.k) mine[0] = id;
+      if (r == lane + 32 && r < a.k) mine[1] = id;
     }
-    id = __shfl_sync(kAll, id, from);
-    if (a.bias) {
-      const float v = value_of(top);
-      if (r > 0 && !(before - v > 2.f * err))  // then only equal inputs are sure: the lower id is first
-        sure = Dt<T>::to_f(src[id]) == Dt<T>::to_f(src[last]) && a.bias[id] == a.bias[last];
-      before = v;
-      last = id;
-    }
-    if (r == lane && r < a.k) mine[0] = id;
-    if (r == lane + 32 && r < a.k) mine[1] = id;
   }
   if (!sure) {
     __syncwarp();
-    route_row_f64<T>(a, row, m, cs);
+    route_row_f64<T, C>(a, row, m, scratch);
     return;
   }
   float w[2] = {0.f, 0.f}, l[2];
@@ -381,11 +483,11 @@ __global__ void __launch_bounds__(kWarps * 32)
 
 template <typename T, int C>
 cudaError_t launch_c(const SoftmaxRoute& a, cudaStream_t s) {
-  const size_t smem = kWarps * (size_t)(a.E + kMaxGroups) * sizeof(double);
-  const int vec = a.per == C && a.E % C == 0 && C * sizeof(T) % 16 == 0 &&
-                  ((uintptr_t)a.logits & 15u) == 0 && a.E * sizeof(T) % 16 == 0;
-  moe_route_softmax_kernel<T, C>
-      <<<(unsigned)((a.T + kWarps - 1) / kWarps), kWarps * 32, smem, s>>>(a, vec);
+  const size_t smem = kWarps * (size_t)(a.E + kMaxGroups) * sizeof(unsigned long long);
+  const bool vec = a.per == C && a.E % C == 0 && C * sizeof(T) % 16 == 0 &&
+                   a.E * sizeof(T) % 16 == 0 && (((uintptr_t)a.logits | (uintptr_t)a.bias) & 15u) == 0;
+  const auto kern = vec ? moe_route_softmax_kernel<T, C, true> : moe_route_softmax_kernel<T, C, false>;
+  kern<<<(unsigned)((a.T + kWarps - 1) / kWarps), kWarps * 32, smem, s>>>(a);
   return cudaGetLastError();
 }
 template <typename T>
