@@ -82,4 +82,5 @@ cudaError_t launch_mx8_gate_up(MxRows a, int64_t rows, MxRows gate, MxRows up,
                                uint8_t* scales, unsigned* status, bool zero_status,
                                cudaStream_t s);
 
+
 }  // namespace moe

@@ -215,13 +215,19 @@ int moe_mx8_forward(const uint8_t* x_codes, const uint8_t* x_scales, const uint3
   unsigned* status = (unsigned*)ws;
   int32_t* offsets = (int32_t*)(b + l.offsets);
   uint32_t* ros = (uint32_t*)(b + l.ros);
-  cudaError_t err = cudaMemsetAsync(status, 0, sizeof(unsigned), s);
-  if (err == cudaSuccess)
-    err = launch_dispatch_map(T, idx, (int)E, top_k, offsets, (uint32_t*)(b + l.tor), ros,
-                              (int32_t*)(b + l.hist), status, s);
-  if (err == cudaSuccess)
-    err = launch_dispatch_block_rows(x_codes, x_scales, T, code_pitch(H), scale_pitch(H), top_k, ros,
-                                     b + l.xc, b + l.xs, s);
+  cudaError_t err;
+  if (R <= kFewSlots) {
+    err = launch_dispatch_few_blocks(x_codes, x_scales, T, code_pitch(H), scale_pitch(H), idx, (int)E,
+                                     top_k, offsets, ros, b + l.xc, b + l.xs, status, s);
+  } else {
+    err = cudaMemsetAsync(status, 0, sizeof(unsigned), s);
+    if (err == cudaSuccess)
+      err = launch_dispatch_map(T, idx, (int)E, top_k, offsets, (uint32_t*)(b + l.tor), ros,
+                                (int32_t*)(b + l.hist), status, s);
+    if (err == cudaSuccess)
+      err = launch_dispatch_block_rows(x_codes, x_scales, T, code_pitch(H), scale_pitch(H), top_k, ros,
+                                       b + l.xc, b + l.xs, s);
+  }
   if (err == cudaSuccess)
     err = launch_mx8_gate_up({b + l.xc, b + l.xs}, R, {gate_codes, gate_scales},
                              {up_codes, up_scales}, offsets, (int)E, (int)I, (int)H, b + l.ac,

@@ -6,7 +6,8 @@
 //
 // A persistent kernel walks tiles (expert, m-tile, n-tile) of 256 columns and 128 rows (a CTA) or
 // 256 rows (a cluster of two CTAs, cta_group::2: each CTA holds 128 of the rows and half of the B
-// rows, so a tile pulls a third fewer bytes through L2).  Roles in each CTA:
+// rows, so a tile pulls a third fewer bytes through L2), or of 64 columns and 128 rows where few rows
+// leave few tiles.  Roles in each CTA:
 //   warp 0      loads, for each K slice (128 bytes a row: 256 values in 4 bits, 128 in 8), the codes
 //               of its A and B rows by TMA into a ring.  For gate/up the B tile holds gate rows 0-63, up rows 0-63, gate
 //               rows 64-127, up rows 64-127 of 128 columns of a.  (Warps 0 and 1 run their loops with
@@ -44,7 +45,8 @@ namespace moe {
 namespace {
 using namespace tc;
 
-constexpr int BM = 128, BN = 256;  // rows of a CTA, columns of a tile
+constexpr int BM = 128;  // rows of a CTA
+constexpr int kWide = 256, kNarrow = 64;  // columns of a tile (BN)
 constexpr int kThreads = 512;
 // Registers of a thread of each warpgroup (the launch gives 128 to each; 72 + 104 + 2 * 168 = 512
 // = 4 * 128 are taken): the epilogue holds 128 accumulator values at once.
@@ -102,20 +104,33 @@ struct Fmt8 {
   }
 };
 
-// CG: CTAs of a tile
-template <typename F, int CG>
+// CG: CTAs of a tile; BN: its columns
+template <typename F, int CG, int BN>
 struct Shape {
-  static constexpr int STAGES = CG == 2 ? 6 : 4;
+  static constexpr int STAGES = BN == kNarrow ? 8 : CG == 2 ? 6 : 4;
+  // Epilogue halves of a tile's columns; of those of a half, the first half is gate's, the other up's.
+  static constexpr int HALVES = BN >= 128 ? 2 : 1, HC = BN / HALVES, GC = HC / 2;
+  // Rows of a copy of A.  Single CTAs, which few rows take, copy the rows that their group has and no
+  // others: with 128 a slice, every CTA asked L2 for the few rows there are at the same time (a token's
+  // 8 experts, H = 2048, I = 768: 1.5 us a slice).
+  static constexpr int A_BOX = CG == 1 && F::CHUNKS == 1 ? 16 : BM;
+  static constexpr int B_CHUNKS = (BN + 127) / 128;  // scale chunks of 128 B rows
   static constexpr int A_BYTES = BM * 128, B_BYTES = BN / CG * 128;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
   // scales of a slice: the chunks of A, then (chunk, row half) of B
-  static constexpr int SF_BYTES = 3 * F::CHUNKS * kScaleChunk;
+  static constexpr int SF_BYTES = (1 + B_CHUNKS) * F::CHUNKS * kScaleChunk;
+  static constexpr int SF_COLS = (1 + B_CHUNKS) * 4;  // columns of tensor memory of 128 values
   static constexpr size_t SMEM = 1024 + (size_t)STAGES * (STAGE_BYTES + SF_BYTES) + kBarBytes +
                                  (kMaxExperts + 4) * sizeof(int) + 8 * kTurnBytes;
 };
-static_assert(Shape<Fmt4, 1>::SMEM <= 232448 && Shape<Fmt4, 2>::SMEM <= 232448 &&
-                  Shape<Fmt8, 1>::SMEM <= 232448 && Shape<Fmt8, 2>::SMEM <= 232448,
+static_assert(Shape<Fmt4, 1, kWide>::SMEM <= 232448 && Shape<Fmt4, 2, kWide>::SMEM <= 232448 &&
+                  Shape<Fmt8, 1, kWide>::SMEM <= 232448 && Shape<Fmt8, 2, kWide>::SMEM <= 232448 &&
+                  Shape<Fmt8, 1, kNarrow>::SMEM <= 232448,
               "shared memory of a CTA");
+static_assert(kScaleCol + 8 * Shape<Fmt8, 1, kNarrow>::SF_COLS <= kTmemCols &&
+                  kScaleCol + 6 * Fmt4::CHUNKS * Shape<Fmt4, 2, kWide>::SF_COLS <= kTmemCols,
+              "tensor memory");
+static_assert((2 * 8 + 3 + 1) * 8 <= kBarBytes, "barriers");
 
 struct Params {
   const int32_t* offsets;  // null: one group of `rows` rows
@@ -191,18 +206,18 @@ __device__ __forceinline__ void store_row(T* row, const float* v, int col0, int 
       if (col0 + i < N) row[col0 + i] = Dt<T>::from_f(v[i]);
   }
 }
-// A warp's 32 rows x 128 columns of an output whose rows are not 16-byte aligned (out: row 0, the
+// A warp's 32 rows x 32 CH columns of an output whose rows are not 16-byte aligned (out: row 0, the
 // warp's first column; rows, cols: how many of them exist): 32 bytes of each row at a time go through
 // shared memory, so that a store's lanes write neighbouring elements of two (f32: four) rows.  With
 // each lane writing its own row, element by element, 5467 x 6895 f16 with K = 512 took 342 us; this
 // way, 74.  (The pair kernel spills nine registers for it.)
-template <typename T>
-__device__ __forceinline__ void store_turned(T* out, int64_t pitch, const uint32_t (&acc)[4][32],
+template <typename T, int CH>
+__device__ __forceinline__ void store_turned(T* out, int64_t pitch, const uint32_t (&acc)[CH][32],
                                              int rows, int cols, uint8_t* turn, int lane) {
   constexpr int CW = 32 / sizeof(T), RW = 32 / CW;  // columns of a piece, rows of a store
   const int rsub = lane / CW, col = lane % CW;
 #pragma unroll
-  for (int c0 = 0; c0 < 128; c0 += CW) {
+  for (int c0 = 0; c0 < 32 * CH; c0 += CW) {
     if (c0 < cols) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -226,35 +241,17 @@ __device__ __forceinline__ void store_turned(T* out, int64_t pitch, const uint32
   }
 }
 
-// silu(g) u to a few units of FP32 (quantising it moves a value near a border between codes by a whole
-// step), for any g that FP32 holds.  With e = exp(-|g| / 2), 1 / (1 + exp(-g)) is 1 / (1 + e^2) for
-// g >= 0 and e^2 / (1 + e^2) below: the divisor stays in [1, 2], and g e e leaves the normal numbers
-// only where silu(g) does.  e is a power of two of h = -|g| log2(e) / 2, whose rounding (and that of the
-// constant) l makes up for.  (expf and a division take twice the instructions, more than the MMAs of a
-// tile can hide: prefill experts 976 -> 1248 us, decode 54 -> 68.)
-__device__ __forceinline__ float silu_mul(float g, float u) {
-  const float x = fabsf(g);
-  const float c = -0.72134752f, c_lo = -9.6298e-9f;  // -log2(e) / 2
-  const float h = x * c, l = fmaf(x, c_lo, fmaf(x, c, -h));
-  float e, r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(h));
-  e = fmaf(e * l, 0.69314718f, e);  // 2^(h + l), l at most 2^-18
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fmaf(e, e, 1.f)));
-  const float m = g < 0.f ? e : 1.f;
-  return g * m * m * r * u;
-}
-
 // What the epilogue writes: the blocks of a; rows that are 16-byte aligned; other rows.
 enum Kind { kGateUp, kRows, kTurned };
 
-template <typename F, int CG, int KIND, typename T>
+template <typename F, int CG, int BN, int KIND, typename T>
 __global__ void __launch_bounds__(kThreads, 1)
     moe_mx_gemm(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
                  const __grid_constant__ CUtensorMap mapB2, const Params p) {
   constexpr bool GATEUP = KIND == kGateUp;
-  using S = Shape<F, CG>;
+  using S = Shape<F, CG, BN>;
   constexpr int STAGES = S::STAGES, STAGE_BYTES = S::STAGE_BYTES, SF_BYTES = S::SF_BYTES;
-  constexpr int CHUNKS = F::CHUNKS;
+  constexpr int CHUNKS = F::CHUNKS, B_CHUNKS = S::B_CHUNKS, HC = S::HC, GC = S::GC;
   constexpr int GROUP = 8 / CHUNKS;  // slices whose scales are 32 bytes of a row
   extern __shared__ uint8_t mx_smem_raw[];
   const uint32_t raw = smem_u32(mx_smem_raw);
@@ -279,11 +276,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (p.zero_status && blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(full_bar(s), 1 + 3 * CG);  // the producer's expect_tx and the scale warps
+      mbar_init(full_bar(s), 1 + (1 + B_CHUNKS) * CG);  // the producer's expect_tx and the scale warps
       mbar_init(empty_bar(s), 1);
     }
     mbar_init(tfull, 1);
-    mbar_init(tempty, 8 * CG);
+    mbar_init(tempty, 4 * S::HALVES * CG);
     mbar_init(drain_bar, 1);
     *abort_f = 0;
     fence_mbar_init();
@@ -360,13 +357,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             else tma_load_2d(dst, m, fb, kb * 128, row, pol);
           };
           if (elect_one()) {
-            if (leader) mbar_expect_tx(full_bar(stage), CG * STAGE_BYTES);
-            load(sa, &mapA, x.r0);
+            const int a_rows = S::A_BOX == BM ? BM : min(BM, x.r1 - x.r0);
+            const int boxes = (a_rows + S::A_BOX - 1) / S::A_BOX;
+            if (leader)
+              mbar_expect_tx(full_bar(stage),
+                             CG * (S::B_BYTES + boxes * S::A_BOX * 128));
+            for (int i = 0; i < boxes; ++i) load(sa + i * S::A_BOX * 128, &mapA, x.r0 + i * S::A_BOX);
             if (GATEUP) {
 #pragma unroll
-              for (int h = 0; h < 2 / CG; ++h) {
-                load(sb + h * 128 * 128, &mapB, b_row + h * 64);
-                load(sb + h * 128 * 128 + 64 * 128, &mapB2, b_row + h * 64);
+              for (int h = 0; h < S::HALVES / CG; ++h) {
+                load(sb + h * HC * 128, &mapB, b_row + h * GC);
+                load(sb + h * HC * 128 + GC * 128, &mapB2, b_row + h * GC);
               }
             } else {
               load(sb, &mapB, b_row);
@@ -420,17 +421,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t da = make_sdesc(sa), db = make_sdesc(sb);
           // a slot of columns for each stage, so that the copies need not wait for the MMAs of the
           // slice before: 128 values (c) take 4 columns for A and 8 for the two halves of B
-          const uint32_t cols = tmem + kScaleCol + stage * 12 * CHUNKS;
+          const uint32_t cols = tmem + kScaleCol + stage * S::SF_COLS * CHUNKS;
           if (elect_one()) {
 #pragma unroll
             for (int c = 0; c < CHUNKS; ++c) {
-              copy(cols + c * 12, sf + c * kScaleChunk);
-              copy(cols + c * 12 + 4, sf + (CHUNKS + 2 * c) * kScaleChunk);
-              copy(cols + c * 12 + 8, sf + (CHUNKS + 1 + 2 * c) * kScaleChunk);
+              copy(cols + c * S::SF_COLS, sf + c * kScaleChunk);
+#pragma unroll
+              for (int h = 0; h < B_CHUNKS; ++h)
+                copy(cols + c * S::SF_COLS + 4 + 4 * h,
+                     sf + (CHUNKS + B_CHUNKS * c + h) * kScaleChunk);
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const uint32_t ca = cols + F::chunk_of(k) * 12, cb = ca + 4;
+              const uint32_t ca = cols + F::chunk_of(k) * S::SF_COLS, cb = ca + 4;
               F::template mma<CG>(tmem, da + 2u * k, db + 2u * k, F::idesc(BM * CG, BN, k), ca, cb,
                                   (kb | k) != 0);
             }
@@ -464,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int align = p.scales_align;
     int stage = 0;
     uint32_t phase = 0;
-    bool stop = part == 3;
+    bool stop = part > B_CHUNKS;
     // groups of slices over all of this CTA's tiles; the next group's words are loaded ahead
     const int groups = (p.KB + GROUP - 1) / GROUP;
     uint32_t next[4][8];
@@ -475,12 +478,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; j < 4; ++j) {
         const int i = 32 * j + lane;
         if (part == 0) {
-          src[j] = p.a_scales + min((int64_t)x.r0 + i, p.rows - 1) * pitch;
+          src[j] = p.a_scales + min((int64_t)x.r0 + i, (S::A_BOX == BM ? p.rows : x.r1) - 1) * pitch;
         } else {
           const int h = part - 1;
-          int n = GATEUP ? x.n * (BN / 2) + h * 64 + (i & 63) : x.n * BN + h * 128 + i;
+          // (of a narrow tile's chunk, rows 64 to 127 are not used)
+          int n = GATEUP ? x.n * (BN / 2) + h * GC + i % GC : x.n * BN + h * 128 + i;
           n = min(n, p.N - 1);
-          const uint8_t* b = GATEUP && j >= 2 ? p.b2_scales : p.b_scales;
+          const uint8_t* b = GATEUP && i % HC >= GC ? p.b2_scales : p.b_scales;
           src[j] = b + ((int64_t)x.e * p.N + n) * pitch;
         }
       }
@@ -495,9 +499,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       point(first);
       load_group(0);
     }
-    // chunk (c, half) of B is chunk CHUNKS + 2 c + half of a slice, chunk c of A is chunk c
+    // chunk (c, half) of B is chunk CHUNKS + B_CHUNKS c + half of a slice, chunk c of A is chunk c
     const uint32_t dst = sf_base + (part == 0 ? 0 : CHUNKS - 1 + part) * kScaleChunk + lane * 16;
-    const uint32_t chunk_step = (part == 0 ? 1 : 2) * kScaleChunk;
+    const uint32_t chunk_step = (part == 0 ? 1 : B_CHUNKS) * kScaleChunk;
     for (int t = first; t < total && !stop; t += step) {
       for (int group = 0; group < groups && !stop; ++group) {
         uint32_t now[4][8];
@@ -553,40 +557,40 @@ __global__ void __launch_bounds__(kThreads, 1)
     set_max_regs_inc<kRegsEpilogue>();
     const int q = warp & 3, h = warp >= 12;  // lane quarter, column half
     uint32_t tphase = 0;
-    for (int t = first; t < total; t += step) {
+    for (int t = h < S::HALVES ? first : total; t < total; t += step) {
       const Tile x = tile_of(t);
       const bool ok = wait_bounded(tfull, tphase, abort_f, p.status);
       if (!__all_sync(0xFFFFFFFFu, ok)) break;
       tphase ^= 1u;
       tc_fence_after();
-      uint32_t acc[4][32];
-      const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + h * 128;
+      uint32_t acc[HC / 32][32];
+      const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + h * HC;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32(taddr + c * 32, acc[c]);
+      for (int c = 0; c < HC / 32; ++c) tmem_ld32(taddr + c * 32, acc[c]);
       tmem_wait_ld();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) arrive_leader(tempty);
       const int row = x.r0 + q * 32 + lane;
       if (KIND == kTurned) {
-        const int col0 = x.n * BN + h * 128;
+        const int col0 = x.n * BN + h * HC;
         store_turned((T*)p.out + (int64_t)(x.r0 + q * 32) * p.N + col0, p.N, acc,
                      x.r1 - x.r0 - q * 32, p.N - col0, turn + (warp - 8) * kTurnBytes, lane);
       } else if (row < x.r1) {
         if (GATEUP) {
-          // columns 0-63 gate, 64-127 up of a's columns n * 128 + h * 64 ..: two blocks
+          // GC columns gate, then GC up, of a's columns n * BN / 2 + h * GC ..: GC / 32 blocks
           const int64_t cp = F::code_pitch(p.N), sp = mx4::scale_pitch(p.N);
           const int blocks = (int)mx4::blocks_of(p.N);
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int blk = x.n * 4 + h * 2 + c;
+          for (int c = 0; c < GC / 32; ++c) {
+            const int blk = x.n * (BN / 64) + h * (GC / 32) + c;
             if (blk >= blocks) continue;
             float a[32];
             uint32_t top = 0;
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
-              const float g = __uint_as_float(acc[c][i]), u = __uint_as_float(acc[c + 2][i]);
-              a[i] = blk * 32 + i < p.N ? silu_mul(g, u) : 0.f;
+              const float g = __uint_as_float(acc[c][i]), u = __uint_as_float(acc[c + GC / 32][i]);
+              a[i] = blk * 32 + i < p.N ? mx4::silu_mul(g, u) : 0.f;
               top = max(top, __float_as_uint(a[i]) & 0x7FFFFFFFu);
             }
             const uint32_t b = F::block(a, top, p.codes + row * cp + blk * F::CODE_BYTES);
@@ -597,8 +601,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           T* orow = (T*)p.out + (int64_t)row * p.N;
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            store_row(orow, reinterpret_cast<const float*>(acc[c]), x.n * BN + h * 128 + c * 32,
+          for (int c = 0; c < HC / 32; ++c)
+            store_row(orow, reinterpret_cast<const float*>(acc[c]), x.n * BN + h * HC + c * 32,
                       p.N, p.store);
         }
       }
@@ -624,12 +628,13 @@ int sm_count(cudaError_t* err) {
   return sms;
 }
 
-template <typename F, int CG, int KIND, typename T>
+template <typename F, int CG, int BN, int KIND, typename T>
 cudaError_t launch_cg(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& b2,
                       const Params& p, int sms, cudaStream_t s) {
-  auto kern = moe_mx_gemm<F, CG, KIND, T>;
+  using S = Shape<F, CG, BN>;
+  auto kern = moe_mx_gemm<F, CG, BN, KIND, T>;
   cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)Shape<F, CG>::SMEM);
+                                         (int)S::SMEM);
   if (err != cudaSuccess) return err;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -638,7 +643,7 @@ cudaError_t launch_cg(const CUtensorMap& a, const CUtensorMap& b, const CUtensor
   attr[0].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = Shape<F, CG>::SMEM;
+  cfg.dynamicSmemBytes = S::SMEM;
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = CG == 2 ? 1 : 0;
@@ -655,14 +660,28 @@ cudaError_t launch_cg(const CUtensorMap& a, const CUtensorMap& b, const CUtensor
 // 512 229 / 219.
 bool use_pairs(int64_t rows, int E) { return rows >= (int64_t)160 * E; }
 
+template <typename F>
+int a_box(int64_t rows, int E) {
+  return use_pairs(rows, E) ? Shape<F, 2, kWide>::A_BOX : Shape<F, 1, kWide>::A_BOX;
+}
+
+// Narrow tiles (in 8 bits) where the wide ones of the experts that rows can reach would not give every
+// SM one.
+template <typename F>
+bool use_narrow(int64_t rows, int E, int64_t columns, int sms) {
+  if (F::CHUNKS != 1) return false;
+  const int64_t experts = rows < E ? rows : E;
+  return !use_pairs(rows, E) && rows <= BM && experts * ((columns + kWide - 1) / kWide) < sms;
+}
+
 template <typename F, int KIND, typename T>
 cudaError_t launch(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& b2,
-                   const Params& p, cudaStream_t s) {
-  cudaError_t err;
-  const int sms = sm_count(&err);
-  if (err != cudaSuccess) return err;
-  return use_pairs(p.rows, p.E) ? launch_cg<F, 2, KIND, T>(a, b, b2, p, sms, s)
-                                : launch_cg<F, 1, KIND, T>(a, b, b2, p, sms, s);
+                   const Params& p, int bn, int sms, cudaStream_t s) {
+  if constexpr (F::CHUNKS == 1) {
+    if (bn == kNarrow) return launch_cg<F, 1, kNarrow, KIND, T>(a, b, b2, p, sms, s);
+  }
+  return use_pairs(p.rows, p.E) ? launch_cg<F, 2, kWide, KIND, T>(a, b, b2, p, sms, s)
+                                : launch_cg<F, 1, kWide, KIND, T>(a, b, b2, p, sms, s);
 }
 
 // Of 32, 16 and 4, the largest that divides the pitch and the three bases.
@@ -692,11 +711,15 @@ cudaError_t launch_product(MxRows a, int64_t rows, MxRows b, const int32_t* offs
                            int K, void* out, int odt, unsigned* status, bool zero_status,
                            cudaStream_t s) {
   CUtensorMap ma, mb;
+  cudaError_t err;
+  const int sms = sm_count(&err);
+  if (err != cudaSuccess) return err;
+  const int bn = use_narrow<F>(rows, E, N, sms) ? kNarrow : kWide;
   const int64_t pitch = F::code_pitch(K);
-  if (!make_map_bytes(&ma, a.codes, pitch, rows, BM) ||
-      !make_map_bytes(&mb, b.codes, pitch, (int64_t)E * N, use_pairs(rows, E) ? BN / 2 : BN))
+  if (!make_map_bytes(&ma, a.codes, pitch, rows, a_box<F>(rows, E)) ||
+      !make_map_bytes(&mb, b.codes, pitch, (int64_t)E * N, use_pairs(rows, E) ? bn / 2 : bn))
     return cudaErrorInvalidValue;
-  Params p = make_params<F>(a, rows, offsets, E, N, K, BN, status);
+  Params p = make_params<F>(a, rows, offsets, E, N, K, bn, status);
   p.b_scales = b.scales;
   p.scales_align = scales_align(p.scale_pitch, a.scales, b.scales, b.scales);
   p.out = out;
@@ -706,14 +729,14 @@ cudaError_t launch_product(MxRows a, int64_t rows, MxRows b, const int32_t* offs
   const bool turned = p.store < 16;
   switch (odt) {
     case MOE_F32:
-      return turned ? launch<F, kTurned, float>(ma, mb, mb, p, s)
-                    : launch<F, kRows, float>(ma, mb, mb, p, s);
+      return turned ? launch<F, kTurned, float>(ma, mb, mb, p, bn, sms, s)
+                    : launch<F, kRows, float>(ma, mb, mb, p, bn, sms, s);
     case MOE_F16:
-      return turned ? launch<F, kTurned, __half>(ma, mb, mb, p, s)
-                    : launch<F, kRows, __half>(ma, mb, mb, p, s);
+      return turned ? launch<F, kTurned, __half>(ma, mb, mb, p, bn, sms, s)
+                    : launch<F, kRows, __half>(ma, mb, mb, p, bn, sms, s);
     case MOE_BF16:
-      return turned ? launch<F, kTurned, __nv_bfloat16>(ma, mb, mb, p, s)
-                    : launch<F, kRows, __nv_bfloat16>(ma, mb, mb, p, s);
+      return turned ? launch<F, kTurned, __nv_bfloat16>(ma, mb, mb, p, bn, sms, s)
+                    : launch<F, kRows, __nv_bfloat16>(ma, mb, mb, p, bn, sms, s);
   }
   return cudaErrorInvalidValue;
 }
@@ -723,19 +746,24 @@ cudaError_t launch_gate_up(MxRows a, int64_t rows, MxRows gate, MxRows up, const
                            int E, int I, int H, uint8_t* codes, uint8_t* scales, unsigned* status,
                            bool zero_status, cudaStream_t s) {
   CUtensorMap ma, mg, mu;
+  cudaError_t err;
+  const int sms = sm_count(&err);
+  if (err != cudaSuccess) return err;
+  const int bn = use_narrow<F>(rows, E, 2 * (int64_t)I, sms) ? kNarrow : kWide;
   const int64_t pitch = F::code_pitch(H);
-  if (!make_map_bytes(&ma, a.codes, pitch, rows, BM) ||
-      !make_map_bytes(&mg, gate.codes, pitch, (int64_t)E * I, 64) ||
-      !make_map_bytes(&mu, up.codes, pitch, (int64_t)E * I, 64))
+  const int box = bn == kNarrow ? Shape<F, 1, kNarrow>::GC : Shape<F, 1, kWide>::GC;
+  if (!make_map_bytes(&ma, a.codes, pitch, rows, a_box<F>(rows, E)) ||
+      !make_map_bytes(&mg, gate.codes, pitch, (int64_t)E * I, box) ||
+      !make_map_bytes(&mu, up.codes, pitch, (int64_t)E * I, box))
     return cudaErrorInvalidValue;
-  Params p = make_params<F>(a, rows, offsets, E, I, H, BN / 2, status);
+  Params p = make_params<F>(a, rows, offsets, E, I, H, bn / 2, status);
   p.b_scales = gate.scales;
   p.b2_scales = up.scales;
   p.scales_align = scales_align(p.scale_pitch, a.scales, gate.scales, up.scales);
   p.codes = codes;
   p.scales = scales;
   p.zero_status = zero_status;
-  return launch<F, kGateUp, float>(ma, mg, mu, p, s);
+  return launch<F, kGateUp, float>(ma, mg, mu, p, bn, sms, s);
 }
 
 }  // namespace

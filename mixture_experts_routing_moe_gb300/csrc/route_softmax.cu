@@ -34,6 +34,9 @@ constexpr int kWarps = 4;
 constexpr int kMaxGroups = 128;
 constexpr unsigned kAll = 0xFFFFFFFFu;
 
+// 64-bit words of a warp's scratch: a key an expert and a group; whole 16-byte vectors.
+__host__ __device__ constexpr int scratch_words(int E) { return (E + 1) / 2 * 2 + kMaxGroups; }
+
 struct SoftmaxRoute {
   const void* logits;
   const float* bias;  // may be null
@@ -79,20 +82,6 @@ __device__ __forceinline__ void write_slot(const SoftmaxRoute& a, int64_t row, i
   reinterpret_cast<T*>(a.w)[row * a.k + r] = Dt<T>::from_f(w);
 }
 
-// l: the logits of this lane's slots (lane, lane + 32); returns the largest of all slots.
-template <typename T>
-__device__ __forceinline__ float largest_chosen(const SoftmaxRoute& a, const T* src,
-                                                const int* mine, float* l) {
-  const int lane = threadIdx.x & 31;
-  uint32_t key = 0;
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    l[h] = lane + 32 * h < a.k ? Dt<T>::to_f(src[mine[h]]) : -INFINITY;
-    key = max(key, key_of(l[h]));
-  }
-  return value_of(__reduce_max_sync(kAll, key));
-}
-
 // Order-preserving map of a double that is not NaN to 64 bits (-0 counts as +0), never 0.
 __device__ __forceinline__ unsigned long long key64_of(double v) {
   const unsigned long long u = (unsigned long long)__double_as_longlong(v + 0.0);
@@ -117,10 +106,10 @@ __device__ __forceinline__ void take_two(K& b1, K& b2, K k) {
   b1 = max(b1, k);
 }
 
-// Which of a lane's n experts (from e0 on) are in a kept group, as bits.  key: their scores' keys; F, to_
-// and of_key turn keys into scores and back.  scratch: E keys and kMaxGroups more.  in, out: the keys of
-// the scores of the last kept group and of the best other one.
-template <int C, typename K, typename ToValue, typename ToKey>
+// Which of a lane's n experts (from e0 on) are in a kept group, as bits.  key: their scores' keys, which
+// value and key_of_value turn into scores and back.  VEC: n is C or 0.  scratch: E keys and kMaxGroups
+// more.  in, out: the keys of the scores of the last kept group and of the best other one.
+template <int C, bool VEC, typename K, typename ToValue, typename ToKey>
 __device__ __forceinline__ unsigned kept_experts(const SoftmaxRoute& a, const K* key, int e0, int n,
                                                  K* scratch, ToValue value, ToKey key_of_value,
                                                  K* in, K* out) {
@@ -129,7 +118,7 @@ __device__ __forceinline__ unsigned kept_experts(const SoftmaxRoute& a, const K*
   if (a.lanes) {  // a group is a.lanes whole lanes: each of them has its score
     K b1 = 0, b2 = 0;
 #pragma unroll
-    for (int i = 0; i < C; ++i) take_two(b1, b2, i < n ? key[i] : (K)0);
+    for (int i = 0; i < C; ++i) take_two(b1, b2, (VEC ? n > 0 : i < n) ? key[i] : (K)0);
     for (int o = 1; o < a.lanes; o <<= 1) {
       const K o1 = __shfl_xor_sync(kAll, b1, o), o2 = __shfl_xor_sync(kAll, b2, o);
       b2 = max(max(b2, o2), min(b1, o1));
@@ -213,10 +202,11 @@ __device__ __forceinline__ int take_best(K* key, K& best, int e0, K* top) {
   return __shfl_sync(kAll, id, from);
 }
 
-// The row's decision in float64 (m: its largest logit, a number).
+// The row's choice in float64 (m: its largest logit, a number): the experts of this lane's slots, lane
+// and lane + 32, as two halves; all ones where a bias is NaN.
 template <typename T, int C>
-__device__ __noinline__ void route_row_f64(const SoftmaxRoute& a, int64_t row, float m,
-                                           unsigned long long* scratch) {
+__device__ __noinline__ unsigned long long choose_f64(const SoftmaxRoute& a, int64_t row, float m,
+                                                      unsigned long long* scratch) {
   typedef unsigned long long K;
   const int lane = threadIdx.x & 31, e0 = lane * a.per, n = max(0, min(a.per, a.E - e0));
   const T* src = reinterpret_cast<const T*>(a.logits) + row * a.E;
@@ -237,14 +227,11 @@ __device__ __noinline__ void route_row_f64(const SoftmaxRoute& a, int64_t row, f
     nan |= c[i] != c[i];
     key[i] = i < n ? key64_of(c[i]) : 0ull;
   }
-  if (__any_sync(kAll, nan)) {
-    for (int r = lane; r < a.k; r += 32) write_slot<T>(a, row, r, r, __int_as_float(0x7FC00000));
-    return;
-  }
+  if (__any_sync(kAll, nan)) return ~0ull;
   unsigned keep = n > 0 ? (n < 32 ? (1u << n) - 1u : ~0u) : 0u;
   if (a.SG < a.G) {
     K in, out;
-    keep = kept_experts<C>(a, key, e0, n, scratch, value64_of, key64_of, &in, &out);
+    keep = kept_experts<C, false>(a, key, e0, n, scratch, value64_of, key64_of, &in, &out);
   }
   K best = 0;
 #pragma unroll
@@ -254,31 +241,14 @@ __device__ __noinline__ void route_row_f64(const SoftmaxRoute& a, int64_t row, f
     if (!((keep >> i) & 1u)) key[i] = 0;
     best = max(best, key[i]);
   }
-  int mine[2] = {0, 0};
+  unsigned long long mine = 0;
   for (int r = 0; r < a.k; ++r) {
     K top;
-    const int id = take_best<C>(key, best, e0, &top);
-    if (r == lane) mine[0] = id;
-    if (r == lane + 32) mine[1] = id;
+    const unsigned id = take_best<C>(key, best, e0, &top);
+    if (r == lane) mine |= id;
+    if (r == lane + 32) mine |= (unsigned long long)id << 32;
   }
-  // renormalised weights do not depend on m: the largest chosen logit keeps them from vanishing
-  float l[2];
-  const float largest = largest_chosen<T>(a, src, mine, l);
-  if (a.renorm) m = largest;
-  double sel = 0.0, w[2] = {0.0, 0.0};
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-    if (lane + 32 * h < a.k) {
-      w[h] = exp((double)l[h] - (double)m);
-      sel += w[h];
-    }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sel += __shfl_xor_sync(kAll, sel, o);
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-    if (lane + 32 * h < a.k)
-      write_slot<T>(a, row, lane + 32 * h, mine[h],
-                    (float)(w[h] / (a.renorm ? sel : z) * (double)a.scale));
+  return mine;
 }
 
 // N values from p on, which is 16-byte aligned.
@@ -297,13 +267,14 @@ __device__ __forceinline__ void load_vec(const T* p, float* v) {
 template <typename T, int C, bool VEC>
 __global__ void __launch_bounds__(kWarps * 32)
     moe_route_softmax_kernel(const __grid_constant__ SoftmaxRoute a) {
-  extern __shared__ unsigned long long soft_smem[];
+  extern __shared__ __align__(16) unsigned long long soft_smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t row = (int64_t)blockIdx.x * kWarps + warp;
   if (row >= a.T) return;  // whole warps leave
-  unsigned long long* scratch = soft_smem + (size_t)warp * (a.E + kMaxGroups);
+  unsigned long long* scratch = soft_smem + (size_t)warp * scratch_words(a.E);
   const T* src = reinterpret_cast<const T*>(a.logits) + row * a.E;
   const int e0 = lane * a.per, n = max(0, min(a.per, a.E - e0));  // this lane's experts
+  auto in = [&](int i) { return VEC ? n > 0 : i < n; };
   float x[C], c[C];
 #pragma unroll
   for (int i = 0; i < C; ++i) x[i] = -INFINITY;
@@ -341,7 +312,7 @@ __global__ void __launch_bounds__(kWarps * 32)
       if (n > 0) load_vec<float, C>(a.bias + e0, b);
     } else {
 #pragma unroll
-      for (int i = 0; i < C; ++i) b[i] = i < n ? __ldg(a.bias + e0 + i) : 0.f;
+      for (int i = 0; i < C; ++i) b[i] = in(i) ? __ldg(a.bias + e0 + i) : 0.f;
     }
     uint32_t top = 0;
 #pragma unroll
@@ -359,29 +330,32 @@ __global__ void __launch_bounds__(kWarps * 32)
   }
   unsigned keep = n > 0 ? (n < 32 ? (1u << n) - 1u : ~0u) : 0u;
   if (sure && a.SG < a.G) {
-    uint32_t in, out;
+    uint32_t last, other;
     uint32_t* floats = reinterpret_cast<uint32_t*>(scratch);
     if (a.bias || !a.two) {
-      keep = kept_experts<C>(a, key, e0, n, floats, value_of, key_of, &in, &out);
+      keep = kept_experts<C, VEC>(a, key, e0, n, floats, value_of, key_of, &last, &other);
     } else {
       uint32_t ekey[C];
 #pragma unroll
       for (int i = 0; i < C; ++i) ekey[i] = __float_as_uint(c[i]) | 0x80000000u;  // (not negative)
-      keep = kept_experts<C>(a, ekey, e0, n, floats, value_of, key_of, &in, &out);
+      keep = kept_experts<C, VEC>(a, ekey, e0, n, floats, value_of, key_of, &last, &other);
     }
     if (a.bias || a.two) {
       // sums of two exponentials: 4e-7 of the sum and 2 * 0.37 * 1.8e-7 (d e^-d <= 0.37)
-      const float vi = value_of(in), vo = value_of(out);
+      const float vi = value_of(last), vo = value_of(other);
       const float bound = a.bias ? (a.two ? 2.f * err + 1.2e-7f * fabsf(vi) : err)
                                  : 4e-7f * vi + 1.4e-7f;
       sure = vi - vo > 2.f * bound;
     }
   }
   uint32_t best = 0;
+  if (VEC && a.lanes) {  // a lane's experts are kept together
 #pragma unroll
-  for (int i = 0; i < C; ++i) {
-    key[i] = (keep >> i) & 1u ? key[i] : 0u;
-    best = max(best, key[i]);
+    for (int i = 0; i < C; ++i) best = max(best, key[i]);
+    best = keep ? best : 0u;
+  } else {
+#pragma unroll
+    for (int i = 0; i < C; ++i) best = max(best, (keep >> i) & 1u ? key[i] : 0u);
   }
   // one expert more than is chosen, for the last one's margin
   const bool more = a.bias && a.k < a.SG * (a.E / a.G);
@@ -393,16 +367,26 @@ __global__ void __launch_bounds__(kWarps * 32)
   uint32_t least = 1u;
   if (sure && rounds <= 32) {
     // `rounds` lanes have an expert at or above the bound, so the last choice is at or above it too
-    uint32_t b = best;
+    // (or, where fewer lanes have experts, their two best do)
+    uint32_t b = best, second = 0;
+    if (rounds > __popc(__ballot_sync(kAll, best != 0u))) {
+      b = 0;
+#pragma unroll
+      for (int i = 0; i < C; ++i) take_two(b, second, (keep >> i) & 1u ? key[i] : 0u);
+    }
     for (int r = 0; r < rounds; ++r) {
       const uint32_t top = warp_max(b);
-      if (top == 0u) break;  // fewer lanes: every kept expert
+      if (top == 0u) break;  // every kept expert
       least = r == rounds - 1 ? top : 1u;
-      b = b == top ? 0u : b;
+      if (b == top) {
+        b = second;
+        second = 0;
+      }
     }
     unsigned above = 0;
 #pragma unroll
     for (int i = 0; i < C; ++i) above |= key[i] >= least ? 1u << i : 0u;
+    above &= keep;
     const int have = __popc(above);
     int before = have;
 #pragma unroll
@@ -412,40 +396,63 @@ __global__ void __launch_bounds__(kWarps * 32)
     }
     count = __shfl_sync(kAll, before, 31);
     if (count <= 32) {
-      // an expert a lane: (key, ~id), so that equal keys rank the lower id first
-      unsigned long long* list = scratch;
+      // an expert a lane, in the order of their ids; each counts the keys above its own, and those as
+      // large of lower ids
+      uint32_t* keys = reinterpret_cast<uint32_t*>(scratch);
+      uint32_t* ids = keys + 32;
       before -= have;
+      __syncwarp();
+      keys[lane] = 0u;
       __syncwarp();
 #pragma unroll
       for (int i = 0; i < C; ++i)
-        if ((above >> i) & 1u)
-          list[before++] = (unsigned long long)key[i] << 32 | (uint32_t)~(e0 + i);
+        if ((above >> i) & 1u) {
+          keys[before] = key[i];
+          ids[before++] = e0 + i;
+        }
       __syncwarp();
-      const unsigned long long own = lane < count ? list[lane] : 0ull;
+      const uint32_t own = keys[lane], id = ids[lane];
       int rank = 0;
-      for (int j = 0; j < count; ++j) rank += list[j] > own;
+      for (int j = 0; j < count; j += 4) {
+        const uint4 v = *reinterpret_cast<const uint4*>(keys + j);
+        rank += v.x + (j < lane) > own;  // (keys are at most 0xFF800000)
+        rank += v.y + (j + 1 < lane) > own;
+        rank += v.z + (j + 2 < lane) > own;
+        rank += v.w + (j + 3 < lane) > own;
+      }
       __syncwarp();
-      if (lane < count) list[rank] = own;
+      if (lane < count) {
+        keys[rank] = own;
+        ids[rank] = id;
+      }
       __syncwarp();
-      const unsigned long long at = lane < count ? list[lane] : 0ull;
-      mine[0] = lane < count ? (int)~(uint32_t)at : 0;
+      mine[0] = lane < count ? (int)ids[lane] : 0;
       if (a.bias) {
-        const int next = __shfl_down_sync(kAll, mine[0], 1);
-        const float v = value_of((uint32_t)(at >> 32)), vn = __shfl_down_sync(kAll, v, 1);
+        const float v = value_of(keys[lane]), vn = __shfl_down_sync(kAll, v, 1);
         const bool clear = lane < count - 1 && v - vn > 2.f * err;
         const unsigned clears = __ballot_sync(kAll, clear);
-        const unsigned ties = __ballot_sync(kAll, lane < count - 1 && !clear && tied(mine[0], next));
         const unsigned chosen = (1u << (a.k - 1)) - 1u;  // pairs among the chosen
-        sure = ((clears | ties) & chosen) == chosen;
-        if (more) {
-          // the last one against the rest: those tied with it, and then a clear margin
-          const int end = __ffs(~(ties >> (a.k - 1))) - 1 + a.k - 1;
-          sure = sure && ((clears >> end) & 1u || (end == count - 1 && least == 1u));
+        if (more ? (clears & (chosen << 1 | 1u)) != (chosen << 1 | 1u) : (clears & chosen) != chosen) {
+          const int next = __shfl_down_sync(kAll, mine[0], 1);
+          const unsigned ties =
+              __ballot_sync(kAll, lane < count - 1 && !clear && tied(mine[0], next));
+          sure = ((clears | ties) & chosen) == chosen;
+          if (more) {
+            // the last one against the rest: those tied with it, and then a clear margin
+            const int end = __ffs(~(ties >> (a.k - 1))) - 1 + a.k - 1;
+            sure = sure && ((clears >> end) & 1u || (end == count - 1 && least == 1u));
+          }
         }
       }
     }
   }
   if (sure && count > 32) {  // many slots, or many alike: a round each
+    best = 0;
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      key[i] = (keep >> i) & 1u ? key[i] : 0u;
+      best = max(best, key[i]);
+    }
     float last_v = 0.f;
     int last = 0;
     const int all = a.SG * (a.E / a.G), end = more ? all : a.k;
@@ -466,24 +473,29 @@ __global__ void __launch_bounds__(kWarps * 32)
   }
   if (!sure) {
     __syncwarp();
-    route_row_f64<T, C>(a, row, m, scratch);
-    return;
+    const unsigned long long chosen = choose_f64<T, C>(a, row, m, scratch);
+    if (chosen == ~0ull) {
+      for (int r = lane; r < a.k; r += 32) write_slot<T>(a, row, r, r, __int_as_float(0x7FC00000));
+      return;
+    }
+    mine[0] = (int)(uint32_t)chosen;
+    mine[1] = (int)(chosen >> 32);
   }
-  float w[2] = {0.f, 0.f}, l[2];
-  const float largest = largest_chosen<T>(a, src, mine, l);
-  if (a.renorm) m = largest;
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-    if (lane + 32 * h < a.k) w[h] = expf(l[h] - m);
-  const float by = a.renorm ? warp_sum(w[0] + w[1]) : z;
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-    if (lane + 32 * h < a.k) write_slot<T>(a, row, lane + 32 * h, mine[h], w[h] / by * a.scale);
+  // Weights.  Renormalised ones do not depend on m: the largest chosen logit keeps them from vanishing.
+  float l[2] = {-INFINITY, -INFINITY}, w[2] = {0.f, 0.f};
+  if (lane < a.k) l[0] = Dt<T>::to_f(src[mine[0]]);
+  if (lane + 32 < a.k) l[1] = Dt<T>::to_f(src[mine[1]]);
+  if (a.renorm) m = value_of(max(warp_max(key_of(l[0])), a.k > 32 ? warp_max(key_of(l[1])) : 0u));
+  w[0] = expf(l[0] - m);
+  if (a.k > 32) w[1] = expf(l[1] - m);
+  const float by = a.renorm ? warp_sum((lane < a.k ? w[0] : 0.f) + (lane + 32 < a.k ? w[1] : 0.f)) : z;
+  if (lane < a.k) write_slot<T>(a, row, lane, mine[0], w[0] / by * a.scale);
+  if (lane + 32 < a.k) write_slot<T>(a, row, lane + 32, mine[1], w[1] / by * a.scale);
 }
 
 template <typename T, int C>
 cudaError_t launch_c(const SoftmaxRoute& a, cudaStream_t s) {
-  const size_t smem = kWarps * (size_t)(a.E + kMaxGroups) * sizeof(unsigned long long);
+  const size_t smem = kWarps * (size_t)scratch_words(a.E) * sizeof(unsigned long long);
   const bool vec = a.per == C && a.E % C == 0 && C * sizeof(T) % 16 == 0 &&
                    a.E * sizeof(T) % 16 == 0 && (((uintptr_t)a.logits | (uintptr_t)a.bias) & 15u) == 0;
   const auto kern = vec ? moe_route_softmax_kernel<T, C, true> : moe_route_softmax_kernel<T, C, false>;

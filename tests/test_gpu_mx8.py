@@ -175,7 +175,8 @@ def check_product(sizes, N, K, dtype, seed, extra_rows=0):
 @pytest.mark.parametrize("sizes,N,K", [
     ([1], 1, 32), ([1], 256, 256), ([128], 256, 512), ([130], 300, 96), ([3, 0, 5], 33, 64),
     ([0, 0, 7], 129, 224), ([127, 1, 129, 64], 384, 1024), ([400], 511, 2080), ([5] * 40, 72, 288),
-    ([257, 31], 520, 4096), ([1, 1], 2000, 1), ([200, 180], 264, 1056)])
+    ([257, 31], 520, 4096), ([1, 1], 2000, 1), ([200, 180], 264, 1056), ([3, 1, 0, 2], 64, 2176),
+    ([128], 65, 1100), ([20, 7], 1030, 4128)])
 def test_product(dtype, sizes, N, K):
     check_product(sizes, N, K, dtype, sum(sizes) * 31 + N + K)
 
@@ -361,7 +362,8 @@ def check_experts(sizes, H, I, dtype, seed):
 
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("sizes,H,I", [([1], 32, 32), ([2, 0, 5], 64, 160), ([130, 3], 256, 72),
-                                       ([40, 0, 300], 200, 416), ([64, 200], 512, 768), ([7], 33, 1)])
+                                       ([40, 0, 300], 200, 416), ([64, 200], 512, 768), ([7], 33, 1),
+                                       ([1, 5, 0, 1], 2080, 100), ([100], 160, 1000)])
 def test_experts(dtype, sizes, H, I):
     check_experts(sizes, H, I, dtype, sum(sizes) + H + I)
 
@@ -409,24 +411,90 @@ def test_layer(dtype, wdt, T, E, H, I, k):
             np.add.at(ref, t, p * y)
             # y rounded to the type, then k products and sums in FP32
             np.add.at(tol, t, p * (d * (1 + torch.finfo(dtype).eps) + half_step(dtype, y) + k * 2.0 ** -23 * np.abs(y)))
-    check_within(np64(out), ref, tol * (1 + torch.finfo(dtype).eps) + half_step(dtype, ref), dtype)
+    tol = tol * (1 + torch.finfo(dtype).eps) + half_step(dtype, ref)
+    check_within(np64(out), ref, tol, dtype)
     # and the same bits from the stages
     d = moe.moe_mx8_dispatch(*x, idx, E, H)
     y = moe.moe_mx8_experts_forward_dispatched((d["codes"], d["scales"]), d["offsets"], *packed, dtype=dtype)
     assert torch.equal(moe.moe_combine(y, d["row_of_slot"], gate.to(DEV)), out)
 
 
-def test_layer_bad_id_and_empty():
-    x, _, packed, _, idx, _, gate = layer(6, 4, 64, 96, 2, 3)
-    idx.view(torch.int32)[3, 1] = 4
+@pytest.mark.parametrize("T", [6, 60])
+def test_layer_bad_id_and_empty(T):
+    x, _, packed, _, idx, _, gate = layer(T, 4, 64, 96, 2, 3)
     g = torch.from_numpy(gate).float().to(DEV)
-    ws = torch.empty(moe.mx8_forward_workspace_bytes(6, 4, 64, 96, 2, torch.bfloat16), dtype=torch.uint8,
+    want = np64(moe.moe_mx8_forward(x, idx, g, *packed))
+    idx.view(torch.int32)[3, 1] = 4
+    idx.view(torch.int32)[4, 0] = -1
+    ws = torch.empty(moe.mx8_forward_workspace_bytes(T, 4, 64, 96, 2, torch.bfloat16), dtype=torch.uint8,
                      device=DEV)
     out = np64(moe.moe_mx8_forward(x, idx, g, *packed, ws=ws))
     assert moe.moe_device_status(ws) == 8
-    assert np.isnan(out[3]).all() and np.isfinite(np.delete(out, 3, 0)).all()
+    assert np.isnan(out[3:5]).all() and (np.delete(out, [3, 4], 0) == np.delete(want, [3, 4], 0)).all()
+    idx.view(torch.int32)[:] = 7                                # none left
+    assert np.isnan(np64(moe.moe_mx8_forward(x, idx, g, *packed, ws=ws))).all()
     out = moe.moe_mx8_forward((x[0][:0], x[1][:0]), idx[:0], g[:0], *packed)
     assert out.shape == (0, 64)
+
+
+@pytest.mark.parametrize("T,E,k", [(8, 1, 1), (16, 2, 2), (9, 3, 3), (64, 1, 1), (64, 2, 1), (1, 64, 64), (21, 3, 3)])
+def test_few_tokens_that_share_experts(T, E, k):
+    """Many slots for an expert, and one for each of many."""
+    x, xv, packed, w, idx, ids, gate = layer(T, E, 96, 160, k, T)
+    dtype = torch.float32
+    out = np64(moe.moe_mx8_forward(x, idx, torch.from_numpy(gate).float().to(DEV), *packed, dtype=dtype))
+    gate = np64(torch.from_numpy(gate).float())
+    ref, tol = np.zeros((T, 96)), np.zeros((T, 96))
+    for e in range(E):
+        t, j = np.nonzero(ids == e)
+        y, d = experts_reference(xv[t], [m[e] for m in w], 96, 160)
+        p = gate[t, j][:, None]
+        np.add.at(ref, t, p * y)
+        np.add.at(tol, t, p * (d + (k + 2) * 2.0 ** -23 * np.abs(y)))
+    check_within(out, ref, tol * 1.001 + half_step(dtype, ref), dtype)
+
+
+def test_few_tokens_the_same_expert_twice():
+    """A token that names an expert in two slots gets it with both weights."""
+    x, _, packed, _, idx, _, gate = layer(4, 6, 64, 96, 2, 3)
+    idx.view(torch.int32)[:] = torch.tensor([[2, 2], [2, 1], [5, 5], [1, 1]], device=DEV)
+    g = torch.from_numpy(gate).float().to(DEV)
+    out = moe.moe_mx8_forward(x, idx, g, *packed, dtype=torch.float32)
+    one = moe.moe_mx8_forward(x, idx[:, :1].contiguous(), g.sum(-1, keepdim=True), *packed, dtype=torch.float32)
+    same = torch.tensor([0, 2, 3], device=DEV)
+    assert torch.allclose(out[same], one[same], rtol=1e-5, atol=1e-5 * float(out.abs().max()))
+
+
+def test_few_tokens_special_blocks():
+    """Scales from both ends, NaN blocks of tokens and of weights, NaN codes."""
+    x, xv, packed, w, idx, ids, gate = layer(3, 3, 64, 64, 3, 7)
+    g = torch.from_numpy(gate).float().to(DEV)
+    want = moe.moe_mx8_forward(x, idx, g, *packed, dtype=torch.float32)
+    xs, scales = x[1].clone(), [p[1].clone() for p in packed]
+    xs[:, :2] -= 60                                            # x 2^-60, gate and up 2^60, exactly
+    scales[0][..., :2] += 60
+    scales[1][..., :2] += 60
+    moved = [(packed[0][0], scales[0]), (packed[1][0], scales[1]), packed[2]]
+    assert torch.equal(moe.moe_mx8_forward((x[0], xs), idx, g, *moved, dtype=torch.float32), want)
+    xs = x[1].clone()
+    xs[1, 1] = 255
+    out = moe.moe_mx8_forward((x[0], xs), idx, g, *packed, dtype=torch.float32)
+    assert torch.isnan(out[1]).all() and torch.equal(out[[0, 2]], want[[0, 2]])
+    codes = x[0].clone()
+    codes[2, 40] = 0x7F
+    out = moe.moe_mx8_forward((codes, x[1]), idx, g, *packed, dtype=torch.float32)
+    assert torch.isnan(out[2]).all() and torch.equal(out[:2], want[:2])
+    down = packed[2][1].clone()
+    down[0, 10, 0] = 255                                       # expert 0's row 10: column 10 of all tokens
+    out = moe.moe_mx8_forward(x, idx, g, packed[0], packed[1], (packed[2][0], down), dtype=torch.float32)
+    bad = torch.isnan(out)
+    assert bad[:, 10].all() and bad.sum() == 3
+    assert torch.equal(out[~bad], want[~bad])
+    # products whose scales meet outside FP32's exponents
+    xs, scales = x[1].clone(), packed[0][1].clone()
+    xs[:], scales[:] = 0, 0
+    out = moe.moe_mx8_forward((x[0], xs), idx, g, (packed[0][0], scales), *packed[1:], dtype=torch.float32)
+    assert (out == 0).all()
 
 
 def test_layer_repeats_streams_and_graphs():
