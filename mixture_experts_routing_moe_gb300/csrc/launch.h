@@ -76,7 +76,7 @@ cudaError_t launch_dispatch_block_rows(const uint8_t* codes, const uint8_t* scal
                                        uint8_t* scales_d, cudaStream_t s);
 
 // Both in one launch for at most kFewSlots slots (T k), which also sets *status.
-constexpr int kFewSlots = 256;
+constexpr int kFewSlots = 2048;
 cudaError_t launch_dispatch_few_blocks(const uint8_t* codes, const uint8_t* scales, int64_t T,
                                        int64_t code_bytes, int64_t scale_bytes, const uint32_t* idx,
                                        int E, int k, int32_t* offsets, uint32_t* row_of_slot,

@@ -8,8 +8,8 @@ import functools
 import torch
 
 from . import binding as B
-from .binding import MoeError, _code, _cuda, _mx4_leading, _mx4_ws, _new, _new_ws, _ptr, _stream, lib
-from .mx8 import _given, _pitch, _rows, on_current_device
+from .binding import MoeError, _code, _new, _new_ws, _ptr, _stream, lib
+from .mx8 import _given, _pitch, _rows, leading, on_current_device, workspace
 
 
 def _like(t, x, where: str, name: str) -> int:
@@ -18,12 +18,10 @@ def _like(t, x, where: str, name: str) -> int:
         return 0
     if t.shape != x.shape or t.dtype != x.dtype:
         raise MoeError(2, f"{where}: {name} is not like x")
-    on_current_device(where, t)
-    return _mx4_leading(t, x.shape[-1], where)
+    return leading(t, x.shape[-1], where)
 
 
 def _weight(weight, x, where: str) -> int:
-    _cuda(weight)
     on_current_device(where, weight)
     if weight.shape != x.shape[-1:]:
         raise MoeError(2, f"{where}: weight is [H]")
@@ -40,8 +38,7 @@ def moe_rms_norm(x, weight, eps: float = 1e-6, residual=None, values: bool = Tru
     where = "moe_rms_norm"
     shape = x.shape
     H = shape[-1]
-    ldx = _mx4_leading(x, H, where)
-    on_current_device(where, x)
+    ldx = leading(x, H, where)
     dt, wdt = _code(x), _weight(weight, x, where)
     ldr = _like(residual, x, where, "residual")
     T, lead, dev = x.numel() // max(H, 1), tuple(shape[:-1]), x.device
@@ -90,8 +87,7 @@ def moe_rms_norm_backward(dy, s, weight, rstd, dsum=None, dx=None, dweight=None,
     stats.  dx may be dy or dsum itself."""
     where = "moe_rms_norm_backward"
     H = dy.shape[-1]
-    lddy = _mx4_leading(dy, H, where)
-    on_current_device(where, dy)
+    lddy = leading(dy, H, where)
     dt, wdt = _code(dy), _weight(weight, dy, where)
     lds, ldds = _like(s, dy, where, "s"), _like(dsum, dy, where, "dsum")
     T = dy.numel() // max(H, 1)
@@ -105,8 +101,7 @@ def moe_rms_norm_backward(dy, s, weight, rstd, dsum=None, dx=None, dweight=None,
     else:
         _given(dweight, (H,), torch.float32, where, "dweight")
     h = _stream(stream)
-    ws = _mx4_ws(ws, max(rms_norm_backward_workspace_bytes(T, H, dy.dtype), 256), dy.device, stream,
-                 h)
+    ws = workspace(ws, rms_norm_backward_workspace_bytes(T, H, dy.dtype), dy.device, stream, h, where)
     B._check(lib().moe_rms_norm_backward(dy.data_ptr(), lddy, s.data_ptr(), lds, weight.data_ptr(),
                                          wdt, rstd.data_ptr(), _ptr(dsum), ldds, dt, T, H,
                                          dx.data_ptr(), lddx, dweight.data_ptr(), ws.data_ptr(),
@@ -117,7 +112,6 @@ def moe_rms_norm_backward(dy, s, weight, rstd, dsum=None, dx=None, dweight=None,
 def _bias(bias, E: int, where: str):
     if bias is None:
         return None
-    _cuda(bias)
     on_current_device(where, bias)
     if bias.dtype != torch.float32 or bias.shape != (E,):
         raise MoeError(3 if bias.dtype != torch.float32 else 2, f"{where}: bias is float32 [E]")
@@ -129,7 +123,6 @@ def moe_route_softmax_grouped(logits, top_k: int, groups: int, selected_groups: 
                               scale: float = 1.0, bias=None, idx=None, w=None, stream=None):
     """moe_route_sigmoid_grouped with softmax scores -> (idx uint32 [T, k], w [T, k])."""
     where = "moe_route_softmax_grouped"
-    _cuda(logits)
     on_current_device(where, logits)
     T, E = logits.shape
     b = _bias(bias, E, where)
@@ -154,7 +147,6 @@ def moe_forward_softmax_grouped(x, logits, gate, up, down, top_k: int, groups: i
                                 ws=None, stream=None):
     """moe_forward with moe_route_softmax_grouped's router -> out [T, H]."""
     where = "moe_forward_softmax_grouped"
-    _cuda(x, logits, gate, up, down)
     on_current_device(where, x, logits, gate, up, down)
     T, H = x.shape
     E, I, _ = gate.shape
@@ -169,7 +161,7 @@ def moe_forward_softmax_grouped(x, logits, gate, up, down, top_k: int, groups: i
     if ws is None:
         ws = _new_ws(B.forward_workspace_bytes(T, E, H, I, top_k, logits.dtype, x.dtype), x.device,
                      stream)
-    _cuda(ws)
+    on_current_device(where, ws)
     B._check(lib().moe_forward_softmax_grouped(
         x.data_ptr(), logits.data_ptr(), _code(logits), b, gate.data_ptr(), up.data_ptr(),
         down.data_ptr(), _code(gate), T, E, H, I, top_k, groups, selected_groups,

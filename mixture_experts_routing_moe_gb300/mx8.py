@@ -10,7 +10,7 @@ import functools
 import torch
 
 from . import binding as B
-from .binding import DTYPE_CODE, MoeError, _code, _cuda, _mx4_leading, _mx4_ws, _new, _new_ws, _stream, lib
+from .binding import DTYPE_CODE, MoeError, _code, _mx4_leading, _mx4_ws, _new, _new_ws, _stream, lib
 
 _u8 = torch.uint8
 
@@ -36,31 +36,43 @@ def _dtype(dtype, where: str) -> int:
     return code
 
 
-def on_current_device(where: str, first, *others):
-    """Kernels are launched on the current device: refuses tensors of another one."""
+# Small calls take a few microseconds on the GPU, so the checks keep to the attributes they need.
+def on_current_device(where: str, *ts):
+    """Kernels are launched on the current device: refuses what is not a contiguous tensor there."""
     dev = torch._C._cuda_getDevice()
-    if first.get_device() != dev:
-        raise ValueError(f"{where}: tensors are on {first.device}, the current device is cuda:{dev}")
-    for t in others:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"{where}: tensors are on {first.device} and {t.device}")
+    for t in ts:
+        if t is not None and (t.get_device() != dev or not t.is_contiguous()):
+            refuse(where, t, dev)
+
+
+def refuse(where: str, t, dev: int):
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError("libmoe takes contiguous CUDA tensors")
+    raise ValueError(f"{where}: a tensor is on {t.device}, the current device is cuda:{dev}")
+
+
+def leading(t, K: int, where: str) -> int:
+    """Elements from one row of K consecutive values to the next, of a tensor on the current device."""
+    dev = torch._C._cuda_getDevice()
+    if t.get_device() != dev:
+        if not t.is_cuda:
+            raise ValueError(f"{where} takes CUDA rows of consecutive values")
+        refuse(where, t, dev)
+    return K if t.is_contiguous() else _mx4_leading(t, K, where)
 
 
 def _rows(codes, scales, K: int, where: str):
     """Checks one operand in blocks, [..., rows] rows of K values; returns the shape of codes."""
-    if not (codes.is_cuda and scales.is_cuda and codes.is_contiguous() and scales.is_contiguous()):
-        raise ValueError("libmoe takes contiguous CUDA tensors")
+    on_current_device(where, codes, scales)
     if codes.dtype is not _u8 or scales.dtype is not _u8:
         raise MoeError(3, f"{where}: codes and scales are uint8")
     shape = codes.shape
     if scales.shape != _scale_shape(shape, K):
         raise MoeError(2, f"{where}: rows of {K} values have {_pitch(K)} bytes of codes and scales")
-    on_current_device(where, codes, scales)
     return shape
 
 
 def _offsets(offsets, E: int, where: str):
-    _cuda(offsets)
     on_current_device(where, offsets)
     if offsets.dtype != torch.int32 or offsets.numel() != E + 1:
         raise MoeError(2, f"{where}: offsets are int32 [E + 1]")
@@ -69,7 +81,6 @@ def _offsets(offsets, E: int, where: str):
 
 def _given(t, shape, dtype, where: str, name: str):
     """Checks an output that the caller gave."""
-    _cuda(t)
     on_current_device(where, t)
     if t.shape != shape or t.dtype != dtype:
         raise MoeError(2, f"{where}: {name} is {dtype} {tuple(shape)}")
@@ -82,8 +93,7 @@ def moe_mx8_quantize(x, codes=None, scales=None, stream=None):
     where = "moe_mx8_quantize"
     shape = x.shape
     K = shape[-1]
-    ld = _mx4_leading(x, K, where)
-    on_current_device(where, x)
+    ld = leading(x, K, where)
     dt = _code(x)
     pc, ps = _pitch(K)
     lead = tuple(shape[:-1])
@@ -106,16 +116,22 @@ def moe_mx8_dequantize(codes, scales, K: int, dtype=torch.bfloat16, out=None, st
     else:
         if out.shape != (*shape[:-1], K):
             raise MoeError(2, f"{where}: out has another shape")
-        dt, ld = _code(out), _mx4_leading(out, K, where)
-        on_current_device(where, out)
+        dt, ld = _code(out), leading(out, K, where)
     B._check(lib().moe_mx8_dequantize(codes.data_ptr(), scales.data_ptr(),
                                       out.numel() // max(K, 1), K, out.data_ptr(), dt, ld,
                                       _stream(stream)), where)
     return out
 
 
+def workspace(ws, need: int, device, stream, handle: int, where: str):
+    """The caller's workspace, or one as the 4-bit operators keep them."""
+    if ws is not None:
+        on_current_device(where, ws)
+        return ws
+    return _mx4_ws(None, need if need > 256 else 256, device, stream, handle)
+
+
 def _idx(idx, T: int, where: str) -> int:
-    _cuda(idx)
     on_current_device(where, idx)
     if idx.dtype != torch.uint32 or idx.dim() != 2 or idx.shape[0] != T:
         raise MoeError(2, f"{where}: idx is uint32 [T, top_k]")
@@ -139,7 +155,6 @@ def moe_mx8_dispatch(codes, scales, idx, E: int, H: int, ws=None, stream=None):
            "row_of_slot": _new(R, torch.uint32, dev, stream)}
     if ws is None:
         ws = _new_ws(B.dispatch_workspace_bytes(T, E, k), dev, stream)
-    _cuda(ws)
     on_current_device(where, ws)
     B._check(lib().moe_mx8_dispatch(codes.data_ptr(), scales.data_ptr(), T, H, idx.data_ptr(), E, k,
                                     *(t.data_ptr() for t in out.values()), ws.data_ptr(),
@@ -166,7 +181,7 @@ def moe_mx8_product(a_codes, a_scales, b_codes, b_scales, offsets=None, dtype=to
     else:
         dt = _code(_given(out, (rows, N), out.dtype, where, "out"))
     s = _stream(stream)
-    ws = _mx4_ws(ws, 256, out.device, stream, s)
+    ws = workspace(ws, 256, out.device, stream, s, where)
     B._check(lib().moe_mx8_product(a_codes.data_ptr(), a_scales.data_ptr(), rows, b_codes.data_ptr(),
                                    b_scales.data_ptr(), off, E, N, K, out.data_ptr(), dt,
                                    ws.data_ptr(), ws.numel(), s), where)
@@ -206,7 +221,7 @@ def moe_mx8_experts_forward_dispatched(x, offsets, gate, up, down, dtype=torch.b
     else:
         dt = _code(_given(y, (rows, H), y.dtype, where, "y"))
     s = _stream(stream)
-    ws = _mx4_ws(ws, max(mx8_experts_workspace_bytes(rows, I), 256), y.device, stream, s)
+    ws = workspace(ws, mx8_experts_workspace_bytes(rows, I), y.device, stream, s, where)
     B._check(lib().moe_mx8_experts_forward_dispatched(
         x[0].data_ptr(), x[1].data_ptr(), off, rows, gate[0].data_ptr(), gate[1].data_ptr(),
         up[0].data_ptr(), up[1].data_ptr(), down[0].data_ptr(), down[1].data_ptr(), E, H, I,
@@ -229,7 +244,6 @@ def moe_mx8_forward(x, idx, w, gate, up, down, dtype=torch.bfloat16, out=None, w
         raise MoeError(2, f"{where}: x is [T, bytes]")
     T = shape[0]
     k = _idx(idx, T, where)
-    _cuda(w)
     on_current_device(where, w)
     if w.shape != idx.shape:
         raise MoeError(2, f"{where}: w is [T, top_k]")
@@ -240,8 +254,8 @@ def moe_mx8_forward(x, idx, w, gate, up, down, dtype=torch.bfloat16, out=None, w
     else:
         dt = _code(_given(out, (T, H), out.dtype, where, "out"))
     s = _stream(stream)
-    ws = _mx4_ws(ws, max(mx8_forward_workspace_bytes(T, E, H, I, k, out.dtype), 256), out.device,
-                 stream, s)
+    ws = workspace(ws, mx8_forward_workspace_bytes(T, E, H, I, k, out.dtype), out.device, stream, s,
+                   where)
     B._check(lib().moe_mx8_forward(
         x[0].data_ptr(), x[1].data_ptr(), idx.data_ptr(), w.data_ptr(), _code(w),
         gate[0].data_ptr(), gate[1].data_ptr(), up[0].data_ptr(), up[1].data_ptr(),
