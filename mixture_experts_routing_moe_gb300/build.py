@@ -66,7 +66,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         return obj
 
     with ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
-        objs = list(ex.map(compile_one, _sources()))
+        # the large ones first: the longest (a minute) would else start when the others are done
+        objs = list(ex.map(compile_one, sorted(_sources(), key=os.path.getsize, reverse=True)))
     tmp = LIB + ".tmp"
     cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -7,7 +7,7 @@
 // A persistent kernel walks tiles (expert, m-tile, n-tile) of 256 columns and 128 rows (a CTA) or
 // 256 rows (a cluster of two CTAs, cta_group::2: each CTA holds 128 of the rows and half of the B
 // rows, so a tile pulls a third fewer bytes through L2), or of 64 columns and 128 rows where few rows
-// leave few tiles.  Roles in each CTA:
+// leave few tiles (or of 128).  Roles in each CTA:
 //   warp 0      loads, for each K slice (128 bytes a row: 256 values in 4 bits, 128 in 8), the codes
 //               of its A and B rows by TMA into a ring.  For gate/up the B tile holds gate rows 0-63, up rows 0-63, gate
 //               rows 64-127, up rows 64-127 of 128 columns of a.  (Warps 0 and 1 run their loops with
@@ -46,7 +46,7 @@ namespace {
 using namespace tc;
 
 constexpr int BM = 128;  // rows of a CTA
-constexpr int kWide = 256, kNarrow = 64;  // columns of a tile (BN)
+constexpr int kWide = 256, kHalf = 128, kNarrow = 64;  // columns of a tile (BN)
 constexpr int kThreads = 512;
 // Registers of a thread of each warpgroup (the launch gives 128 to each; 72 + 104 + 2 * 168 = 512
 // = 4 * 128 are taken): the epilogue holds 128 accumulator values at once.
@@ -107,7 +107,7 @@ struct Fmt8 {
 // CG: CTAs of a tile; BN: its columns
 template <typename F, int CG, int BN>
 struct Shape {
-  static constexpr int STAGES = BN == kNarrow ? 8 : CG == 2 ? 6 : 4;
+  static constexpr int STAGES = BN == kNarrow ? 8 : CG == 2 || BN == kHalf ? 6 : 4;
   // Epilogue halves of a tile's columns; of those of a half, the first half is gate's, the other up's.
   static constexpr int HALVES = BN >= 128 ? 2 : 1, HC = BN / HALVES, GC = HC / 2;
   // Rows of a copy of A.  Single CTAs, which few rows take, copy the rows that their group has and no
@@ -125,7 +125,7 @@ struct Shape {
 };
 static_assert(Shape<Fmt4, 1, kWide>::SMEM <= 232448 && Shape<Fmt4, 2, kWide>::SMEM <= 232448 &&
                   Shape<Fmt8, 1, kWide>::SMEM <= 232448 && Shape<Fmt8, 2, kWide>::SMEM <= 232448 &&
-                  Shape<Fmt8, 1, kNarrow>::SMEM <= 232448,
+                  Shape<Fmt8, 1, kNarrow>::SMEM <= 232448 && Shape<Fmt8, 1, kHalf>::SMEM <= 232448,
               "shared memory of a CTA");
 static_assert(kScaleCol + 8 * Shape<Fmt8, 1, kNarrow>::SF_COLS <= kTmemCols &&
                   kScaleCol + 6 * Fmt4::CHUNKS * Shape<Fmt4, 2, kWide>::SF_COLS <= kTmemCols,
@@ -482,7 +482,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           const int h = part - 1;
           // (of a narrow tile's chunk, rows 64 to 127 are not used)
-          int n = GATEUP ? x.n * (BN / 2) + h * GC + i % GC : x.n * BN + h * 128 + i;
+          int n = GATEUP ? x.n * (BN / 2) + (h * 128 + i) / HC * GC + i % GC
+                         : x.n * BN + h * 128 + i;
           n = min(n, p.N - 1);
           const uint8_t* b = GATEUP && i % HC >= GC ? p.b2_scales : p.b_scales;
           src[j] = b + ((int64_t)x.e * p.N + n) * pitch;
@@ -665,13 +666,17 @@ int a_box(int64_t rows, int E) {
   return use_pairs(rows, E) ? Shape<F, 2, kWide>::A_BOX : Shape<F, 1, kWide>::A_BOX;
 }
 
-// Narrow tiles (in 8 bits) where the wide ones of the experts that rows can reach would not give every
-// SM one.
+// Columns of a tile (in 8 bits).  A slice costs some 470 cycles of issue however narrow its tile is (and
+// a tile of 64 columns reads 16 KB of A's rows and zeros for 8 KB of weights), so narrower tiles pay only as
+// long as every SM has one at most.  One token's 8 experts, H = 2048, I = 768: tiles of 256 columns
+// (48 and 64 of them) take 23.6 + 11 us, of 64 (192 and 256) 16.3 + 9.1, of 128 11.6 + 7.5.
 template <typename F>
-bool use_narrow(int64_t rows, int E, int64_t columns, int sms) {
-  if (F::CHUNKS != 1) return false;
-  const int64_t experts = rows < E ? rows : E;
-  return !use_pairs(rows, E) && rows <= BM && experts * ((columns + kWide - 1) / kWide) < sms;
+int tile_columns(int64_t rows, int E, int64_t columns, int sms) {
+  if (F::CHUNKS != 1 || use_pairs(rows, E) || rows > BM) return kWide;
+  const int64_t experts = rows < E ? rows : E;  // that rows can reach
+  for (int bn : {kNarrow, kHalf})
+    if (experts * ((columns + bn - 1) / bn) <= sms) return bn;
+  return kWide;
 }
 
 template <typename F, int KIND, typename T>
@@ -679,6 +684,7 @@ cudaError_t launch(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap
                    const Params& p, int bn, int sms, cudaStream_t s) {
   if constexpr (F::CHUNKS == 1) {
     if (bn == kNarrow) return launch_cg<F, 1, kNarrow, KIND, T>(a, b, b2, p, sms, s);
+    if (bn == kHalf) return launch_cg<F, 1, kHalf, KIND, T>(a, b, b2, p, sms, s);
   }
   return use_pairs(p.rows, p.E) ? launch_cg<F, 2, kWide, KIND, T>(a, b, b2, p, sms, s)
                                 : launch_cg<F, 1, kWide, KIND, T>(a, b, b2, p, sms, s);
@@ -706,15 +712,14 @@ Params make_params(MxRows a, int64_t rows, const int32_t* offsets, int E, int N,
   return p;
 }
 
-template <typename F>
+template <typename F, typename T>
 cudaError_t launch_product(MxRows a, int64_t rows, MxRows b, const int32_t* offsets, int E, int N,
-                           int K, void* out, int odt, unsigned* status, bool zero_status,
-                           cudaStream_t s) {
+                           int K, void* out, unsigned* status, bool zero_status, cudaStream_t s) {
   CUtensorMap ma, mb;
   cudaError_t err;
   const int sms = sm_count(&err);
   if (err != cudaSuccess) return err;
-  const int bn = use_narrow<F>(rows, E, N, sms) ? kNarrow : kWide;
+  const int bn = tile_columns<F>(rows, E, N, sms);
   const int64_t pitch = F::code_pitch(K);
   if (!make_map_bytes(&ma, a.codes, pitch, rows, a_box<F>(rows, E)) ||
       !make_map_bytes(&mb, b.codes, pitch, (int64_t)E * N, use_pairs(rows, E) ? bn / 2 : bn))
@@ -723,22 +728,11 @@ cudaError_t launch_product(MxRows a, int64_t rows, MxRows b, const int32_t* offs
   p.b_scales = b.scales;
   p.scales_align = scales_align(p.scale_pitch, a.scales, b.scales, b.scales);
   p.out = out;
-  const uintptr_t both = (uintptr_t)out | (uintptr_t)N * (odt == MOE_F32 ? 4 : 2);
+  const uintptr_t both = (uintptr_t)out | (uintptr_t)N * sizeof(T);
   p.store = both % 32 == 0 ? 32 : both % 16 == 0 ? 16 : 1;
   p.zero_status = zero_status;
-  const bool turned = p.store < 16;
-  switch (odt) {
-    case MOE_F32:
-      return turned ? launch<F, kTurned, float>(ma, mb, mb, p, bn, sms, s)
-                    : launch<F, kRows, float>(ma, mb, mb, p, bn, sms, s);
-    case MOE_F16:
-      return turned ? launch<F, kTurned, __half>(ma, mb, mb, p, bn, sms, s)
-                    : launch<F, kRows, __half>(ma, mb, mb, p, bn, sms, s);
-    case MOE_BF16:
-      return turned ? launch<F, kTurned, __nv_bfloat16>(ma, mb, mb, p, bn, sms, s)
-                    : launch<F, kRows, __nv_bfloat16>(ma, mb, mb, p, bn, sms, s);
-  }
-  return cudaErrorInvalidValue;
+  return p.store < 16 ? launch<F, kTurned, T>(ma, mb, mb, p, bn, sms, s)
+                      : launch<F, kRows, T>(ma, mb, mb, p, bn, sms, s);
 }
 
 template <typename F>
@@ -749,9 +743,10 @@ cudaError_t launch_gate_up(MxRows a, int64_t rows, MxRows gate, MxRows up, const
   cudaError_t err;
   const int sms = sm_count(&err);
   if (err != cudaSuccess) return err;
-  const int bn = use_narrow<F>(rows, E, 2 * (int64_t)I, sms) ? kNarrow : kWide;
+  const int bn = tile_columns<F>(rows, E, 2 * (int64_t)I, sms);
   const int64_t pitch = F::code_pitch(H);
-  const int box = bn == kNarrow ? Shape<F, 1, kNarrow>::GC : Shape<F, 1, kWide>::GC;
+  const int box = bn == kWide ? Shape<F, 1, kWide>::GC : Shape<F, 1, kHalf>::GC;
+  static_assert(Shape<F, 1, kHalf>::GC == Shape<F, 1, kNarrow>::GC, "rows of a copy of gate or up");
   if (!make_map_bytes(&ma, a.codes, pitch, rows, a_box<F>(rows, E)) ||
       !make_map_bytes(&mg, gate.codes, pitch, (int64_t)E * I, box) ||
       !make_map_bytes(&mu, up.codes, pitch, (int64_t)E * I, box))

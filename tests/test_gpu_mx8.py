@@ -176,7 +176,7 @@ def check_product(sizes, N, K, dtype, seed, extra_rows=0):
     ([1], 1, 32), ([1], 256, 256), ([128], 256, 512), ([130], 300, 96), ([3, 0, 5], 33, 64),
     ([0, 0, 7], 129, 224), ([127, 1, 129, 64], 384, 1024), ([400], 511, 2080), ([5] * 40, 72, 288),
     ([257, 31], 520, 4096), ([1, 1], 2000, 1), ([200, 180], 264, 1056), ([3, 1, 0, 2], 64, 2176),
-    ([128], 65, 1100), ([20, 7], 1030, 4128)])
+    ([128], 65, 1100), ([20, 7], 1030, 4128), ([2] * 10, 1000, 288), ([1, 0, 3] * 4, 1100, 1500)])
 def test_product(dtype, sizes, N, K):
     check_product(sizes, N, K, dtype, sum(sizes) * 31 + N + K)
 
@@ -363,7 +363,8 @@ def check_experts(sizes, H, I, dtype, seed):
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("sizes,H,I", [([1], 32, 32), ([2, 0, 5], 64, 160), ([130, 3], 256, 72),
                                        ([40, 0, 300], 200, 416), ([64, 200], 512, 768), ([7], 33, 1),
-                                       ([1, 5, 0, 1], 2080, 100), ([100], 160, 1000)])
+                                       ([1, 5, 0, 1], 2080, 100), ([100], 160, 1000),
+                                       ([1] * 8, 288, 768), ([3, 0, 1] * 4, 100, 790)])
 def test_experts(dtype, sizes, H, I):
     check_experts(sizes, H, I, dtype, sum(sizes) + H + I)
 
