@@ -6,33 +6,39 @@
 //
 // A persistent kernel walks tiles (expert, m-tile, n-tile) of 256 columns and 128 rows (a CTA) or
 // 256 rows (a cluster of two CTAs, cta_group::2: each CTA holds 128 of the rows and half of the B
-// rows, so a tile pulls a third fewer bytes through L2), or of 64 columns and 128 rows where few rows
-// leave few tiles (or of 128).  Roles in each CTA:
+// rows, so a tile pulls a third fewer bytes through L2), or in 8 bits of 64 or 128 columns and 128
+// rows where few rows leave few tiles.  Roles in each CTA:
 //   warp 0      loads, for each K slice (128 bytes a row: 256 values in 4 bits, 128 in 8), the codes
-//               of its A and B rows by TMA into a ring.  For gate/up the B tile holds gate rows 0-63, up rows 0-63, gate
-//               rows 64-127, up rows 64-127 of 128 columns of a.  (Warps 0 and 1 run their loops with
-//               all lanes; an elected one issues.)
-//   warp 1      (of CTA 0) copies each slice's scales to tensor memory and issues its four MMAs of 32
-//               bytes a row (K = 64 or 32, N = 256); tcgen05.commit frees the slot.
-//   warps 4-6   scales of A and of the two halves of B: each lane holds 32 bytes (four or
-//               eight slices) of four rows in registers, loads the next 32 ahead, and writes each slice's words to
-//               the chunk layout, 16 bytes at a time.  Groups start at any row, so no bulk copy of
-//               a fixed box would do.
-//   warps 8-15  epilogue: each warp takes 32 rows x 128 columns of the accumulator into registers
-//               at once and frees it, so the next tile's MMAs run while it converts and stores.
-//               (256 accumulator columns and the scales leave no room for a second accumulator.)
+//               of its A and B rows by TMA into a ring.  For gate/up the B tile of 256 columns holds
+//               gate rows 0-63, up rows 0-63, gate rows 64-127, up rows 64-127 of 128 columns of a.
+//               (Warps 0 and 1 run their loops with all lanes; an elected one issues.)
+//   warp 1      (of CTA 0) copies each slice's scales to tensor memory and issues its four MMAs of
+//               32 bytes a row (K = 64 or 32); tcgen05.commit frees the slot.
+//   warps 4-6   scales of A and of the two halves of B: each lane holds 32 bytes (four or eight
+//               slices) of four rows in registers, loads the next 32 ahead, and writes each slice's
+//               words to the chunk layout, 16 bytes at a time.  Groups start at any row, so no bulk
+//               copy of a fixed box would do.
+//   warps 8-15  epilogue: each warp takes 32 rows and half of the columns of the accumulator into
+//               registers at once and frees it, so the next tile's MMAs run while it converts and
+//               stores.  (256 accumulator columns and the scales leave no room for a second
+//               accumulator.)
 // Waits are bounded; on expiry the status word records the timeout and every role leaves.
 //
-// What bounds it, in 4 bits: at 8192^3 it runs in 159-161 us, 6.9 PFLOP/s, the tensor pipe 80 % active (in K =
-// 64 steps); without the scales (skipped, to time the rest) it takes 154, so the tensor pipe and
-// its operands' way through shared memory are what is left.  Deep K keeps that (K = 14336: 6.6); at
-// K = 2048 a tile is 8 slices, and the 1400 cycles in which the accumulator is emptied while no MMA
-// can run are a fifth of it (3.4 with groups that fill 78 % of their tiles).  On the way there, at
-// 8192^3: scales four bytes at a time per slice, 671 us (the L1 tag stage); pairs with a full
-// release at cluster scope for each slice, 467 (it waits for the warp's loads in flight), releasing
-// shared memory only, 250; 16-byte chunk stores, 238; whole-warp issue loops with an elected lane,
-// 195; two slices behind one proxy fence, 184; scale rows located once a tile and loaded 32 bytes
-// at a time, 163.
+// What bounds it, in 4 bits: at 8192^3 it runs in 159-161 us, 6.9 PFLOP/s, the tensor pipe 80 %
+// active (in K = 64 steps); without the scales (skipped, to time the rest) it takes 154, so the
+// tensor pipe and its operands' way through shared memory are what is left.  Deep K keeps that
+// (K = 14336: 6.6); at K = 2048 a tile is 8 slices, and the 1400 cycles in which the accumulator is
+// emptied while no MMA can run are a fifth of it (3.4 with groups that fill 78 % of their tiles).  On
+// the way there, at 8192^3: scales four bytes at a time per slice, 671 us (the L1 tag stage); pairs
+// with a full release at cluster scope for each slice, 467 (it waits for the warp's loads in flight),
+// releasing shared memory only, 250; 16-byte chunk stores, 238; whole-warp issue loops with an
+// elected lane, 195; two slices behind one proxy fence, 184; scale rows located once a tile and
+// loaded 32 bytes at a time, 163.
+// In 8 bits a slice's MMAs take twice as long (512 cycles), so the rest hides better: 8192^3 in
+// 313-318 us, 3.5 PFLOP/s, the tensor pipe 87 % active; under sustained load, at the 1.4 GHz that its
+// power leaves, 371.  A tile of 64 slices is 36300 cycles, of which 32800 are MMAs and some 2000 the
+// emptying.  Raw scales that came by TMA instead of through the scale warps' loads made no
+// difference there (363 and 371 us on two boxes) and few rows slower.
 #pragma once
 
 #include "launch.h"
@@ -658,7 +664,7 @@ cudaError_t launch_cg(const CUtensorMap& a, const CUtensorMap& b, const CUtensor
 // Pairs when groups average at least 160 rows; below that a pair's taller tiles multiply mostly
 // padding, above it they read fewer bytes through L2.  Experts of 32 groups, H = 4096, I = 2048,
 // one CTA against a pair: 64 rows a group 91 / 96 us, 96 95 / 102, 128 105 / 107, 192 119 / 112,
-// 512 229 / 219.
+// 512 229 / 219.  In 8 bits: 64 147 / 157, 128 155 / 165, 160 184 / 171, 192 188 / 173, 512 353 / 310.
 bool use_pairs(int64_t rows, int E) { return rows >= (int64_t)160 * E; }
 
 template <typename F>
@@ -666,17 +672,18 @@ int a_box(int64_t rows, int E) {
   return use_pairs(rows, E) ? Shape<F, 2, kWide>::A_BOX : Shape<F, 1, kWide>::A_BOX;
 }
 
-// Columns of a tile (in 8 bits).  A slice costs some 470 cycles of issue however narrow its tile is (and
-// a tile of 64 columns reads 16 KB of A's rows and zeros for 8 KB of weights), so narrower tiles pay only as
-// long as every SM has one at most.  One token's 8 experts, H = 2048, I = 768: tiles of 256 columns
-// (48 and 64 of them) take 23.6 + 11 us, of 64 (192 and 256) 16.3 + 9.1, of 128 11.6 + 7.5.
+// Columns of a tile (in 8 bits) of at most 128 rows.  A slice costs some 470 cycles of issue however narrow
+// its tile is, so the narrowest pay only as long as every SM has one at most, and half ones where there
+// are a few a SM, to deal them out evenly.  Experts, cold, with a row for each reached, at 64 / 128 / 256
+// columns: 4 of 16, H = 1024, I = 512: 18.9 / 21.0 / 25.1 us; 8 of 128, H = 2048, I = 768: 31.2 / 27.1 /
+// 33.2; 28 of them 55.8 / 49.6 / 53.7, 51 84.4 / 70.1 / 72.2; 2 of 8, H = 4096, I = 14336: 123 / 95 / 109;
+// 5 of them 250 / 195 / 177; 61 of 256, H = 7168, I = 2048: 600 / 443 / 443.
 template <typename F>
 int tile_columns(int64_t rows, int E, int64_t columns, int sms) {
   if (F::CHUNKS != 1 || use_pairs(rows, E) || rows > BM) return kWide;
   const int64_t experts = rows < E ? rows : E;  // that rows can reach
-  for (int bn : {kNarrow, kHalf})
-    if (experts * ((columns + bn - 1) / bn) <= sms) return bn;
-  return kWide;
+  if (experts * ((columns + kNarrow - 1) / kNarrow) <= sms) return kNarrow;
+  return experts * ((columns + kWide - 1) / kWide) <= 3 * (int64_t)sms ? kHalf : kWide;
 }
 
 template <typename F, int KIND, typename T>

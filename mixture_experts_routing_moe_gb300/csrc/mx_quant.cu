@@ -4,11 +4,11 @@
 // A block's scale is a power of two taken from the exponent field of its largest magnitude, so
 // scaling is exact and the only rounding is the conversion to e2m1 or e4m3.  Both kernels are bound
 // by memory: 2 or 4 bytes a value against 17/32 or 33/32 of a byte.  A lane owns units of eight
-// consecutive values (16 or 32 bytes in, four or eight bytes of codes out), four lanes a block; the block's maximum is
-// two shuffles.  A group of L lanes (32, or a smaller power of two for narrow rows) takes U * L
-// units of one row, U of them in flight; values wait in their storage type (16 registers for four
-// units of 16 bits), which leaves room for 2048 threads an SM: with them widened on arrival,
-// 1024 threads fitted and 16384 x 7168 bf16 took 100 us to quantise under the profiler.
+// consecutive values (16 or 32 bytes in, four or eight bytes of codes out), four lanes a block; the
+// block's maximum is two shuffles.  A group of L lanes (32, or a smaller power of two for narrow
+// rows) takes U * L units of one row, U of them in flight; values wait in their storage type (16
+// registers for four units of 16 bits), which leaves room for 2048 threads an SM: with them widened
+// on arrival, 1024 threads fitted and 16384 x 7168 bf16 took 100 us to quantise under the profiler.
 // Rows that are not 16-byte aligned are read and written one element a lane, consecutive lanes
 // consecutive elements, and turned around in shared memory.
 #include "launch.h"

@@ -15,15 +15,17 @@
 //   (C + 5) 2^-24.
 // Where a margin that the choice rests on is within twice the bound (the last kept group against the
 // best other one, each chosen expert against the next, unless the two have the same logit and bias,
-// and the last one against the first that is not tied with it so), or a score is not finite, the warp decides the row again in float64.
+// and the last one against the first that is not tied with it so), or a score is not finite, the warp
+// decides the row again in float64.
 //
-// What bounds it is the issue of integer and FP32 instructions.  With k rounds of a warp maximum,
-// each of which sent the lane that gave it looking for its next best, a row of 256 experts took 1800
-// (16384 rows: 57 us, 25 of them the tail of 32 rows in float64).  So the choice is made among few:
-// the rounds run over the lanes' best alone, which bounds the last choice from below, the experts
-// above that bound (mostly a dozen) go to shared memory, one for each lane, and each counts those
-// before it.  The float64 form keeps a lane's scores in registers, so that its exponentials overlap,
-// and ranks them as 64-bit integers.
+// What bounds it is the issue of integer and FP32 instructions: some 1050 a row of 256 experts with
+// eight groups and a bias, 18 us for 16384 rows, and the last rows that float64 decides (28 us
+// together; 65536 rows 79).  With k rounds of a warp maximum, each of which sent the lane that gave
+// it looking for its next best, a row took 1800 (57 us, 25 of them 32 rows in float64).  So the
+// choice is made among few: the rounds run over the lanes' best alone, which bounds the last choice
+// from below, the experts above that bound (mostly a dozen) go to shared memory, one for each lane,
+// and each counts those before it.  The float64 form keeps a lane's scores in registers, so that
+// its exponentials overlap, and ranks them as 64-bit integers.
 #include "common.cuh"
 #include "launch.h"
 
