@@ -76,15 +76,15 @@ struct Fmt4 {
     if (CG == 2) umma2_mxf4(d, a, b, idesc, sfa, sfb, more);
     else umma_mxf4(d, a, b, idesc, sfa, sfb, more);
   }
-  // Scale byte of a block whose largest magnitude has the bits `top`, and its codes at `out`.
-  static __device__ uint32_t block(const float* a, uint32_t top, uint8_t* out) {
+  // Scale byte of a block whose largest magnitude has the bits `top`, and its codes.
+  static __device__ uint32_t block(const float* a, uint32_t top, uint4* out) {
     const uint32_t b = mx4::scale_byte(top);
     const float inv = mx4::inv_scale(b);
     uint4 w = make_uint4(0, 0, 0, 0);
     if (b != 255u)
       w = make_uint4(mx4::codes8(a, inv), mx4::codes8(a + 8, inv), mx4::codes8(a + 16, inv),
                      mx4::codes8(a + 24, inv));
-    st_v4(out, w);
+    out[0] = w;
     return b;
   }
 };
@@ -99,13 +99,13 @@ struct Fmt8 {
     if (CG == 2) umma2_mxf8(d, a, b, idesc, sfa, sfb, more);
     else umma_mxf8(d, a, b, idesc, sfa, sfb, more);
   }
-  static __device__ uint32_t block(const float* a, uint32_t top, uint8_t* out) {
+  static __device__ uint32_t block(const float* a, uint32_t top, uint4* out) {
     const uint32_t b = mx8::scale_byte(top);
     uint32_t w[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) w[i] = b == 255u ? 0u : mx8::codes4(a + 4 * i, mx8::inv_scale(b));
-    st_v4(out, make_uint4(w[0], w[1], w[2], w[3]));
-    st_v4(out + 16, make_uint4(w[4], w[5], w[6], w[7]));
+    out[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    out[1] = make_uint4(w[4], w[5], w[6], w[7]);
     return b;
   }
 };
@@ -148,7 +148,6 @@ struct Params {
   int scales_align;          // see load_scales()
   int E, N, KB, NT;          // N: rows of one expert's B (gate/up: I); KB: slices
   void* out;
-  int store;                 // bytes of a store: 32 or 16 where they divide the pitch and the base
   uint8_t* codes;            // gate/up: rows of N values in blocks
   uint8_t* scales;
   unsigned* status;
@@ -183,33 +182,33 @@ __device__ __forceinline__ void load_scales(const uint8_t* row, int at, int pitc
   }
 }
 
-__device__ __forceinline__ void st_v8(void* p, const uint4& a, const uint4& b) {
-  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(a.x), "r"(a.y),
-               "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
-               : "memory");
-}
-// 32 accumulator columns of a row, 32 bytes (a whole sector; 16 cost twice the requests) or 16 at a
-// time; the last columns of a row of a ragged N one by one.
-template <typename T>
-__device__ __forceinline__ void store_row(T* row, const float* v, int col0, int N, int store) {
-  constexpr int W = 16 / sizeof(T);
-  if (col0 + 32 <= N) {
+// V pieces of 16 bytes of each of a warp's 32 rows (a lane holds its row's; out: row 0, the warp's first
+// byte; rows, bytes: how many of them exist, whole pieces).  They go through the warp's 1 KB of shared
+// memory, 64 / V rows at a time (swizzled, so neither way has conflicts), and V lanes store V neighbouring
+// pieces: whole lines of 128 bytes where V = 8.  With each lane writing 32 bytes of its own row at a time,
+// the first slices of the next tile came 2500 cycles late behind the requests: 8192 x 8192 bf16 with
+// K = 2048 took 100 us (4 bits: 68), this way 91 (60); without any store 80 (47).  8192^3 339 us, now 326
+// (161, now 155).
+template <int V>
+__device__ __forceinline__ void store_lines(uint8_t* out, int64_t pitch, const uint4 (&v)[V], int rows,
+                                            int bytes, uint32_t turn, int lane) {
+  static_assert(V == 2 || V == 4 || V == 8, "pieces of a row");
+  constexpr int ROWS = 64 / V;
+  auto at = [&](int row, int j) { return turn + (row * V + (j ^ (row / (8 / V) % V))) * 16; };
 #pragma unroll
-    for (int i = 0; i < 32 / W; i += 2) {
-      Vec16<T> q, r;
-      q.from_float(v + i * W);
-      r.from_float(v + (i + 1) * W);
-      if (store == 32) {
-        st_v8(row + col0 + i * W, q.u, r.u);
-      } else {
-        st_v4(row + col0 + i * W, q.u);
-        st_v4(row + col0 + (i + 1) * W, r.u);
-      }
+  for (int g = 0; g < 32 / ROWS; ++g) {
+    if (lane / ROWS == g) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) st_shared_v4(at(lane % ROWS, j), v[j].x, v[j].y, v[j].z, v[j].w);
     }
-  } else {
+    __syncwarp();
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (col0 + i < N) row[col0 + i] = Dt<T>::from_f(v[i]);
+    for (int h = 0; h < 2; ++h) {
+      const int row = (h * 32 + lane) / V, j = lane % V;
+      const uint4 q = ld_shared_v4(at(row, j));
+      if (g * ROWS + row < rows && j * 16 < bytes) st_v4(out + (g * ROWS + row) * pitch + j * 16, q);
+    }
+    __syncwarp();
   }
 }
 // A warp's 32 rows x 32 CH columns of an output whose rows are not 16-byte aligned (out: row 0, the
@@ -578,39 +577,59 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) arrive_leader(tempty);
-      const int row = x.r0 + q * 32 + lane;
-      if (KIND == kTurned) {
-        const int col0 = x.n * BN + h * HC;
-        store_turned((T*)p.out + (int64_t)(x.r0 + q * 32) * p.N + col0, p.N, acc,
-                     x.r1 - x.r0 - q * 32, p.N - col0, turn + (warp - 8) * kTurnBytes, lane);
-      } else if (row < x.r1) {
-        if (GATEUP) {
-          // GC columns gate, then GC up, of a's columns n * BN / 2 + h * GC ..: GC / 32 blocks
-          const int64_t cp = F::code_pitch(p.N), sp = mx4::scale_pitch(p.N);
-          const int blocks = (int)mx4::blocks_of(p.N);
+      const int64_t row0 = x.r0 + q * 32;
+      const int rows = x.r1 - (int)row0;  // of the warp's that the group has, or more
+      if (rows <= 0) continue;
+      uint8_t* my_turn = turn + (warp - 8) * kTurnBytes;
+      if (GATEUP) {
+        // GC columns gate, then GC up, of a's columns n * BN / 2 + h * GC ..: GC / 32 blocks
+        constexpr int BLOCKS = GC / 32, PIECES = F::CODE_BYTES / 16;
+        const int64_t cp = F::code_pitch(p.N), sp = mx4::scale_pitch(p.N);
+        const int blocks = (int)mx4::blocks_of(p.N), blk0 = x.n * (BN / 64) + h * BLOCKS;
+        uint4 codes[BLOCKS * PIECES];
+        uint32_t scale = 0;  // bytes, the first block's lowest
 #pragma unroll
-          for (int c = 0; c < GC / 32; ++c) {
-            const int blk = x.n * (BN / 64) + h * (GC / 32) + c;
-            if (blk >= blocks) continue;
-            float a[32];
-            uint32_t top = 0;
+        for (int c = 0; c < BLOCKS; ++c) {
+          float a[32];
+          uint32_t top = 0;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const float g = __uint_as_float(acc[c][i]), u = __uint_as_float(acc[c + GC / 32][i]);
-              a[i] = blk * 32 + i < p.N ? mx4::silu_mul(g, u) : 0.f;
-              top = max(top, __float_as_uint(a[i]) & 0x7FFFFFFFu);
-            }
-            const uint32_t b = F::block(a, top, p.codes + row * cp + blk * F::CODE_BYTES);
-            p.scales[row * sp + blk] = (uint8_t)b;
-            if (blk == blocks - 1)
-              for (int z = blocks; z & 3; ++z) p.scales[row * sp + z] = 0;
+          for (int i = 0; i < 32; ++i) {
+            const float g = __uint_as_float(acc[c][i]), u = __uint_as_float(acc[c + BLOCKS][i]);
+            a[i] = (blk0 + c) * 32 + i < p.N ? mx4::silu_mul(g, u) : 0.f;
+            top = max(top, __float_as_uint(a[i]) & 0x7FFFFFFFu);
           }
-        } else {
-          T* orow = (T*)p.out + (int64_t)row * p.N;
+          scale |= F::block(a, top, codes + c * PIECES) << (8 * c);
+        }
+        store_lines(p.codes + row0 * cp + (int64_t)blk0 * F::CODE_BYTES, cp, codes, rows,
+                    (blocks - blk0) * F::CODE_BYTES, smem_u32(my_turn), lane);
+        if (lane < rows && blk0 < blocks) {
+          // pitches are multiples of four, and a row's bytes past its last block are zero
+          uint8_t* sc = p.scales + (row0 + lane) * sp + blk0;
+          if (BLOCKS == 2 && blk0 + 1 < blocks) *reinterpret_cast<uint16_t*>(sc) = (uint16_t)scale;
+          else *sc = (uint8_t)scale;
+          const int last = min(blk0 + BLOCKS, blocks);
+          if (last == blocks)
+            for (int z = last; z & 3; ++z) sc[z - blk0] = 0;
+        }
+      } else if (KIND == kTurned) {
+        const int col0 = x.n * BN + h * HC;
+        store_turned((T*)p.out + row0 * p.N + col0, p.N, acc, rows, p.N - col0, my_turn, lane);
+      } else {
+        constexpr int W = 16 / sizeof(T), C = 8 * W;  // columns of a piece and of a line
 #pragma unroll
-          for (int c = 0; c < HC / 32; ++c)
-            store_row(orow, reinterpret_cast<const float*>(acc[c]), x.n * BN + h * HC + c * 32,
-                      p.N, p.store);
+        for (int c = 0; c < HC / C; ++c) {
+          const int col0 = x.n * BN + h * HC + c * C;
+          uint4 line[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            Vec16<T> piece;
+            const int e = c * C + j * W;
+            piece.from_float(reinterpret_cast<const float*>(acc[e / 32]) + e % 32);
+            line[j] = piece.u;
+          }
+          if (col0 < p.N)
+            store_lines((uint8_t*)((T*)p.out + row0 * p.N + col0), (int64_t)p.N * sizeof(T), line, rows,
+                        (p.N - col0) * (int)sizeof(T), smem_u32(my_turn), lane);
         }
       }
     }
@@ -735,11 +754,9 @@ cudaError_t launch_product(MxRows a, int64_t rows, MxRows b, const int32_t* offs
   p.b_scales = b.scales;
   p.scales_align = scales_align(p.scale_pitch, a.scales, b.scales, b.scales);
   p.out = out;
-  const uintptr_t both = (uintptr_t)out | (uintptr_t)N * sizeof(T);
-  p.store = both % 32 == 0 ? 32 : both % 16 == 0 ? 16 : 1;
   p.zero_status = zero_status;
-  return p.store < 16 ? launch<F, kTurned, T>(ma, mb, mb, p, bn, sms, s)
-                      : launch<F, kRows, T>(ma, mb, mb, p, bn, sms, s);
+  return ((uintptr_t)out | (uintptr_t)N * sizeof(T)) % 16 ? launch<F, kTurned, T>(ma, mb, mb, p, bn, sms, s)
+                                                          : launch<F, kRows, T>(ma, mb, mb, p, bn, sms, s);
 }
 
 template <typename F>
