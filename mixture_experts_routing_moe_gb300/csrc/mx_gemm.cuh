@@ -28,17 +28,19 @@
 // active (in K = 64 steps); without the scales (skipped, to time the rest) it takes 154, so the
 // tensor pipe and its operands' way through shared memory are what is left.  Deep K keeps that
 // (K = 14336: 6.6); at K = 2048 a tile is 8 slices, and the 1400 cycles in which the accumulator is
-// emptied while no MMA can run are a fifth of it (3.4 with groups that fill 78 % of their tiles).  On
+// emptied while no MMA can run are a fifth of it (3.4 with groups that fill 78 % of their tiles).  (These
+// before the stores of 16-bit rows went by whole lines: see store_lines; 155-157 since.)  On
 // the way there, at 8192^3: scales four bytes at a time per slice, 671 us (the L1 tag stage); pairs
 // with a full release at cluster scope for each slice, 467 (it waits for the warp's loads in flight),
 // releasing shared memory only, 250; 16-byte chunk stores, 238; whole-warp issue loops with an
 // elected lane, 195; two slices behind one proxy fence, 184; scale rows located once a tile and
 // loaded 32 bytes at a time, 163.
 // In 8 bits a slice's MMAs take twice as long (512 cycles), so the rest hides better: 8192^3 in
-// 313-318 us, 3.5 PFLOP/s, the tensor pipe 87 % active; under sustained load, at the 1.4 GHz that its
-// power leaves, 371.  A tile of 64 slices is 36300 cycles, of which 32800 are MMAs and some 2000 the
-// emptying.  Raw scales that came by TMA instead of through the scale warps' loads made no
-// difference there (363 and 371 us on two boxes) and few rows slower.
+// 313-321 us by itself, 3.5 PFLOP/s, the tensor pipe 87 % active; under load, at the 1.4 GHz that its
+// power leaves, 364-373.  A tile of 64 slices took 36300 cycles, of which 32800 are MMAs; the emptying
+// is some 1000, and the next tile's first slices came late behind the stores (store_lines).  Raw
+// scales that came by TMA instead of through the scale warps' loads made no difference there (363 and
+// 371 us on two boxes) and few rows slower.
 #pragma once
 
 #include "launch.h"
@@ -148,6 +150,7 @@ struct Params {
   int scales_align;          // see load_scales()
   int E, N, KB, NT;          // N: rows of one expert's B (gate/up: I); KB: slices
   void* out;
+  int store;                 // bytes of a store of FP32 rows: 32 or 16
   uint8_t* codes;            // gate/up: rows of N values in blocks
   uint8_t* scales;
   unsigned* status;
@@ -182,13 +185,43 @@ __device__ __forceinline__ void load_scales(const uint8_t* row, int at, int pitc
   }
 }
 
+__device__ __forceinline__ void st_v8(void* p, const uint4& a, const uint4& b) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(a.x), "r"(a.y),
+               "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+               : "memory");
+}
+// 32 accumulator columns of an FP32 row, 32 bytes (a whole sector; 16 cost twice the requests) or 16 at a
+// time; the last columns of a row of a ragged N one by one.  (Whole lines by store_lines, which rows of 16
+// bits take, made one wave of short tiles slower, 3001 x 1000 with K = 1376: 14.5 -> 16.5 us in replays
+// back to back; 8192^3 357 -> 354.)
+__device__ __forceinline__ void store_row(float* row, const float* v, int col0, int N, int store) {
+  if (col0 + 32 <= N) {
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      Vec16<float> q, r;
+      q.from_float(v + 4 * i);
+      r.from_float(v + 4 * (i + 1));
+      if (store == 32) {
+        st_v8(row + col0 + 4 * i, q.u, r.u);
+      } else {
+        st_v4(row + col0 + 4 * i, q.u);
+        st_v4(row + col0 + 4 * (i + 1), r.u);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (col0 + i < N) row[col0 + i] = v[i];
+  }
+}
 // V pieces of 16 bytes of each of a warp's 32 rows (a lane holds its row's; out: row 0, the warp's first
 // byte; rows, bytes: how many of them exist, whole pieces).  They go through the warp's 1 KB of shared
 // memory, 64 / V rows at a time (swizzled, so neither way has conflicts), and V lanes store V neighbouring
 // pieces: whole lines of 128 bytes where V = 8.  With each lane writing 32 bytes of its own row at a time,
 // the first slices of the next tile came 2500 cycles late behind the requests: 8192 x 8192 bf16 with
-// K = 2048 took 100 us (4 bits: 68), this way 91 (60); without any store 80 (47).  8192^3 339 us, now 326
-// (161, now 155).
+// K = 2048 took 99 to 104 us on three boxes (4 bits: 68), this way 91 to 96 (60), and without any store
+// 80 (47).  2 or 4 KB a warp, the L2's eviction hints and stores spread over the next tile's time
+// changed little (K = 2048 96.5, 91.4 against 91.6, and 90.2).
 template <int V>
 __device__ __forceinline__ void store_lines(uint8_t* out, int64_t pitch, const uint4 (&v)[V], int rows,
                                             int bytes, uint32_t turn, int lane) {
@@ -614,6 +647,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else if (KIND == kTurned) {
         const int col0 = x.n * BN + h * HC;
         store_turned((T*)p.out + row0 * p.N + col0, p.N, acc, rows, p.N - col0, my_turn, lane);
+      } else if constexpr (sizeof(T) == 4) {
+        if (lane < rows) {
+#pragma unroll
+          for (int c = 0; c < HC / 32; ++c)
+            store_row((float*)p.out + (row0 + lane) * p.N, reinterpret_cast<const float*>(acc[c]),
+                      x.n * BN + h * HC + c * 32, p.N, p.store);
+        }
       } else {
         constexpr int W = 16 / sizeof(T), C = 8 * W;  // columns of a piece and of a line
 #pragma unroll
@@ -754,9 +794,11 @@ cudaError_t launch_product(MxRows a, int64_t rows, MxRows b, const int32_t* offs
   p.b_scales = b.scales;
   p.scales_align = scales_align(p.scale_pitch, a.scales, b.scales, b.scales);
   p.out = out;
+  const uintptr_t both = (uintptr_t)out | (uintptr_t)N * sizeof(T);
+  p.store = both % 32 ? 16 : 32;
   p.zero_status = zero_status;
-  return ((uintptr_t)out | (uintptr_t)N * sizeof(T)) % 16 ? launch<F, kTurned, T>(ma, mb, mb, p, bn, sms, s)
-                                                          : launch<F, kRows, T>(ma, mb, mb, p, bn, sms, s);
+  return both % 16 ? launch<F, kTurned, T>(ma, mb, mb, p, bn, sms, s)
+                   : launch<F, kRows, T>(ma, mb, mb, p, bn, sms, s);
 }
 
 template <typename F>
