@@ -8,6 +8,8 @@
 // (r % 32) * 16 + (r / 32) * 4; tcgen05.cp 32x128b.warpx4 spreads it over four 32-bit columns
 // (column j: rows 32 j .. 32 j + 31, repeated in each 32-lane quarter).  Each K = 64 step uses two
 // of the four bytes, named by the scale ids of the instruction descriptor (0 or 2).
+// kind::mxf8f6f4 does the same for e4m3 operands: 128 values a 128-byte row, K = 32 an instruction, one
+// of the four bytes (0 to 3).
 #pragma once
 
 #include "tcgen05.cuh"

@@ -283,6 +283,26 @@ def test_output_on_any_element():
     assert torch.equal(moe.moe_mx8_product(c, s, c, s, out=out), want)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("sizes", [[3, 0, 5], [200, 180, 1]])
+@pytest.mark.parametrize("N", [8, 72, 264, 1000])
+def test_output_inside_another_tensor(dtype, sizes, N):
+    """Rows of whole 16 bytes that are no whole lines, at an address that 32 does not divide: the same
+    values as in a tensor of its own, and nothing written before, behind or past the groups."""
+    K, E, rows = 160, len(sizes), sum(sizes) + 2
+    a = moe.moe_mx8_quantize(rows_of(rows, K, dtype, N).to(DEV))
+    b = moe.moe_mx8_quantize(rows_of(E * N, K, dtype, N + 1).to(DEV).view(E, N, K))
+    off, _ = offsets_of(sizes)
+    want = moe.moe_mx8_product(*a, *b, offsets=off, dtype=dtype)
+    pad = 16 // want.element_size()
+    room = torch.full((rows * N + 3 * pad,), 42.0, dtype=dtype, device=DEV)
+    out = room[pad:pad + rows * N].view(rows, N)
+    assert out.data_ptr() % 32 == 16
+    moe.moe_mx8_product(*a, *b, offsets=off, out=out)
+    assert torch.equal(out[:-2], want[:-2])
+    assert (out[-2:] == 42).all() and (room[:pad] == 42).all() and (room[pad + rows * N:] == 42).all()
+
+
 # ----------------------------------------------------------------------------------- dispatch
 def routed(T, E, k, seed, bad=()):
     """Different experts for each token, as idx and the slots' rows in a stable order."""
