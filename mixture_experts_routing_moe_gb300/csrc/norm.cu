@@ -220,14 +220,15 @@ __device__ __forceinline__ Place place(int W, int64_t T) {
   p.ok = p.t < T;
   return p;
 }
-// The sum of v over a row's W warps, in a fixed order (every thread of the block calls it; `part` has
-// a float for each warp, whose last values every thread has read before another barrier).
+// The sum of v over a row's W warps, in a fixed order (every thread of the row calls it: a row has a barrier
+// of its own; `part` has a float for each warp, whose last values every thread of the row has read before
+// another barrier).
 __device__ __forceinline__ float row_sum(float v, int W, const Place& p, float* part) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   if (W == 1) return v;
   if (p.lane == 0) part[threadIdx.x >> 5] = v;
-  __syncthreads();
+  asm volatile("bar.sync %0, %1;" ::"r"(p.g + 1), "r"(32 * W) : "memory");
   v = 0.f;
   for (int i = 0; i < W; ++i) v += part[p.g * W + i];
   return v;
@@ -243,6 +244,15 @@ __device__ __forceinline__ float rsqrt_exact(float m) {
 // The sum of a unit's squares, as a tree.
 __device__ __forceinline__ f2 squares(const f2* v) {
   return add2(fma2(v[1], v[1], mul2(v[0], v[0])), fma2(v[3], v[3], mul2(v[2], v[2])));
+}
+// A mean (with eps) below 2^-100 may have squares that FP32 loses.  Such a row is summed and normalised
+// again times 2^100: the square of its smallest number is then 2^-98, the sum of 2^24 squares at most
+// 2^124.  Only calls with an eps below 2^-100 can meet one, and take kernels that look (LIFTS): the few
+// registers that it takes cost 6 % (16384 x 7168 bf16 with blocks), in f32 5 to 20 %.
+constexpr float kTiny = 0x1p-100f, kLift = 0x1p100f;
+__device__ __forceinline__ void lift_unit(f2* v) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = mul2(v[i], pack(kLift, kLift));
 }
 // The larger of m and two magnitudes; a NaN stays one.
 __device__ __forceinline__ float max_abs(float m, f2 v) {
@@ -333,11 +343,11 @@ __device__ __forceinline__ void load_rows(const NormArgs& a, int64_t t, int W, c
 }
 
 // Row groups walk the rows g, g + groups, ..., a row ahead with their loads where registers allow it;
-// the weight stays in registers.  THREADS: the most that a block has; BLOCKS of them an SM.
-template <typename T, typename TW, bool VEC, int U, int THREADS, int BLOCKS>
+// the weight stays in registers.  THREADS: the most that a block has; BLOCKS of them an SM.  LIFTS: kTiny.
+template <typename T, typename TW, bool VEC, bool LIFTS, int U, int THREADS, int BLOCKS>
 __global__ void __launch_bounds__(THREADS, BLOCKS)
     moe_rms_norm_kernel(const __grid_constant__ NormArgs a, int W, int64_t groups, int blocks) {
-  __shared__ float part[2][32];
+  __shared__ float part[LIFTS ? 3 : 2][32];
   constexpr bool AHEAD = U > 1 && sizeof(T) == 2 && THREADS <= 512;
   const int H = (int)a.H;
   const Place p = place(W, groups);
@@ -369,24 +379,37 @@ __global__ void __launch_bounds__(THREADS, BLOCKS)
         parts = add2(parts, squares(v));
       }
     }
-    const float ss = row_sum(sum2(parts), W, p, part[turn]);
+    float mean = row_sum(sum2(parts), W, p, part[turn]) / (float)H + a.eps;
     if (!ok) continue;
-    const float r = rsqrt_exact(ss / (float)H + a.eps);
-    if (a.rstd && p.w == 0 && p.lane == 0) a.rstd[t] = r;
+    const bool lifted = LIFTS && mean < kTiny;
+    if (lifted) {
+      parts = 0;
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        f2 v[4];
+        widen(q[j], v);
+        lift_unit(v);
+        parts = add2(parts, squares(v));
+      }
+      mean = row_sum(sum2(parts), W, p, part[2]) / (float)H + a.eps * kLift * kLift;
+    }
+    const float r = rsqrt_exact(mean);
+    if (a.rstd && p.w == 0 && p.lane == 0) a.rstd[t] = lifted ? r * kLift : r;
 #pragma unroll
     for (int j = 0; j < U; ++j) {
       f2 v[4];
       widen(q[j], v);
+      if (lifted) lift_unit(v);
       finish_unit<T, TW, VEC>(a, t, (j * W + p.w) * 32, p.lane, blocks, v, w[j], r);
     }
   }
 }
 
 // Rows that a block's registers do not hold: a block a row, which it reads twice.
-template <typename T, typename TW, bool VEC>
+template <typename T, typename TW, bool VEC, bool LIFTS>
 __global__ void __launch_bounds__(1024)
     moe_rms_norm_long(const __grid_constant__ NormArgs a, int blocks) {
-  __shared__ float part[32];
+  __shared__ float part[LIFTS ? 2 : 1][32];
   const Place p = place(32, a.T);
   const int H = (int)a.H, steps = (blocks * 4 + 1023) / 1024;
   const T* x = (const T*)a.x + p.t * a.ldx;
@@ -405,15 +428,27 @@ __global__ void __launch_bounds__(1024)
     widen(q, v);
     parts = add2(parts, squares(v));
   }
-  const float ss = row_sum(sum2(parts), 32, p, part);
-  const float r = rsqrt_exact(ss / (float)H + a.eps);
-  if (a.rstd && threadIdx.x == 0) a.rstd[p.t] = r;
+  // a lane reads what it wrote itself (the sum may lie where x or the residual was)
+  auto again = [&](int u0) { return sum ? load_unit<T, VEC>(sum, u0, p.lane, H) : value(u0); };
+  float mean = row_sum(sum2(parts), 32, p, part[0]) / (float)H + a.eps;
+  const bool lifted = LIFTS && mean < kTiny;
+  if (lifted) {
+    parts = 0;
+    for (int j = 0; j < steps; ++j) {
+      f2 v[4];
+      widen(again((j * 32 + p.w) * 32), v);
+      lift_unit(v);
+      parts = add2(parts, squares(v));
+    }
+    mean = row_sum(sum2(parts), 32, p, part[LIFTS]) / (float)H + a.eps * kLift * kLift;
+  }
+  const float r = rsqrt_exact(mean);
+  if (a.rstd && threadIdx.x == 0) a.rstd[p.t] = lifted ? r * kLift : r;
   for (int j = 0; j < steps; ++j) {
     const int u0 = (j * 32 + p.w) * 32;
-    // a lane reads what it wrote itself (the sum may lie where x or the residual was)
-    const Unit<T> q = sum ? load_unit<T, VEC>(sum, u0, p.lane, H) : value(u0);
     f2 v[4];
-    widen(q, v);
+    widen(again(u0), v);
+    if (lifted) lift_unit(v);
     finish_unit<T, TW, VEC>(a, p.t, u0, p.lane, blocks, v,
                             load_weight<TW, VEC>(a.weight, u0, p.lane, H), r);
   }
@@ -605,12 +640,12 @@ bool rows_aligned(const void* p, int64_t ld, size_t size) {
   return !p || (((uintptr_t)p & 15u) == 0 && (ld * (int64_t)size) % 16 == 0);
 }
 
-template <typename T, typename TW, bool VEC>
-cudaError_t norm_v(const NormArgs& a, cudaStream_t s) {
+template <typename T, typename TW, bool VEC, bool LIFTS>
+cudaError_t norm_l(const NormArgs& a, cudaStream_t s) {
   constexpr int U = kUnits<T>;
   const int64_t blocks = mx8::blocks_of(a.H), warps = (blocks + 7) / 8;  // warps at a unit a lane
   if (warps > 32 * U) {
-    moe_rms_norm_long<T, TW, VEC><<<(unsigned)a.T, 1024, 0, s>>>(a, (int)blocks);
+    moe_rms_norm_long<T, TW, VEC, LIFTS><<<(unsigned)a.T, 1024, 0, s>>>(a, (int)blocks);
     return cudaGetLastError();
   }
   // Few rows: a unit a lane, for latency.  Many: U, for bytes in flight with fewer threads.  (In bf16 with
@@ -618,14 +653,20 @@ cudaError_t norm_v(const NormArgs& a, cudaStream_t s) {
   // 4.1 / 4.6, 304 x 7168 7.0 / 5.3.)
   const bool few = warps <= 32 && a.T * warps <= 152 * 32;
   const int W = few ? (int)warps : (int)((warps + U - 1) / U), G = W >= 8 ? 1 : 8 / W;
-  const auto kern = few       ? moe_rms_norm_kernel<T, TW, VEC, 1, 1024, 1>
-                    : W <= 8  ? moe_rms_norm_kernel<T, TW, VEC, U, 256, kNormBlocks<T>>
-                    : W <= 16 ? moe_rms_norm_kernel<T, TW, VEC, U, 512, 1>
-                              : moe_rms_norm_kernel<T, TW, VEC, U, 1024, 1>;
+  const auto kern = few       ? moe_rms_norm_kernel<T, TW, VEC, LIFTS, 1, 1024, 1>
+                    : W <= 8  ? moe_rms_norm_kernel<T, TW, VEC, LIFTS, U, 256, kNormBlocks<T>>
+                    : W <= 16 ? moe_rms_norm_kernel<T, TW, VEC, LIFTS, U, 512, 1>
+                              : moe_rms_norm_kernel<T, TW, VEC, LIFTS, U, 1024, 1>;
   const int64_t all = (a.T + G - 1) / G, most = W <= 8 ? 152 * kNormBlocks<T> : 152;
   const int64_t grid = few || all < most ? all : most;
   kern<<<(unsigned)grid, 32 * W * G, 0, s>>>(a, W, grid * G, (int)blocks);
   return cudaGetLastError();
+}
+template <typename T, typename TW, bool VEC>
+cudaError_t norm_v(const NormArgs& a, cudaStream_t s) {
+  if constexpr (Dt<T>::code != MOE_F16)  // (FP32 holds f16's squares)
+    if (a.eps < kTiny) return norm_l<T, TW, VEC, true>(a, s);
+  return norm_l<T, TW, VEC, false>(a, s);
 }
 template <typename T>
 cudaError_t norm_t(const NormArgs& a, cudaStream_t s) {
