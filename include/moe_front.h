@@ -26,7 +26,8 @@ extern "C" {
  *   rstd [T] float: (mean(s^2) + eps)^(-1/2), for moe_rms_norm_backward.
  * The mean is FP32: squares past its range give rstd 0.  Rows whose squares are below it are normalised
  * like others (with an rstd of infinity where it is past FP32's range: root mean squares below 2^-128).
- * A NaN or an infinity stays in its row.
+ * A NaN or an infinity stays in its row.  Weights are numbers: an infinite one makes its column of y
+ * infinite or NaN, and its blocks 255.
  * sum may be x or residual itself, y may be x, with the same row stride; other overlaps are not
  * allowed.
  * Limits: 0 <= T < 2^31 - 1024, 1 <= H < 2^24, H <= ld < 2^31 (else MOE_ERR_SHAPE); eps finite and

@@ -272,7 +272,8 @@ __device__ __forceinline__ void finish_unit(const NormArgs& a, int64_t t, int u0
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     // h r w with one rounding (h r and what its rounding left, both times w): a value next to a border
-    // between codes is moved by a step of the code
+    // between codes is moved by a step of the code.  (An infinite w may meet a remainder of zero: NaN.
+    // To look for one cost 7 %, 16384 x 7168 bf16 with blocks.)
     const f2 left = fma2(h[i], r2, mul2(h[i], minus));
     v[i] = fma2(mul2(h[i], r2), v[i], mul2(left, v[i]));
   }
