@@ -150,7 +150,7 @@ struct Params {
   int scales_align;          // see load_scales()
   int E, N, KB, NT;          // N: rows of one expert's B (gate/up: I); KB: slices
   void* out;
-  int store;                 // bytes of a store of FP32 rows: 32 or 16
+  int store;                 // kRows: bytes of a store, 32 or 16
   uint8_t* codes;            // gate/up: rows of N values in blocks
   uint8_t* scales;
   unsigned* status;
@@ -190,28 +190,30 @@ __device__ __forceinline__ void st_v8(void* p, const uint4& a, const uint4& b) {
                "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
                : "memory");
 }
-// 32 accumulator columns of an FP32 row, 32 bytes (a whole sector; 16 cost twice the requests) or 16 at a
-// time; the last columns of a row of a ragged N one by one.  (Whole lines by store_lines, which rows of 16
-// bits take, made one wave of short tiles slower, 3001 x 1000 with K = 1376: 14.5 -> 16.5 us in replays
-// back to back; 8192^3 357 -> 354.)
-__device__ __forceinline__ void store_row(float* row, const float* v, int col0, int N, int store) {
+// 32 accumulator columns of a row, 32 bytes (a whole sector; 16 cost twice the requests) or 16 at a time;
+// the last columns of a row of a ragged N one by one.  (FP32 rows by whole lines, as store_lines writes
+// them, made one wave of short tiles slower, 3001 x 1000 with K = 1376: 14.5 -> 16.5 us in replays back to
+// back; 8192^3 357 -> 354.)
+template <typename T>
+__device__ __forceinline__ void store_row(T* row, const float* v, int col0, int N, int store) {
+  constexpr int W = 16 / sizeof(T);
   if (col0 + 32 <= N) {
 #pragma unroll
-    for (int i = 0; i < 8; i += 2) {
-      Vec16<float> q, r;
-      q.from_float(v + 4 * i);
-      r.from_float(v + 4 * (i + 1));
+    for (int i = 0; i < 32 / W; i += 2) {
+      Vec16<T> q, r;
+      q.from_float(v + i * W);
+      r.from_float(v + (i + 1) * W);
       if (store == 32) {
-        st_v8(row + col0 + 4 * i, q.u, r.u);
+        st_v8(row + col0 + i * W, q.u, r.u);
       } else {
-        st_v4(row + col0 + 4 * i, q.u);
-        st_v4(row + col0 + 4 * (i + 1), r.u);
+        st_v4(row + col0 + i * W, q.u);
+        st_v4(row + col0 + (i + 1) * W, r.u);
       }
     }
   } else {
 #pragma unroll
     for (int i = 0; i < 32; ++i)
-      if (col0 + i < N) row[col0 + i] = v[i];
+      if (col0 + i < N) row[col0 + i] = Dt<T>::from_f(v[i]);
   }
 }
 // V pieces of 16 bytes of each of a warp's 32 rows (a lane holds its row's; out: row 0, the warp's first
@@ -279,8 +281,9 @@ __device__ __forceinline__ void store_turned(T* out, int64_t pitch, const uint32
   }
 }
 
-// What the epilogue writes: the blocks of a; rows that are 16-byte aligned; other rows.
-enum Kind { kGateUp, kRows, kTurned };
+// What the epilogue writes: the blocks of a; rows that are 16-byte aligned, by lanes or (16 bits) by whole
+// lines; other rows.
+enum Kind { kGateUp, kRows, kLines, kTurned };
 
 template <typename F, int CG, int BN, int KIND, typename T>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -633,9 +636,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           scale |= F::block(a, top, codes + c * PIECES) << (8 * c);
         }
-        store_lines(p.codes + row0 * cp + (int64_t)blk0 * F::CODE_BYTES, cp, codes, rows,
-                    (blocks - blk0) * F::CODE_BYTES, smem_u32(my_turn), lane);
+        // (Single CTAs' lanes store their own rows: through shared memory the experts of 256 tokens, k = 8,
+        // 128 experts took 57.8 us in place of 56.5 in 4 bits, those of 2000 118 and 115.)
+        if (CG == 2)
+          store_lines(p.codes + row0 * cp + (int64_t)blk0 * F::CODE_BYTES, cp, codes, rows,
+                      (blocks - blk0) * F::CODE_BYTES, smem_u32(my_turn), lane);
         if (lane < rows && blk0 < blocks) {
+          if (CG == 1) {
+            uint8_t* at = p.codes + (row0 + lane) * cp + (int64_t)blk0 * F::CODE_BYTES;
+#pragma unroll
+            for (int c = 0; c < BLOCKS; ++c) {
+              if (blk0 + c >= blocks) continue;
+              if (PIECES == 2) st_v8(at + c * 32, codes[c * PIECES], codes[c * PIECES + PIECES - 1]);
+              else st_v4(at + c * 16, codes[c]);
+            }
+          }
           // pitches are multiples of four, and a row's bytes past its last block are zero
           uint8_t* sc = p.scales + (row0 + lane) * sp + blk0;
           if (BLOCKS == 2 && blk0 + 1 < blocks) *reinterpret_cast<uint16_t*>(sc) = (uint16_t)scale;
@@ -647,11 +662,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else if (KIND == kTurned) {
         const int col0 = x.n * BN + h * HC;
         store_turned((T*)p.out + row0 * p.N + col0, p.N, acc, rows, p.N - col0, my_turn, lane);
-      } else if constexpr (sizeof(T) == 4) {
+      } else if constexpr (KIND == kRows) {
         if (lane < rows) {
 #pragma unroll
           for (int c = 0; c < HC / 32; ++c)
-            store_row((float*)p.out + (row0 + lane) * p.N, reinterpret_cast<const float*>(acc[c]),
+            store_row((T*)p.out + (row0 + lane) * p.N, reinterpret_cast<const float*>(acc[c]),
                       x.n * BN + h * HC + c * 32, p.N, p.store);
         }
       } else {
@@ -745,14 +760,29 @@ int tile_columns(int64_t rows, int E, int64_t columns, int sms) {
   return experts * ((columns + kWide - 1) / kWide) <= 3 * (int64_t)sms ? kHalf : kWide;
 }
 
+// Whether wide tiles' rows of 16 bits go by whole lines: pairs' do, and single CTAs' when the output is at
+// least three full tiles an SM, as the way through shared memory costs a tile some 1500 cycles that only the
+// next tile's slices, which come earlier, make up for.  By lanes / by lines, in 4 bits: 64 rows in 16 groups,
+// N = 768, K = 2048 7.0 / 7.9 us; 5000 in 32, N = 2048, K = 512 14.9 / 16.0; 256 tokens' experts 56.5 / 58.8,
+// 2000 tokens' 114.8 / 112.9; 20000 in 128, N = 2048, K = 768 39.7 / 37.4.  In 8 bits, the same rows: 8.8 /
+// 9.0; 15.3 / 16.2; layers 90.3 / 90.9, 183.1 / 181.8; 62.5 / 61.4.  Pairs: 3001 rows in 7, N = 1000,
+// K = 1376 11.6 / 10.3 and 12.2 / 10.9; 10000 in 32, N = 2048, K = 512 29.1 / 25.6 in 8 bits; 4096 in one,
+// N = 2048, K = 512 10.5 / 10.7 and 11.5 / 11.8.
+bool by_lines(int64_t rows, int E, int64_t N, int sms) {
+  return use_pairs(rows, E) || rows * N >= (int64_t)3 * BM * kWide * sms;
+}
+
+// KIND of a wide tile; narrow ones and pairs have only one of kRows and kLines.
 template <typename F, int KIND, typename T>
 cudaError_t launch(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& b2,
                    const Params& p, int bn, int sms, cudaStream_t s) {
+  constexpr int SMALL = KIND == kLines ? kRows : KIND;
+  constexpr int PAIR = KIND == kRows && sizeof(T) == 2 ? kLines : KIND;
   if constexpr (F::CHUNKS == 1) {
-    if (bn == kNarrow) return launch_cg<F, 1, kNarrow, KIND, T>(a, b, b2, p, sms, s);
-    if (bn == kHalf) return launch_cg<F, 1, kHalf, KIND, T>(a, b, b2, p, sms, s);
+    if (bn == kNarrow) return launch_cg<F, 1, kNarrow, SMALL, T>(a, b, b2, p, sms, s);
+    if (bn == kHalf) return launch_cg<F, 1, kHalf, SMALL, T>(a, b, b2, p, sms, s);
   }
-  return use_pairs(p.rows, p.E) ? launch_cg<F, 2, kWide, KIND, T>(a, b, b2, p, sms, s)
+  return use_pairs(p.rows, p.E) ? launch_cg<F, 2, kWide, PAIR, T>(a, b, b2, p, sms, s)
                                 : launch_cg<F, 1, kWide, KIND, T>(a, b, b2, p, sms, s);
 }
 
@@ -797,8 +827,10 @@ cudaError_t launch_product(MxRows a, int64_t rows, MxRows b, const int32_t* offs
   const uintptr_t both = (uintptr_t)out | (uintptr_t)N * sizeof(T);
   p.store = both % 32 ? 16 : 32;
   p.zero_status = zero_status;
-  return both % 16 ? launch<F, kTurned, T>(ma, mb, mb, p, bn, sms, s)
-                   : launch<F, kRows, T>(ma, mb, mb, p, bn, sms, s);
+  if (both % 16) return launch<F, kTurned, T>(ma, mb, mb, p, bn, sms, s);
+  if constexpr (sizeof(T) == 2)
+    if (by_lines(rows, E, N, sms)) return launch<F, kLines, T>(ma, mb, mb, p, bn, sms, s);
+  return launch<F, kRows, T>(ma, mb, mb, p, bn, sms, s);
 }
 
 template <typename F>
