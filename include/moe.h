@@ -16,7 +16,8 @@
  *  - Work is enqueued on the caller's stream `stream` (a cudaStream_t; NULL = legacy default
  *    stream).  Every call returns as soon as the work is enqueued.
  *  - Every argument is checked on the host before anything is enqueued; a rejected call enqueues
- *    nothing and returns the status below.  T = 0 is valid and enqueues nothing.
+ *    nothing and returns the status below.  T = 0 is valid and enqueues nothing:
+ *    outputs that do not shrink with T (a dispatch's offsets) stay as they were.
  *  - MOE_ERR_CUDA means a CUDA launch or query failed (including "no device").
  *  - Kernels never trap.  Conditions only the device can see (an expert index >= E handed to
  *    moe_dispatch; a pipeline wait in the tensor-core kernels that exceeded its time limit) are

@@ -171,6 +171,12 @@ def _new_ws(need: int, device, stream):
     return _new(max(need, 256), torch.uint8, device, stream)
 
 
+def _no_rows(offsets, stream):
+    """The offsets of a call without tokens, for which the library enqueues nothing."""
+    with torch.cuda.stream(stream):
+        offsets.zero_()
+
+
 def _cuda(*ts):
     for t in ts:
         if t is not None and (not t.is_cuda or not t.is_contiguous()):
@@ -277,6 +283,8 @@ def moe_dispatch(x, idx, E: int, x_d=None, offsets=None, token_of_row=None, row_
     _check(lib().moe_dispatch(_ptr(x), _code(x), T, H, _ptr(idx), E, k, _ptr(x_d), _ptr(offsets),
                               _ptr(token_of_row), _ptr(row_of_slot), _ptr(ws), ws.numel(),
                               _stream(stream)), "moe_dispatch")
+    if T == 0:
+        _no_rows(offsets, stream)
     return {"x_d": x_d, "offsets": offsets, "token_of_row": token_of_row,
             "row_of_slot": row_of_slot, "ws": ws}
 

@@ -159,6 +159,8 @@ def moe_mx8_dispatch(codes, scales, idx, E: int, H: int, ws=None, stream=None):
     B._check(lib().moe_mx8_dispatch(codes.data_ptr(), scales.data_ptr(), T, H, idx.data_ptr(), E, k,
                                     *(t.data_ptr() for t in out.values()), ws.data_ptr(),
                                     ws.numel(), _stream(stream)), where)
+    if T == 0:
+        B._no_rows(out["offsets"], stream)
     return {**out, "ws": ws}
 
 
