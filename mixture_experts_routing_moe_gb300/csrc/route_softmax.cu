@@ -531,10 +531,16 @@ cudaError_t launch_route_softmax_grouped(const void* logits, int ldt, const floa
   a.idx = idx;
   a.w = w;
   // Experts of a lane: the fewest that make a group a power of two of whole lanes, as the groups'
-  // scores then take a few shuffles instead of a walk through shared memory; else the fewest.
+  // scores then take a few shuffles instead of a walk through shared memory, if that takes no more than
+  // twice the registers; else the fewest.  Few lanes with many experts each are slower than the walk, as
+  // the fast choice runs out of candidates (16384 rows, k = 8, bias, lanes / walk: 248 experts in 8 groups,
+  // 31 a lane for 8, 112 / 36 us; 72 in 8, 9 for 3, 63 / 25; 60 in one, 15 for 2, 59 / 16).  At twice the
+  // registers neither is better everywhere (56 in 8 groups, k = 6 27.4 / 22.6 us, one row 3.2 / 3.8; 500 in
+  // 20 75.8 / 78.6, one row 5.2 / 6.3).
   const int gs = E / G, least = (E + 31) / 32;
+  auto registers = [](int n) { return n <= 4 ? 4 : n <= 8 ? 8 : n <= 16 ? 16 : 32; };  // see launch_t()
   a.per = least;
-  for (int per = least; per <= 32 && per <= gs; ++per)
+  for (int per = least; per <= 32 && per <= gs && registers(per) <= 2 * registers(least); ++per)
     if (gs % per == 0 && ((gs / per) & (gs / per - 1)) == 0) {
       a.per = per;
       a.lanes = gs / per;
