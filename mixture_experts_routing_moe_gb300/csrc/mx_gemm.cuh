@@ -24,19 +24,19 @@
 //               accumulator.)
 // Waits are bounded; on expiry the status word records the timeout and every role leaves.
 //
-// What bounds it, in 4 bits: at 8192^3 it runs in 159-161 us, 6.9 PFLOP/s, the tensor pipe 80 %
-// active (in K = 64 steps); without the scales (skipped, to time the rest) it takes 154, so the
-// tensor pipe and its operands' way through shared memory are what is left.  Deep K keeps that
+// What bounds it, in 4 bits: at 8192^3 it runs in 152-157 us, 7.0-7.2 PFLOP/s, the tensor pipe 83 %
+// active (in K = 64 steps).  Before the stores of 16-bit rows went by whole lines (store_lines) it took
+// 159-161, and without the scales (skipped, to time the rest) 154, so the tensor pipe and its operands'
+// way through shared memory are what is left.  Deep K kept that
 // (K = 14336: 6.6); at K = 2048 a tile is 8 slices, and the 1400 cycles in which the accumulator is
-// emptied while no MMA can run are a fifth of it (3.4 with groups that fill 78 % of their tiles).  (These
-// before the stores of 16-bit rows went by whole lines: see store_lines; 155-157 since.)  On
+// emptied while no MMA can run are a fifth of it (3.4 with groups that fill 78 % of their tiles).  On
 // the way there, at 8192^3: scales four bytes at a time per slice, 671 us (the L1 tag stage); pairs
 // with a full release at cluster scope for each slice, 467 (it waits for the warp's loads in flight),
 // releasing shared memory only, 250; 16-byte chunk stores, 238; whole-warp issue loops with an
 // elected lane, 195; two slices behind one proxy fence, 184; scale rows located once a tile and
 // loaded 32 bytes at a time, 163.
 // In 8 bits a slice's MMAs take twice as long (512 cycles), so the rest hides better: 8192^3 in
-// 313-321 us by itself, 3.5 PFLOP/s, the tensor pipe 87 % active; under load, at the 1.4 GHz that its
+// 310-321 us by itself, 3.5 PFLOP/s, the tensor pipe 87 % active; under load, at the 1.4 GHz that its
 // power leaves, 364-373.  A tile of 64 slices took 36300 cycles, of which 32800 are MMAs; the emptying
 // is some 1000, and the next tile's first slices came late behind the stores (store_lines).  Raw
 // scales that came by TMA instead of through the scale warps' loads made no difference there (363 and
@@ -65,7 +65,7 @@ constexpr int kTurnBytes = 1024;  // an epilogue warp's: 32 rows x 32 bytes
 constexpr uint32_t kTmemCols = 512, kScaleCol = 256;
 
 // What the two formats differ in.  A 128-byte slice of a row has CHUNKS x 128 values (a chunk holds the
-// scales of 128 rows and four blocks); WORDS 32-bit words of a row's scales.
+// scales of 128 rows and four blocks).
 struct Fmt4 {
   static constexpr int CHUNKS = 2, CODE_BYTES = 16;  // CODE_BYTES: of a block
   static __host__ __device__ int64_t code_pitch(int64_t K) { return mx4::code_pitch(K); }
@@ -192,8 +192,8 @@ __device__ __forceinline__ void st_v8(void* p, const uint4& a, const uint4& b) {
 }
 // 32 accumulator columns of a row, 32 bytes (a whole sector; 16 cost twice the requests) or 16 at a time;
 // the last columns of a row of a ragged N one by one.  (FP32 rows by whole lines, as store_lines writes
-// them, made one wave of short tiles slower, 3001 x 1000 with K = 1376: 14.5 -> 16.5 us in replays back to
-// back; 8192^3 357 -> 354.)
+// them, made one wave of short tiles slower, 3001 x 1000 with K = 1376 in 8 bits: 11.7 -> 13.3 us; 8192 x
+// 8192 would gain, K = 2048 122 -> 109, K = 8192 334 -> 329.)
 template <typename T>
 __device__ __forceinline__ void store_row(T* row, const float* v, int col0, int N, int store) {
   constexpr int W = 16 / sizeof(T);
