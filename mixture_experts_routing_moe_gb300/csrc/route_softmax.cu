@@ -21,12 +21,12 @@
 // What bounds it is the issue of integer and FP32 instructions: some 1050 a row of 256 experts with
 // eight groups and a bias, 18 us for 16384 rows, and the last rows that float64 decides (28 us
 // together; 65536 rows 79).  These are of logits of spread 2, where 32 of the 16384 rows go there; a zero
-// bias and spreads of 6 and 8 send 8 and 26 % (43 and 79 us), and one bias of -inf all (200).  With k rounds of a warp maximum, each of which sent the lane that gave
-// it looking for its next best, a row took 1800 (57 us, 25 of them 32 rows in float64).  So the
-// choice is made among few: the rounds run over the lanes' best alone, which bounds the last choice
-// from below, the experts above that bound (mostly a dozen) go to shared memory, one for each lane,
-// and each counts those before it.  The float64 form keeps a lane's scores in registers, so that
-// its exponentials overlap, and ranks them as 64-bit integers.
+// bias and spreads of 6 and 8 send 8 and 26 % (43 and 79 us), and one bias of -inf all (200).  With k
+// rounds of a warp maximum, each of which sent the lane that gave it looking for its next best, a row
+// took 1800 (57 us, 25 of them 32 rows in float64).  So the choice is made among few: the rounds run over
+// the lanes' best alone, which bounds the last choice from below, the experts above that bound (mostly a
+// dozen) go to shared memory, one for each lane, and each counts those before it.  The float64 form keeps
+// a lane's scores in registers, so that its exponentials overlap, and ranks them as 64-bit integers.
 #include "common.cuh"
 #include "launch.h"
 
